@@ -28,6 +28,10 @@ SVDQ_F32 = 1
 QFMT_INT4 = 0
 QFMT_FP6 = 1
 GROUP = 64
+FP8_BLOCK = 128
+FP8_MOE_MAX_TOKENS = 64
+FP8_MOE_MAX_EXPERTS = 256
+FP8_MOE_MAX_TOP_K = 16
 
 _vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
 
@@ -59,6 +63,13 @@ SIGNATURES = {
     "w4a16_weight_bytes": (_sz, [_i, _i]),
     "w4a16_prepare_weights": (_i, [_vp, _i, _i, _i, _vp]),
     "w4a16_linear": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
+    "svdq_fp8_prepare_weights": (_i, [_vp, _i, _i, _vp, _vp]),
+    "svdq_fp8_quantize_act": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
+    "svdq_fp8_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp]),
+    "svdq_fp8_workspace_bytes": (_sz, [_i, _i]),
+    "svdq_fp8_linear": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp, _i, _vp]),
+    "svdq_fp8_moe_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "svdq_fp8_moe_layer": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp, _vp]),
     "svdq_debug_group_partials": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
     "w8a8_debug_acc": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp]),
     "svdq_debug_set_arch_override": (_i, [C.c_char_p]),
@@ -280,6 +291,23 @@ def w4a16_prepare_weights(W_bits, group=GROUP):
     return out[:nbytes]
 
 
+def fp8_blocks(n) -> int:
+    """Blocks of 128 that cover n features."""
+    return -(-n // FP8_BLOCK)
+
+
+def svdq_fp8_prepare_weights(W_bits):
+    """Block-scaled FP8 weight of a bf16 weight W [K, N]: E4M3 codes (uint8,
+    [N, K]) and scales (float32, [ceil(N/128), ceil(K/128)])."""
+    W_bits = np.ascontiguousarray(W_bits, dtype=np.uint16)
+    K, N = W_bits.shape
+    qw = np.empty((N, K), np.uint8)
+    sw = np.empty((fp8_blocks(N), fp8_blocks(K)), np.float32)
+    st = lib().svdq_fp8_prepare_weights(_np_ptr(W_bits, np.uint16), K, N, qw.ctypes.data, sw.ctypes.data)
+    _check("svdq_fp8_prepare_weights", st)
+    return qw, sw
+
+
 # ---------------------------------------------------------------- device --
 #
 # Every wrapper checks, before calling into the library, that each tensor
@@ -435,6 +463,97 @@ def w4a16_linear(X, packed, bias, Y, N, group=GROUP, stream=None):
                             _dev_ptr(bias, 2, N * 2, "bias", dev), M, N, K, group,
                             _dev_ptr(Y, 2, M * N * 2, "Y", dev), _stream(stream))
     _check("w4a16_linear", st)
+
+
+def svdq_fp8_quantize_act(X, qx, sx, stream=None):
+    """E4M3 codes qx [M, K] (1-byte elements) and scales sx [ceil(K/128), M] of X [M, K] bf16."""
+    M, K = _shape2(X, "X")
+    dev = _current_device()
+    st = lib().svdq_fp8_quantize_act(_dev_ptr(X, 2, M * K * 2, "X", dev), M, K, _dev_ptr(qx, 1, M * K, "qx", dev),
+                                     _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev), _stream(stream))
+    _check("svdq_fp8_quantize_act", st)
+
+
+def _fp8_weight(qw, sw, K, dev):
+    N, Kw = _shape2(qw, "qw")
+    if Kw != K:
+        raise ValueError(f"qw has {Kw} columns, X has K = {K}")
+    return N, _dev_ptr(qw, 1, N * K, "qw", dev), _dev_ptr(sw, 4, fp8_blocks(N) * fp8_blocks(K) * 4, "sw", dev)
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def svdq_fp8_gemm(qx, sx, qw, sw, bias, Y, stream=None):
+    """Y [M, N] (bf16 or fp32, by its element size) of quantized activations
+    qx [M, K], sx and the block-scaled weight qw [N, K], sw."""
+    M, K = _shape2(qx, "qx")
+    dev = _current_device()
+    N, qwp, swp = _fp8_weight(qw, sw, K, dev)
+    wide = Y.element_size()
+    st = lib().svdq_fp8_gemm(_dev_ptr(qx, 1, M * K, "qx", dev), _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev),
+                             qwp, swp, _dev_ptr(bias, 2, N * 2, "bias", dev), M, N, K,
+                             _dev_ptr(Y, 4 if wide == 4 else 2, M * N * wide, "Y", dev),
+                             SVDQ_F32 if wide == 4 else SVDQ_BF16, _stream(stream))
+    _check("svdq_fp8_gemm", st)
+
+
+def svdq_fp8_workspace_bytes(M, K) -> int:
+    return int(lib().svdq_fp8_workspace_bytes(M, K))
+
+
+def svdq_fp8_linear(X, qw, sw, bias, workspace, Y, stream=None):
+    """Y [M, N] (bf16 or fp32, by its element size) = X [M, K] bf16 quantized
+    on the way, times the block-scaled weight qw [N, K], sw, plus bias."""
+    M, K = _shape2(X, "X")
+    dev = _current_device()
+    N, qwp, swp = _fp8_weight(qw, sw, K, dev)
+    wide = Y.element_size()
+    ws_need = svdq_fp8_workspace_bytes(M, K)
+    st = lib().svdq_fp8_linear(_dev_ptr(X, 2, M * K * 2, "X", dev), qwp, swp, _dev_ptr(bias, 2, N * 2, "bias", dev),
+                               M, N, K, _dev_ptr(workspace, None, ws_need, "workspace", dev), _nbytes(workspace),
+                               _dev_ptr(Y, 4 if wide == 4 else 2, M * N * wide, "Y", dev),
+                               SVDQ_F32 if wide == 4 else SVDQ_BF16, _stream(stream))
+    _check("svdq_fp8_linear", st)
+
+
+def svdq_fp8_moe_workspace_bytes(T, I, E, top_k) -> int:  # noqa: E741
+    return int(lib().svdq_fp8_moe_workspace_bytes(T, I, E, top_k))
+
+
+def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=None, renormalize=True, stream=None):
+    """Mixture-of-experts layer of a few tokens: Y [T, H] bf16 from X [T, H],
+    the router wr [E, H] (bf16) and the experts' block-scaled FP8 weights
+    w13 [E, 2, I, H], s13 and w2 [E, H, I], s2. idx [T, top_k] int32 and
+    gate [T, top_k] fp32 take the choices and their weights; each may be None
+    (top_k is given then, if both are)."""
+    T, H = _shape2(X, "X")
+    E, Hr = _shape2(wr, "wr")
+    if w13 is None or w13.dim() != 4 or w2 is None or w2.dim() != 3:
+        raise TypeError("w13 must be a 4-D and w2 a 3-D tensor")
+    I = int(w13.shape[2])  # noqa: E741
+    if Hr != H or tuple(w13.shape) != (E, 2, I, H) or tuple(w2.shape) != (E, H, I):
+        raise ValueError(f"X [{T}, {H}], wr [{E}, {Hr}], w13 {list(w13.shape)} and w2 {list(w2.shape)} do not fit")
+    for name, t in (("idx", idx), ("gate", gate)):
+        if t is not None:
+            rows, k = _shape2(t, name)
+            top_k = k if top_k is None else top_k
+            if (rows, k) != (T, top_k):
+                raise ValueError(f"{name} is [{rows}, {k}], the call writes [{T}, {top_k}]")
+    if top_k is None:
+        raise ValueError("top_k is needed where neither idx nor gate is given")
+    dev = _current_device()
+    gi, gh = fp8_blocks(I), fp8_blocks(H)
+    need = svdq_fp8_moe_workspace_bytes(T, I, E, top_k)
+    st = lib().svdq_fp8_moe_layer(
+        _dev_ptr(X, 2, T * H * 2, "X", dev), _dev_ptr(wr, 2, E * H * 2, "wr", dev),
+        _dev_ptr(w13, 1, E * 2 * I * H, "w13", dev), _dev_ptr(s13, 4, E * 2 * gi * gh * 4, "s13", dev),
+        _dev_ptr(w2, 1, E * H * I, "w2", dev), _dev_ptr(s2, 4, E * gh * gi * 4, "s2", dev), T, H, I, E, top_k,
+        1 if renormalize else 0, _dev_ptr(idx, 4, T * top_k * 4, "idx", dev),
+        _dev_ptr(gate, 4, T * top_k * 4, "gate", dev), _dev_ptr(workspace, None, need, "workspace", dev),
+        _nbytes(workspace), _dev_ptr(Y, 2, T * H * 2, "Y", dev), _stream(stream))
+    _check("svdq_fp8_moe_layer", st)
 
 
 def svdq_debug_group_partials(qx, qw, P, M, N, K, group=GROUP, qfmt=QFMT_INT4, stream=None):

@@ -83,6 +83,19 @@ svdq_status check_w4a4_shape(int M, int K, int rank, int group) {
     return SVDQ_OK;
 }
 
+// Block-scaled FP8: a tile's rows are addressed with 32-bit offsets (256 rows
+// of K bytes).
+constexpr int kFp8MaxK = 1 << 22;
+
+svdq_status check_fp8_linear_shape(int M, int N, int K, int y_dtype) {
+    if (M < 0 || N <= 0 || K <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (K % 16 || N % 8 || K >= kFp8MaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (y_dtype != SVDQ_BF16 && y_dtype != SVDQ_F32) return SVDQ_ERR_INVALID_ARGUMENT;
+    // tiles (64 x 64 at the least) are numbered in one grid dimension
+    if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) >= ((int64_t)1 << 31)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    return SVDQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -203,6 +216,13 @@ svdq_status svdq_mx_prepare_residual(const uint16_t *W, int K, int N, const floa
     for (int k = 0; k < K; ++k)
         if (!std::isfinite(smooth[k]) || !(smooth[k] > 0.0f)) return SVDQ_ERR_NUMERICAL;
     return svdq::mx_prepare_residual_impl(W, K, N, smooth, l1t, l2t, rank, qw, uw);
+}
+
+svdq_status svdq_fp8_prepare_weights(const uint16_t *W, int K, int N, uint8_t *qw, float *sw) {
+    if (!W || !qw || !sw || K <= 0 || N <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (K % 16 || N % 8) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (!svdq::all_finite_bf16(W, (int64_t)K * N)) return SVDQ_ERR_NUMERICAL;
+    return svdq::fp8_prepare_impl(W, K, N, qw, sw);
 }
 
 // ---------------------------------------------------------------- device ---
@@ -451,6 +471,82 @@ svdq_status svdq_mx_linear(const uint8_t *qx, const uint8_t *ux, const uint16_t 
     if (M == 0) return SVDQ_OK;
     return launched(svdq::launch_mx_linear(qx, ux, rank ? T : nullptr, qw, uw, rank ? l2t : nullptr, bias, M, N,
                                            K, rank, Y, y_dtype == SVDQ_F32, (hipStream_t)stream));
+}
+
+svdq_status svdq_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, void *stream) {
+    if (M < 0 || K <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (K % 16 || K >= kFp8MaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (M > 0 && (!X || !qx || !sx)) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(X) || !aligned16(qx) || !aligned16(sx)) return SVDQ_ERR_MISALIGNED;
+    const svdq_status st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (M == 0) return SVDQ_OK;
+    return launched(svdq::launch_fp8_quantize_act(X, M, K, qx, sx, (hipStream_t)stream));
+}
+
+svdq_status svdq_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
+                          const uint16_t *bias, int M, int N, int K, void *Y, int y_dtype, void *stream) {
+    svdq_status st = check_fp8_linear_shape(M, N, K, y_dtype);
+    if (st != SVDQ_OK) return st;
+    if (!qw || !sw || (M > 0 && (!qx || !sx || !Y))) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(qx) || !aligned16(sx) || !aligned16(qw) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (M == 0) return SVDQ_OK;
+    return launched(svdq::launch_fp8_gemm(qx, sx, qw, sw, bias, M, N, K, Y, y_dtype == SVDQ_F32,
+                                          (hipStream_t)stream));
+}
+
+size_t svdq_fp8_workspace_bytes(int M, int K) {
+    if (M < 0 || K <= 0 || K % 16) return 0;
+    return svdq::fp8_workspace_scales(M, K) + (size_t)svdq::fp8_blocks(K) * (size_t)M * sizeof(float);
+}
+
+svdq_status svdq_fp8_linear(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias, int M,
+                            int N, int K, void *workspace, size_t workspace_bytes, void *Y, int y_dtype,
+                            void *stream) {
+    svdq_status st = check_fp8_linear_shape(M, N, K, y_dtype);
+    if (st != SVDQ_OK) return st;
+    if (!qw || !sw || (M > 0 && (!X || !Y || !workspace))) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (M > 0 && workspace_bytes < svdq_fp8_workspace_bytes(M, K)) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(X) || !aligned16(qw) || !aligned16(sw) || !aligned16(bias) || !aligned16(workspace) ||
+        !aligned16(Y))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (M == 0) return SVDQ_OK;
+    uint8_t *qx = static_cast<uint8_t *>(workspace);
+    float *sx = reinterpret_cast<float *>(qx + svdq::fp8_workspace_scales(M, K));
+    st = launched(svdq::launch_fp8_quantize_act(X, M, K, qx, sx, (hipStream_t)stream));
+    if (st != SVDQ_OK) return st;
+    return launched(svdq::launch_fp8_gemm(qx, sx, qw, sw, bias, M, N, K, Y, y_dtype == SVDQ_F32,
+                                          (hipStream_t)stream));
+}
+
+size_t svdq_fp8_moe_workspace_bytes(int T, int I, int E, int top_k) {
+    if (T < 0 || I <= 0 || E <= 0 || top_k <= 0) return 0;
+    return svdq::fp8_moe_workspace_size(T, I, E, top_k);
+}
+
+svdq_status svdq_fp8_moe_layer(const uint16_t *X, const uint16_t *wr, const uint8_t *w13, const float *s13,
+                               const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k,
+                               int renormalize, int32_t *idx, float *gate, void *workspace, size_t workspace_bytes,
+                               uint16_t *Y, void *stream) {
+    if (T < 0 || H <= 0 || I <= 0 || E <= 0 || top_k <= 0 || top_k > E) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (H % 16 || I % 16 || H >= kFp8MaxK || I >= kFp8MaxK || T > SVDQ_FP8_MOE_MAX_TOKENS ||
+        E > SVDQ_FP8_MOE_MAX_EXPERTS || top_k > SVDQ_FP8_MOE_MAX_TOP_K)
+        return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (!wr || !w13 || !s13 || !w2 || !s2 || (T > 0 && (!X || !Y || !workspace))) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (T > 0 && workspace_bytes < svdq::fp8_moe_workspace_size(T, I, E, top_k)) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(X) || !aligned16(wr) || !aligned16(w13) || !aligned16(s13) || !aligned16(w2) || !aligned16(s2) ||
+        !aligned16(idx) || !aligned16(gate) || !aligned16(workspace) || !aligned16(Y))
+        return SVDQ_ERR_MISALIGNED;
+    const svdq_status st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0) return SVDQ_OK;
+    return launched(svdq::launch_fp8_moe(X, wr, w13, s13, w2, s2, T, H, I, E, top_k, renormalize != 0, idx, gate,
+                                         workspace, Y, (hipStream_t)stream));
 }
 
 svdq_status svdq_debug_group_partials(const uint8_t *qx, const uint8_t *qw,

@@ -1,0 +1,408 @@
+// The block-scaled FP8 linear: E4M3 codes with one fp32 scale per block of
+// 128 -- weights in 128 x 128 blocks, activations per token and 128 features.
+//
+//   A[m, g]  = max(max_{k in g} |X[m, k]|, 2^-100)
+//   sx[g, m] = fp32(A / 448),  qx = E4M3(fp32(X fp32(448 / A)))
+//   acc[m,n] = sum_g (sx[g, m] sw[n / 128, g]) sum_{k in g} qx[m, k] qw[n, k]
+//   Y        = acc + bias, rounded once to bf16 (nearest even) or kept fp32
+//
+// A group of 128 codes is summed by the matrix core (products of two E4M3
+// numbers are exact, fp32 accumulation); the scale of a group's partial sum
+// is one fp32 product per token and 128 output columns, and is applied with
+// one fp32 FMA per output element and group.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "fp8_common.h"
+#include "internal.h"
+
+namespace svdq {
+
+namespace {
+
+// ---- activation pass -------------------------------------------------------
+
+constexpr int kF8QThreads = 256;
+constexpr int kF8QRows = 16;    // tokens per block
+constexpr int kF8QGroups = 4;   // groups of 128 features per block
+
+// One block quantizes 16 tokens x 4 groups. 16 lanes hold one token's group,
+// 8 consecutive features (one 16-byte load) each; their largest magnitude is
+// found on the bf16 bit patterns (an integer maximum orders magnitudes, and
+// puts NaN above all, so a NaN reaches the scale). All four loads of a thread
+// are in flight together. The scales of the block go through LDS so that 16
+// tokens' scales of a group are stored as one 64-byte segment.
+__global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_t *__restrict__ X, int M, int K,
+                                                                   int G, uint8_t *__restrict__ qx,
+                                                                   float *__restrict__ sx) {
+    __shared__ float sxs[kF8QGroups][kF8QRows];
+    const int row = threadIdx.x >> 4, part = threadIdx.x & 15;
+    const int m = blockIdx.x * kF8QRows + row;
+    const int g0 = blockIdx.y * kF8QGroups;
+    const size_t base = (size_t)m * K;
+    u32x4 v[kF8QGroups];
+#pragma unroll
+    for (int i = 0; i < kF8QGroups; ++i) {
+        const int k = (g0 + i) * kF8Block + part * 8;
+        v[i] = u32x4{0u, 0u, 0u, 0u};
+        if (m < M && k < K) v[i] = *reinterpret_cast<const u32x4 *>(X + base + k);
+    }
+#pragma unroll
+    for (int i = 0; i < kF8QGroups; ++i) {
+        uint32_t mx = kF8TinyBits;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx = max(mx, max(v[i][j] & 0x7FFFu, (v[i][j] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
+        const float a = bf16_bits_to_f32(mx);
+        const float r = kF8Max / a;
+        if (part == 0) sxs[i][row] = a / kF8Max;
+        const int k = (g0 + i) * kF8Block + part * 8;
+        if (m < M && k < K) *reinterpret_cast<u32x2 *>(qx + base + k) = fp8_codes8(v[i], r);
+    }
+    __syncthreads();
+    const int g = threadIdx.x >> 4;
+    if (g < kF8QGroups && g0 + g < G) {
+        const int mm = blockIdx.x * kF8QRows + part;
+        if (mm < M) sx[(size_t)(g0 + g) * M + mm] = sxs[g][part];
+    }
+}
+
+// ---- the product, many tokens ----------------------------------------------
+
+constexpr uint32_t kF8Oob = 0x80000000u;
+
+typedef __attribute__((address_space(3))) void f8_lds_void;
+
+template <int BN, int BM>
+struct F8Stage {
+    uint8_t a[BN * kF8Block];
+    uint8_t b[BM * kF8Block];
+};
+
+// Block tile BN = 32 WN TN (output columns) x BM = 32 WM TM (tokens), WN x WM
+// waves of TN x TM MFMA tiles of 32 x 32. One LDS stage is one group of 128
+// bytes of K for the block's rows of both operands, double buffered; operands
+// go straight from global memory to LDS (1 KB per load: 8 rows x 128 bytes).
+// The 16-byte chunk c of row r sits at chunk position c ^ ((r >> 1) & 7), so
+// that the operand reads of 16 consecutive rows fall on distinct banks; a
+// lane fetches the global chunk that belongs at the position it writes. Rows
+// past N or M and chunks past K read zeros (their offset is past the buffer).
+// kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
+template <int WN, int WM, int TN, int TM, bool kWide>
+__global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
+    const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
+    const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
+    int tiles_n) {
+    constexpr int BN = 32 * WN * TN, BM = 32 * WM * TM, NW = WN * WM, kThreads = 64 * NW;
+    using Stage = F8Stage<BN, BM>;
+    __shared__ __attribute__((aligned(16))) Stage st0;
+    __shared__ __attribute__((aligned(16))) Stage st1;
+    __shared__ __attribute__((aligned(16))) float bias_s[BN];
+
+    int tile_n, tile_m;
+    fp8_tile_of_block(blockIdx.x, gridDim.x, tiles_n, tile_n, tile_m);
+    const int n0 = tile_n * BN;
+    const int m0 = tile_m * BM;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % WN;
+    const int wm = wave / WN;
+    const int r32 = lane & 31;
+    const int lh = lane >> 5;
+    const int S = (K + kF8Block - 1) / kF8Block;
+
+    const __amdgpu_buffer_rsrc_t ra = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(BN, N - n0) * (uint32_t)K);
+    const __amdgpu_buffer_rsrc_t rb = fp8_rsrc(qx + (size_t)m0 * K, (uint32_t)min(BM, M - m0) * (uint32_t)K);
+
+    // load j of a stage fills staged rows 8 j .. 8 j + 7 (the weights' rows
+    // first, then the activations'), lane l row 8 j + l / 8 at position l % 8
+    constexpr int kLoads = (BN + BM) / 8 / NW;
+    uint32_t gbase[kLoads];
+    int gchunk[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int j = wave * kLoads + i;
+        const int r = (j < BN / 8 ? j : j - BN / 8) * 8 + lane / 8;
+        gchunk[i] = ((lane % 8) ^ ((r >> 1) & 7)) * 16;
+        gbase[i] = (uint32_t)r * (uint32_t)K + (uint32_t)gchunk[i];
+    }
+    const bool loads_a = wave * kLoads < BN / 8;  // a wave's loads are all of one operand
+    static_assert((BN / 8) % kLoads == 0, "a wave loads one operand");
+    const int dst0 = (loads_a ? wave * kLoads : wave * kLoads - BN / 8) * 1024;
+    auto issue_stage = [&](int s, Stage &st) __attribute__((always_inline)) {
+        const int k0 = s * kF8Block;
+        const bool part = k0 + kF8Block > K;
+        uint8_t *dst = (loads_a ? st.a : st.b) + dst0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t off = gbase[i] + (uint32_t)k0;
+            if (part && k0 + gchunk[i] >= K) off = kF8Oob;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(loads_a ? ra : rb, (f8_lds_void *)(dst + i * 1024), 16, off, 0,
+                                                     0, 0);
+        }
+    };
+    // a lane's operand of one half (64 k) of a group: chunks 4 h + lh and 4 h + 2 + lh of row r
+    auto frag = [&](const uint8_t *base, int r, int h) __attribute__((always_inline)) {
+        const int x = (r >> 1) & 7;
+        const u32x4 lo = *reinterpret_cast<const u32x4 *>(base + r * kF8Block + ((4 * h + lh) ^ x) * 16);
+        const u32x4 hi = *reinterpret_cast<const u32x4 *>(base + r * kF8Block + ((4 * h + 2 + lh) ^ x) * 16);
+        return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    };
+
+    f32x16 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    // this wave's columns lie in one block of 128: one weight scale a group
+    const float *swr = sw + (size_t)((n0 + wn * 32 * TN) / kF8Block < (N + kF8Block - 1) / kF8Block
+                                         ? (n0 + wn * 32 * TN) / kF8Block
+                                         : 0) * S;
+    int mrow[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) mrow[i] = min(m0 + (wm * TM + i) * 32 + r32, M - 1);
+    auto scales = [&](int s, float (&out)[TM]) __attribute__((always_inline)) {
+        const float w = swr[s];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) out[i] = sx[(size_t)s * M + mrow[i]] * w;
+    };
+
+    for (int i = tid; i < BN; i += kThreads)
+        bias_s[i] = bias && n0 + i < N ? bf16_bits_to_f32(bias[n0 + i]) : 0.0f;
+    issue_stage(0, st0);
+    float sc[TM], sc_next[TM];
+    scales(0, sc);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+
+    auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
+        if (s + 1 < S) {
+            scales(s + 1, sc_next);
+            issue_stage(s + 1, nxt);
+        }
+        i32x8 b[TM][2];
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) b[j][h] = frag(cur.b, (wm * TM + j) * 32 + r32, h);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            const int r = (wn * TN + i) * 32 + r32;
+            const i32x8 a0 = frag(cur.a, r, 0), a1 = frag(cur.a, r, 1);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                f32x16 p;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[e] = 0.0f;
+                if constexpr (kWide) {
+                    p = mfma_wide_32x32x64(a0, b[j][0], p);
+                    p = mfma_wide_32x32x64(a1, b[j][1], p);
+                } else {
+                    p = mfma_fp8_32x32x64(a0, b[j][0], p);
+                    p = mfma_fp8_32x32x64(a1, b[j][1], p);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(sc[j], p[e], acc[i][j][e]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TM; ++j) sc[j] = sc_next[j];
+        // stage s + 1 has landed, and everyone is done with stage s
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+    };
+    int s = 0;
+    for (; s + 1 < S; s += 2) {
+        run_stage(s, st0, st1);
+        run_stage(s + 1, st1, st0);
+    }
+    if (s < S) run_stage(s, st0, st1);
+
+    // Output: 32 tokens x BN columns at a time through LDS (the waves of one
+    // wm write, everyone stores whole row segments), alternating between the
+    // two stages.
+    constexpr int wide = kWide ? 4 : 2;
+    constexpr int pitch = BN * wide + 16;
+    static_assert(sizeof(Stage) >= 32 * pitch, "LDS too small for the output tile");
+    constexpr int pieces = BN * wide / 16;  // 16-byte pieces of a row
+#pragma unroll
+    for (int p = 0; p < WM * TM; ++p) {
+        uint8_t *buf = reinterpret_cast<uint8_t *>((p & 1) ? &st1 : &st0);
+        if (wm == p / TM) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int qq = 0; qq < 4; ++qq) {
+                    const int nl = (wn * TN + i) * 32 + 8 * qq + 4 * lh;
+                    const f32x4 bv = *reinterpret_cast<const f32x4 *>(bias_s + nl);
+                    f32x4 v;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) v[t] = acc[i][p % TM][4 * qq + t] + bv[t];
+                    if constexpr (kWide)
+                        *reinterpret_cast<f32x4 *>(buf + r32 * pitch + nl * 4) = v;
+                    else
+                        *reinterpret_cast<u32x2 *>(buf + r32 * pitch + nl * 2) =
+                            u32x2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
+                }
+        }
+        __syncthreads();
+        for (int c = tid; c < 32 * pieces; c += kThreads) {
+            const int row = c / pieces, piece = c % pieces;
+            const int m = m0 + 32 * p + row;
+            const int64_t n = n0 + piece * (16 / wide);
+            if (m < M && n < N)
+                *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(Y) + ((int64_t)m * N + n) * wide) =
+                    *reinterpret_cast<const u32x4 *>(buf + row * pitch + piece * 16);
+        }
+    }
+}
+
+// ---- the product, few tokens -----------------------------------------------
+
+// One block computes 16 output columns of at most 16 MT tokens; its W waves
+// take the groups of K in turn (wave w groups w, w + W, ...), kF8Ahead of them
+// in flight, straight from global memory into the operands of the 16x16x128
+// MFMA (weights as A: row = output column; tokens as B), and add their sums in
+// LDS in a fixed order. The weight is read once: HBM-bound.
+constexpr int kF8Ahead = 4;
+
+template <int W, int MT, bool kWide>
+__global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(const uint8_t *__restrict__ qx,
+                                                            const float *__restrict__ sx,
+                                                            const uint8_t *__restrict__ qw,
+                                                            const float *__restrict__ sw,
+                                                            const uint16_t *__restrict__ bias, int M, int N, int K,
+                                                            void *__restrict__ Y) {
+    __shared__ f32x4 red[W][MT][64];
+    const int n0 = blockIdx.x * 16;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, q4 = lane >> 4;
+    const int G = (K + kF8Block - 1) / kF8Block;
+    const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(16, N - n0) * (uint32_t)K);
+    const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(qx, (uint32_t)M * (uint32_t)K);
+    const float *swr = sw + (size_t)(n0 / kF8Block) * G;
+
+    // a lane's 32 codes of a group: chunks of 16 at k = 16 q4 and 64 + 16 q4
+    auto operand = [&](__amdgpu_buffer_rsrc_t r, int row, int g) __attribute__((always_inline)) {
+        const int k = g * kF8Block + 16 * q4;
+        const uint32_t off = (uint32_t)row * (uint32_t)K + (uint32_t)k;
+        const u32x4 lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k < K ? off : kF8Oob, 0, 0));
+        const u32x4 hi =
+            __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k + 64 < K ? off + 64 : kF8Oob, 0, 0));
+        return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    };
+
+    f32x4 acc[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int mrow[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) mrow[j] = min(16 * j + r16, M - 1);
+
+    for (int g0 = wave; g0 < G; g0 += W * kF8Ahead) {
+        i32x8 a[kF8Ahead], b[kF8Ahead][MT];
+        float s[kF8Ahead][MT];
+#pragma unroll
+        for (int u = 0; u < kF8Ahead; ++u) {
+            const int g = g0 + W * u;  // past K: every chunk reads zeros
+            a[u] = operand(rw, r16, g);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                b[u][j] = operand(rx, mrow[j], g);
+                s[u][j] = sx[(size_t)min(g, G - 1) * M + mrow[j]] * swr[min(g, G - 1)];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kF8Ahead; ++u) {
+            if (g0 + W * u >= G) break;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                const f32x4 p = kWide ? mfma_wide_16x16x128(a[u], b[u][j], zero) : mfma_fp8_16x16x128(a[u], b[u][j], zero);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(s[u][j], p[e], acc[j][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) red[wave][j][lane] = acc[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256 * MT; i += 64 * W) {
+        const int m = i >> 4, c = i & 15;  // consecutive threads: consecutive columns of a token
+        const int src = 16 * (c >> 2) + (m & 15);
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) v += red[w][m >> 4][src][c & 3];
+        const int n = n0 + c;
+        if (m < M && n < N) {
+            if (bias) v += bf16_bits_to_f32(bias[n]);
+            if constexpr (kWide)
+                static_cast<float *>(Y)[(size_t)m * N + n] = v;
+            else
+                static_cast<uint16_t *>(Y)[(size_t)m * N + n] = (uint16_t)f32_to_bf16_bits(v);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, hipStream_t stream) {
+    const int G = fp8_blocks(K);
+    hipLaunchKernelGGL(fp8_quantize_kernel,
+                       dim3((M + kF8QRows - 1) / kF8QRows, (G + kF8QGroups - 1) / kF8QGroups), dim3(kF8QThreads), 0,
+                       stream, X, M, K, G, qx, sx);
+    return hipGetLastError();
+}
+
+template <int WN, int WM, int TN, int TM, bool kWide>
+static hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
+                              const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
+    constexpr int BN = 32 * WN * TN, BM = 32 * WM * TM;
+    const int tiles_n = (N + BN - 1) / BN, tiles_m = (M + BM - 1) / BM;
+    hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, TN, TM, kWide>), dim3(tiles_n * tiles_m), dim3(64 * WN * WM), 0,
+                       stream, qx, sx, qw, sw, bias, M, N, K, Y, tiles_n);
+    return hipGetLastError();
+}
+
+template <bool kWide>
+static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
+                              const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
+    if (M <= 64) {
+        const dim3 grid((N + 15) / 16), block(512);
+        auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, block, 0, stream, qx, sx, qw, sw, bias, M, N, K, Y);
+        };
+        if (M <= 16)
+            go(fp8_skinny_kernel<8, 1, kWide>);
+        else if (M <= 32)
+            go(fp8_skinny_kernel<8, 2, kWide>);
+        else
+            go(fp8_skinny_kernel<8, 4, kWide>);
+        return hipGetLastError();
+    }
+    const int64_t big = (int64_t)((N + 255) / 256) * ((M + 255) / 256);
+    if (big >= 128) {
+        if constexpr (kWide)
+            return launch_tile<2, 2, 2, 2, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+        else
+            return launch_tile<2, 4, 4, 2, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+    }
+    return launch_tile<2, 2, 1, 1, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+}
+
+hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
+                           const uint16_t *bias, int M, int N, int K, void *Y, bool y_f32, hipStream_t stream) {
+    return y_f32 ? launch_gemm<true>(qx, sx, qw, sw, bias, M, N, K, Y, stream)
+                 : launch_gemm<false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+}
+
+}  // namespace svdq

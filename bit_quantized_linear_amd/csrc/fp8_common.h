@@ -1,0 +1,93 @@
+// Device helpers shared by the block-scaled FP8 kernels (fp8.hip,
+// fp8_moe.hip): the code format, conversions and MFMA wrappers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "device_common.h"
+
+namespace svdq {
+
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kF8Block = 128;             // features, and output columns, per scale
+constexpr float kF8Max = 448.0f;          // largest E4M3 value
+constexpr uint32_t kF8TinyBits = 0x0D80u;  // bf16 bits of 2^-100, the least magnitude a scale is made from
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t fp8_rsrc(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+// E4M3 x E4M3 with fp32 accumulation, unscaled. A lane's operand is 32 codes
+// of one row (A) or column (B); the 32x32 output layout is that of the other
+// 32x32 MFMAs. The matrix core adds the 8 products of a lane's 8 consecutive
+// codes aligned to the largest of them and cuts what lies 14 or more bits
+// below its leading one (measured: 2^16 + 2^3 is exact, 2^16 + 7.5 gives
+// 2^16); everything else is summed as in fp32. That is a relative error of
+// about 2e-5 of a sum of random products: a hundredth of bf16's rounding, but
+// two hundred times that of fp32, so outputs in fp32 take the bf16 MFMA
+// (mfma_wide_*), whose operands hold E4M3 values exactly and whose sums keep
+// 24 bits.
+__device__ __forceinline__ f32x16 mfma_fp8_32x32x64(i32x8 a, i32x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mfma_fp8_16x16x128(i32x8 a, i32x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// Eight E4M3 codes as bf16 values (exact).
+__device__ __forceinline__ bf16x8 fp8_widen8(uint32_t a, uint32_t b) {
+    u32x4 v;
+    v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false));
+    v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true));
+    v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false));
+    v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true));
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// The products of the two functions above on bf16 MFMAs.
+__device__ __forceinline__ f32x16 mfma_wide_32x32x64(i32x8 a, i32x8 b, f32x16 c) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) c = mfma_bf16_32x32x16(fp8_widen8(a[i], a[i + 1]), fp8_widen8(b[i], b[i + 1]), c);
+    return c;
+}
+
+__device__ __forceinline__ f32x4 mfma_wide_16x16x128(i32x8 a, i32x8 b, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) c = mfma_bf16_16x16x32(fp8_widen8(a[i], a[i + 1]), fp8_widen8(b[i], b[i + 1]), c);
+    return c;
+}
+
+// The E4M3 codes (nearest even; NaN for NaN) of 8 bf16 values times r.
+__device__ __forceinline__ u32x2 fp8_codes8(u32x4 v, float r) {
+    u32x2 out;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float x0 = __uint_as_float(v[2 * i] << 16) * r, x1 = __uint_as_float(v[2 * i] & 0xFFFF0000u) * r;
+        const float x2 = __uint_as_float(v[2 * i + 1] << 16) * r,
+                    x3 = __uint_as_float(v[2 * i + 1] & 0xFFFF0000u) * r;
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(x0, x1, 0, false);
+        out[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x2, x3, w, true);
+    }
+    return out;
+}
+
+// Blocks are dealt to the 8 XCDs round-robin (block b runs on XCD b % 8): XCD
+// c takes a contiguous tile range, walked four token tiles at a time across
+// the columns, so that the tiles an XCD runs together share operand rows in
+// its L2. With T tiles the first T % 8 XCDs have one tile more.
+__device__ __forceinline__ void fp8_tile_of_block(int b, int T, int tiles_n, int &tile_n, int &tile_m) {
+    const int x = b % 8, per = T / 8, more = T % 8;
+    const int id = x * per + min(x, more) + b / 8;
+    const int tiles_m = T / tiles_n;
+    const int group = id / (4 * tiles_n);
+    const int gm = min(4, tiles_m - group * 4);
+    const int in_group = id - group * 4 * tiles_n;
+    tile_m = group * 4 + in_group % gm;
+    tile_n = in_group / gm;
+}
+
+}  // namespace svdq

@@ -26,13 +26,14 @@ svdq_status mx_prepare_residual_impl(const uint16_t *W, int K, int N, const floa
 size_t mx_scale_ld(int rows);
 svdq_status w4a16_prepare_impl(const uint16_t *W, int K, int N, uint8_t *packed);
 size_t w4a16_container_bytes(int K, int N);
+svdq_status fp8_prepare_impl(const uint16_t *W, int K, int N, uint8_t *qw, float *sw);
 svdq_status repack_codes_impl(const uint8_t *q, int rows, int K, int qfmt, uint8_t *out);
 svdq_status truncated_svd(const double *A, int K, int N, int rank, double *U,
                           double *S, double *V);
 bool all_finite_bf16(const uint16_t *p, int64_t n);
 
 // ---- device launchers (act_quant.hip, w4a4_gemm.hip, w4a4_fp6_gemm.hip, w8a8.hip, w4a16.hip,
-//      mx_gemm.hip) ----
+//      mx_gemm.hip, fp8.hip, fp8_moe.hip) ----
 // Arguments are validated by the caller; launchers only pick a grid and launch.
 hipError_t launch_channel_absmax(const uint16_t *X, int M, int K, float *absmax,
                                  hipStream_t stream);
@@ -97,6 +98,18 @@ hipError_t launch_mx_linear(const uint8_t *qx, const uint8_t *ux, const uint16_t
                             int rank, void *Y, bool y_f32, hipStream_t stream);
 hipError_t launch_w4a16_linear(const uint16_t *X, const uint8_t *packed, const uint16_t *bias, int M,
                                int N, int K, uint16_t *Y, hipStream_t stream);
+
+// block-scaled FP8 (fp8.hip, fp8_moe.hip)
+inline int fp8_blocks(int n) { return (n + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK; }
+// byte offset of the scales behind the codes of X in svdq_fp8_linear's workspace
+inline size_t fp8_workspace_scales(int M, int K) { return ((size_t)M * (size_t)K + 255) / 256 * 256; }
+hipError_t launch_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, hipStream_t stream);
+hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
+                           const uint16_t *bias, int M, int N, int K, void *Y, bool y_f32, hipStream_t stream);
+size_t fp8_moe_workspace_size(int T, int I, int E, int top_k);
+hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *w13, const float *s13,
+                          const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k, bool renorm,
+                          int32_t *idx, float *gate, void *workspace, uint16_t *Y, hipStream_t stream);
 
 // matrix-core rate microbenchmark (peak.hip)
 int64_t mfma_rate_ops_per_wave_round(int kind);

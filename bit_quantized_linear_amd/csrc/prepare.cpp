@@ -481,6 +481,42 @@ svdq_status w8a8_prepare_impl(const uint16_t *W, int K, int N, int8_t *qw, float
     return SVDQ_OK;
 }
 
+// E4M3 code of v (nearest even, |v| < 464; v is finite): the step is 2^-9 below
+// 2^-6 and an eighth of the binade above.
+static uint8_t e4m3_code(float v) {
+    const float m = std::fabs(v);
+    int x = -6;
+    if (m > 0.0f) std::frexp(m, &x);  // m = f 2^x, f in [0.5, 1): binade x - 1
+    const int binade = std::max(x - 1, -6);
+    // m / step, an integer up to 16 after rounding (16: the next binade's first)
+    const int u = (int)std::nearbyint(std::ldexp(m, 3 - binade));
+    // 8 codes per binade: u of binade -6 counts from code 0, of a higher one from its own 8
+    const int code = (binade + 6) * 8 + u;
+    return (uint8_t)(code | (std::signbit(v) ? 0x80 : 0));
+}
+
+svdq_status fp8_prepare_impl(const uint16_t *W, int K, int N, uint8_t *qw, float *sw) {
+    const int G = fp8_blocks(K), B = fp8_blocks(N);
+    parallel_for(0, B, [&](int64_t b0, int64_t b1) {
+        for (int64_t b = b0; b < b1; ++b) {
+            const int n0 = (int)b * SVDQ_FP8_BLOCK, n1 = std::min(N, n0 + SVDQ_FP8_BLOCK);
+            for (int g = 0; g < G; ++g) {
+                const int k0 = g * SVDQ_FP8_BLOCK, k1 = std::min(K, k0 + SVDQ_FP8_BLOCK);
+                float amax = std::ldexp(1.0f, -100);
+                for (int k = k0; k < k1; ++k)
+                    for (int n = n0; n < n1; ++n)
+                        amax = std::max(amax, std::fabs(bf16_to_f32(W[(int64_t)k * N + n])));
+                sw[b * G + g] = amax / 448.0f;
+                const float r = 448.0f / amax;
+                for (int k = k0; k < k1; ++k)
+                    for (int n = n0; n < n1; ++n)
+                        qw[(int64_t)n * K + k] = e4m3_code(bf16_to_f32(W[(int64_t)k * N + n]) * r);
+            }
+        }
+    });
+    return SVDQ_OK;
+}
+
 // W4A16 container (the awq_w4a16 layer type): each column's K-groups
 // quantized like the residual above, then written in units of 32 columns
 // (two tiles of 16) x one pair of K-groups (128 k). Unit (b, p) holds 2 x

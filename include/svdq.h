@@ -111,6 +111,10 @@ typedef enum svdq_qformat {
 
 #define SVDQ_GROUP 64
 #define SVDQ_MAX_RANK 64
+#define SVDQ_FP8_BLOCK 128
+#define SVDQ_FP8_MOE_MAX_TOKENS 64
+#define SVDQ_FP8_MOE_MAX_EXPERTS 256
+#define SVDQ_FP8_MOE_MAX_TOP_K 16
 
 /* Text of a status code (static storage; never NULL). */
 const char *svdq_status_string(int status);
@@ -243,6 +247,21 @@ size_t w4a16_weight_bytes(int K, int N);
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, NUMERICAL (non-finite W). */
 svdq_status w4a16_prepare_weights(const uint16_t *W, int K, int N, int group,
                                   uint8_t *packed);
+
+/* ------------------------------------------- block-scaled FP8 (HOST) --- */
+
+/* Weight preparation of the block-scaled FP8 linear: OCP E4M3 codes with one
+ * fp32 scale per 128 x 128 block of the weight (the last blocks of a row or
+ * column hold what is left of N and K).
+ *   per block: A = max(max |W|, 2^-100), sw = fp32(A / 448),
+ *   qw = E4M3(fp32(W * fp32(448 / A))), round to nearest even.
+ * In:  W [K, N] bf16 bits.
+ * Out: qw [N, K] E4M3 bytes (one row per output column, K contiguous);
+ *      sw [ceil(N/128), ceil(K/128)] fp32. Codes and scales of a checkpoint
+ *      quantized elsewhere in this layout (value = code * scale) serve as well.
+ * Shapes: K % 16 == 0, N % 8 == 0.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, NUMERICAL (non-finite W). */
+svdq_status svdq_fp8_prepare_weights(const uint16_t *W, int K, int N, uint8_t *qw, float *sw);
 
 /* Re-encodes packed codes from the canonical INT4 container into `qfmt`
  * (SVDQ_QFMT_INT4 copies). In: q [rows, K/2]; out: [rows, svdq_qrow_bytes(K,
@@ -454,6 +473,88 @@ svdq_status svdq_mx_linear(const uint8_t *qx, const uint8_t *ux,
 svdq_status w4a16_linear(const uint16_t *X, const uint8_t *packed,
                          const uint16_t *bias, int M, int N, int K, int group,
                          uint16_t *Y, void *stream);
+
+/* Activation quantization of the block-scaled FP8 linear -- one pass over X:
+ *   per token m and block g of 128 features (the last holds what is left of
+ *   K): A = max(max |X|, 2^-100), sx[g, m] = fp32(A / 448),
+ *   qx = E4M3(fp32(X * fp32(448 / A))), round to nearest even.
+ *   A block with a NaN gives NaN codes and scale; one with an infinity an
+ *   infinite scale and a NaN code for it: its token's outputs are NaN.
+ * In:  X [M, K] bf16.
+ * Out: qx [M, K] E4M3 bytes; sx [ceil(K/128), M] fp32.
+ * Shapes: M >= 0 (M == 0 launches nothing), K % 16 == 0.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
+ *      HIP. */
+svdq_status svdq_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, void *stream);
+
+/* The block-scaled FP8 product on quantized activations (one pass of
+ * svdq_fp8_quantize_act can serve several linears):
+ *   acc[m, n] = sum_g (sx[g, m] sw[n/128, g]) sum_{k in g} qx[m, k] qw[n, k]
+ *               (one fp32 FMA per block)
+ *   Y = acc + bias[n], rounded once to bf16 (nearest even) or stored as fp32.
+ * A block's sum for a bf16 output comes from the FP8 MFMA, which cuts products
+ * more than 13 bits below the largest of their 8 neighbours (a relative error
+ * of about 2e-5, a hundredth of the output's rounding); for an fp32 output
+ * from the bf16 MFMA on the same values, to fp32 precision, at a lower rate.
+ * In:  qx, sx (svdq_fp8_quantize_act); qw, sw (svdq_fp8_prepare_weights);
+ *      bias [N] bf16 or NULL; y_dtype SVDQ_BF16 or SVDQ_F32.
+ * Out: Y [M, N]. Shapes: M >= 0 (M == 0 launches nothing), K % 16 == 0,
+ *      N % 8 == 0, K < 2^22. Deterministic.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
+ *      HIP. */
+svdq_status svdq_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
+                          const uint16_t *bias, int M, int N, int K, void *Y, int y_dtype, void *stream);
+
+/* Bytes of device workspace svdq_fp8_linear needs for an [M, K] input (0 on a
+ * bad argument): the codes and scales of X. */
+size_t svdq_fp8_workspace_bytes(int M, int K);
+
+/* The block-scaled FP8 linear from bf16 activations: svdq_fp8_quantize_act and
+ * svdq_fp8_gemm, with the same results.
+ * In:  X [M, K] bf16; the rest as svdq_fp8_gemm; workspace of at least
+ *      svdq_fp8_workspace_bytes(M, K) bytes (device, 16-byte aligned, not read
+ *      before it is written; calls that may overlap in time need one each).
+ * Out: Y [M, N]. Shapes and errors: as svdq_fp8_gemm. */
+svdq_status svdq_fp8_linear(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias,
+                            int M, int N, int K, void *workspace, size_t workspace_bytes, void *Y,
+                            int y_dtype, void *stream);
+
+/* Bytes of device workspace of svdq_fp8_moe_layer (0 on a bad argument). */
+size_t svdq_fp8_moe_workspace_bytes(int T, int I, int E, int top_k);
+
+/* A mixture-of-experts layer for a few tokens: router, gated experts with
+ * block-scaled FP8 weights and bf16 activations, weighted sum.
+ *   l[t, e]  = sum_h X[t, h] Wr[e, h]                    (fp64)
+ *   idx[t]   = the top_k largest l[t], in descending order, ties to the lowest
+ *              expert (NaN orders below every number)
+ *   gate[t, j] = exp(l[t, idx_j]) / sum exp(l[t, e])  -- the sum over all
+ *              experts, or over the chosen ones if renormalize != 0
+ *   for e = idx[t, j]:  g = X[t] W13[e, 0]^T, u = X[t] W13[e, 1]^T   (fp32),
+ *              h = g / (1 + exp(-g)) * u  (kept to 16 significant bits),
+ *              o[t, j] = h W2[e]^T                         (fp32)
+ *   Y[t]     = sum_j gate[t, j] o[t, j], rounded once to bf16.
+ * The value of a weight is its E4M3 code times its block's scale.
+ * In:  X [T, H] bf16; wr [E, H] bf16; w13 [E, 2, I, H] E4M3 (gate, up) with
+ *      s13 [E, 2, ceil(I/128), ceil(H/128)] fp32; w2 [E, H, I] E4M3 with
+ *      s2 [E, ceil(H/128), ceil(I/128)] fp32: each matrix as
+ *      svdq_fp8_prepare_weights writes it for one expert.
+ * Out: Y [T, H] bf16; idx [T, top_k] int32 and gate [T, top_k] fp32, the
+ *      choices (each may be NULL).
+ * Workspace: device memory of at least svdq_fp8_moe_workspace_bytes(T, I, E,
+ *      top_k) bytes, owned by the caller, not read before it is written; calls
+ *      that may overlap in time need one each.
+ * Shapes: 0 <= T <= SVDQ_FP8_MOE_MAX_TOKENS (T == 0 launches nothing),
+ *      H % 16 == 0, I % 16 == 0, 1 <= E <= SVDQ_FP8_MOE_MAX_EXPERTS,
+ *      1 <= top_k <= min(E, SVDQ_FP8_MOE_MAX_TOP_K), H < 2^22, I < 2^22.
+ * The weights of the experts that some token chose are read once (those of an
+ * expert with more than 16 tokens once per 16). Deterministic; a token's
+ * outputs depend on its own row of X only.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
+ *      HIP. */
+svdq_status svdq_fp8_moe_layer(const uint16_t *X, const uint16_t *wr, const uint8_t *w13, const float *s13,
+                               const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k,
+                               int renormalize, int32_t *idx, float *gate, void *workspace,
+                               size_t workspace_bytes, uint16_t *Y, void *stream);
 
 /* ------------------------------------------- TEST-ONLY (same kernels) --- */
 

@@ -31,10 +31,13 @@ against the pages:
   down-projection) with the down-projection's activation side produced from
   the up-projection's output (``oracle/mlp.py``).
 
+* the block-scaled FP8 linear and the mixture-of-experts layer on its weights
+  (``oracle/fp8.py``) are not on the pages; their definition stands there.
+
 Where the pages leave a step open, the reading taken is stated at the
 function that takes it. Parity status of every function is listed in
 ``oracle/svdquant.py``, ``oracle/w8a8.py``, ``oracle/w4a16.py``,
-``oracle/mxfp4.py`` and ``oracle/mlp.py`` headers.
+``oracle/mxfp4.py``, ``oracle/mlp.py`` and ``oracle/fp8.py`` headers.
 """
 
-from . import mlp, mxfp4, svdquant, w4a16, w8a8  # noqa: F401
+from . import fp8, mlp, mxfp4, svdquant, w4a16, w8a8  # noqa: F401

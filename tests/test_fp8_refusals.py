@@ -1,0 +1,132 @@
+"""What the block-scaled FP8 entry points refuse, before anything is launched:
+by the library (shapes, null and misaligned pointers, an unsupported device)
+and by the binding (tensors that do not cover what a call touches). No GPU."""
+
+import pytest
+
+from bit_quantized_linear_amd import binding as b
+from tests.test_binding_checks import Dev, Reached, guarded  # noqa: F401
+
+FAKE = 0x10000
+MISALIGNED = 0x10008
+INVALID, SHAPE, MIS = b.SVDQ_ERR_INVALID_ARGUMENT, b.SVDQ_ERR_UNSUPPORTED_SHAPE, b.SVDQ_ERR_MISALIGNED
+
+
+def quantize(X=FAKE, M=16, K=128, qx=FAKE, sx=FAKE):
+    return b.lib().svdq_fp8_quantize_act(X, M, K, qx, sx, None)
+
+
+def gemm(qx=FAKE, sx=FAKE, qw=FAKE, sw=FAKE, bias=None, M=16, N=64, K=128, Y=FAKE, dt=0):
+    return b.lib().svdq_fp8_gemm(qx, sx, qw, sw, bias, M, N, K, Y, dt, None)
+
+
+def linear(X=FAKE, qw=FAKE, sw=FAKE, bias=None, M=16, N=64, K=128, ws=FAKE, wb=1 << 20, Y=FAKE, dt=0):
+    return b.lib().svdq_fp8_linear(X, qw, sw, bias, M, N, K, ws, wb, Y, dt, None)
+
+
+def moe(X=FAKE, wr=FAKE, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, T=2, H=64, I=32, E=4, k=2, idx=None,  # noqa: E741
+        gate=None, ws=FAKE, wb=1 << 20, Y=FAKE):
+    return b.lib().svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, T, H, I, E, k, 1, idx, gate, ws, wb, Y, None)
+
+
+@pytest.mark.parametrize("call,args,status", [
+    (quantize, {"M": -1}, INVALID), (quantize, {"K": 0}, INVALID), (quantize, {"K": 120}, SHAPE),
+    (quantize, {"K": 1 << 22}, SHAPE), (quantize, {"X": None}, INVALID), (quantize, {"sx": None}, INVALID),
+    (quantize, {"qx": MISALIGNED}, MIS),
+    (gemm, {"M": -1}, INVALID), (gemm, {"N": 0}, INVALID), (gemm, {"K": 72}, SHAPE), (gemm, {"N": 60}, SHAPE),
+    (gemm, {"K": 1 << 22}, SHAPE), (gemm, {"M": 2147483647, "N": 2147483640}, SHAPE), (gemm, {"dt": 2}, INVALID),
+    (gemm, {"qw": None}, INVALID), (gemm, {"sx": None}, INVALID), (gemm, {"Y": None}, INVALID),
+    (gemm, {"bias": MISALIGNED}, MIS), (gemm, {"sw": MISALIGNED}, MIS),
+    (linear, {"wb": 16 * 128}, INVALID), (linear, {"ws": None}, INVALID), (linear, {"X": None}, INVALID),
+    (linear, {"X": MISALIGNED}, MIS), (linear, {"N": 4}, SHAPE), (linear, {"K": 24}, SHAPE),
+    (moe, {"T": -1}, INVALID), (moe, {"T": 65}, SHAPE), (moe, {"H": 72}, SHAPE), (moe, {"I": 40}, SHAPE),
+    (moe, {"E": 257}, SHAPE), (moe, {"k": 0}, INVALID), (moe, {"k": 5}, INVALID),
+    (moe, {"E": 64, "k": 17}, SHAPE), (moe, {"wb": 64}, INVALID), (moe, {"ws": None}, INVALID),
+    (moe, {"w13": None}, INVALID), (moe, {"s2": None}, INVALID), (moe, {"X": None}, INVALID),
+    (moe, {"Y": None}, INVALID), (moe, {"idx": MISALIGNED}, MIS), (moe, {"w2": MISALIGNED}, MIS),
+], ids=str)
+def test_refused_before_a_launch(call, args, status):
+    assert call(**args) == status
+
+
+@pytest.mark.parametrize("call", [quantize, gemm, linear, moe])
+def test_other_devices_fail_closed(call):
+    b.svdq_debug_set_arch_override("gfx942")
+    try:
+        assert call() == b.SVDQ_ERR_UNSUPPORTED_DEVICE
+    finally:
+        b.svdq_debug_set_arch_override(None)
+
+
+def test_workspace_bytes():
+    assert b.svdq_fp8_workspace_bytes(3, 144) >= 3 * 144 + 4 * 2 * 3
+    assert b.svdq_fp8_workspace_bytes(0, 144) == 0 and b.svdq_fp8_workspace_bytes(-1, 144) == 0
+    assert b.svdq_fp8_workspace_bytes(3, 100) == 0
+    assert b.svdq_fp8_moe_workspace_bytes(2, 32, 4, 2) >= 2 * 2 * 2 * 32 * 2
+    assert b.svdq_fp8_moe_workspace_bytes(2, 32, 0, 2) == 0
+
+
+def _case(name):
+    M, K, N = 40, 144, 136
+    ws = lambda n: Dev((n,), 1)  # noqa: E731
+    if name == "quantize":
+        return lambda t: b.svdq_fp8_quantize_act(t["X"], t["qx"], t["sx"]), {
+            "X": Dev((M, K), 2), "qx": Dev((M, K), 1), "sx": Dev((2, M), 4)}
+    if name == "gemm":
+        return lambda t: b.svdq_fp8_gemm(t["qx"], t["sx"], t["qw"], t["sw"], t["bias"], t["Y"]), {
+            "qx": Dev((M, K), 1), "sx": Dev((2, M), 4), "qw": Dev((N, K), 1), "sw": Dev((2, 2), 4),
+            "bias": Dev((N,), 2), "Y": Dev((M, N), 2)}
+    if name == "linear":
+        return lambda t: b.svdq_fp8_linear(t["X"], t["qw"], t["sw"], t["bias"], t["ws"], t["Y"]), {
+            "X": Dev((M, K), 2), "qw": Dev((N, K), 1), "sw": Dev((2, 2), 4), "bias": Dev((N,), 2),
+            "ws": ws(b.svdq_fp8_workspace_bytes(M, K)), "Y": Dev((M, N), 4)}
+    T, H, I, E, k = 3, 144, 48, 5, 2  # noqa: E741
+    return lambda t: b.svdq_fp8_moe_layer(t["X"], t["wr"], t["w13"], t["s13"], t["w2"], t["s2"], t["Y"], t["idx"],
+                                          t["gate"], t["ws"]), {
+        "X": Dev((T, H), 2), "wr": Dev((E, H), 2), "w13": Dev((E, 2, I, H), 1), "s13": Dev((E, 2, 1, 2), 4),
+        "w2": Dev((E, H, I), 1), "s2": Dev((E, 2, 1), 4), "Y": Dev((T, H), 2), "idx": Dev((T, k), 4),
+        "gate": Dev((T, k), 4), "ws": ws(b.svdq_fp8_moe_workspace_bytes(T, I, E, k))}
+
+
+class SizeQueries:
+    """The guard of the shared fixture lets the older size queries through;
+    the ones here go to the library too."""
+
+    def __init__(self, guard):
+        self.guard = guard
+
+    def __getattr__(self, name):
+        if name in ("svdq_fp8_workspace_bytes", "svdq_fp8_moe_workspace_bytes"):
+            return getattr(self.guard.real, name)
+        return getattr(self.guard, name)
+
+
+@pytest.mark.parametrize("name", ["quantize", "gemm", "linear", "moe"])
+def test_the_binding_checks_every_tensor(name, guarded, monkeypatch):  # noqa: F811
+    sized = SizeQueries(guarded)
+    monkeypatch.setattr(b, "lib", lambda: sized)
+    call, tensors = _case(name)
+    with pytest.raises(Reached):
+        call(tensors)
+    for arg, t in tensors.items():
+        short = Dev((1,) * len(t.shape), t.element_size())
+        if (name, arg) != ("quantize", "X"):  # whose shape is what gives the sizes
+            with pytest.raises((ValueError, TypeError)):
+                call({**tensors, arg: short})
+        with pytest.raises((ValueError, TypeError)):
+            call({**tensors, arg: Dev(t.shape, t.element_size(), device=1)})
+        if arg != "ws":
+            with pytest.raises((ValueError, TypeError)):
+                call({**tensors, arg: Dev(t.shape, 8)})
+
+
+def test_moe_shapes_that_do_not_fit(guarded, monkeypatch):  # noqa: F811
+    sized = SizeQueries(guarded)
+    monkeypatch.setattr(b, "lib", lambda: sized)
+    call, t = _case("moe")
+    for arg, shape in (("wr", (5, 128)), ("w13", (5, 2, 48, 128)), ("w13", (4, 2, 48, 144)), ("w2", (5, 48, 144)),
+                       ("gate", (3, 3)), ("idx", (2, 2))):
+        with pytest.raises(ValueError):
+            call({**t, arg: Dev(shape, t[arg].element_size())})
+    with pytest.raises(ValueError):
+        b.svdq_fp8_moe_layer(t["X"], t["wr"], t["w13"], t["s13"], t["w2"], t["s2"], t["Y"], None, None, t["ws"])
