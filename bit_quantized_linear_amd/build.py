@@ -41,9 +41,10 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I
 HIP_FLAGS = COMMON + [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",
                       "-packed-fp32-ops"]
 CXX_FLAGS = COMMON + ["-I", os.path.join(ROCM, "include"), "-D__HIP_PLATFORM_AMD__", "-pthread"]
-# per-source extras: the W4A16 kernel feeds every MFMA result straight into
-# VALU arithmetic, so its MFMAs write VGPRs (no accumulation-register copies)
-HIP_EXTRA = {"w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# per-source extras: the W4A16 and block-scaled FP8 kernels feed every MFMA
+# result straight into VALU arithmetic, so their MFMAs write VGPRs (no
+# accumulation-register copies)
+HIP_EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("w4a16.hip", "fp8.hip", "fp8_moe.hip")}
 
 
 def _run(cmd):

@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "fp8_common.h"
@@ -83,22 +84,52 @@ struct F8Stage {
     uint8_t b[BM * kF8Block];
 };
 
-// Block tile BN = 32 WN TN (output columns) x BM = 32 WM TM (tokens), WN x WM
-// waves of TN x TM MFMA tiles of 32 x 32. One LDS stage is one group of 128
+// Operands of one 16-row tile and group: the codes, or their bf16 values.
+struct F8Codes {
+    i32x8 v;
+    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+        v = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    }
+    __device__ __forceinline__ static f32x4 product(const F8Codes &a, const F8Codes &b) {
+        return mfma_fp8_16x16x128(a.v, b.v, f32x4{0.f, 0.f, 0.f, 0.f});
+    }
+};
+
+struct F8Wide {
+    bf16x8 v[4];
+    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+        v[0] = fp8_widen8(lo[0], lo[1]);
+        v[1] = fp8_widen8(lo[2], lo[3]);
+        v[2] = fp8_widen8(hi[0], hi[1]);
+        v[3] = fp8_widen8(hi[2], hi[3]);
+    }
+    __device__ __forceinline__ static f32x4 product(const F8Wide &a, const F8Wide &b) {
+        f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = mfma_bf16_16x16x32(a.v[i], b.v[i], c);
+        return c;
+    }
+};
+
+// Block tile BN = 16 WN TN (output columns) x BM = 16 WM TM (tokens), WN x WM
+// waves of TN x TM MFMA tiles of 16 x 16. One LDS stage is one group of 128
 // bytes of K for the block's rows of both operands, double buffered; operands
 // go straight from global memory to LDS (1 KB per load: 8 rows x 128 bytes).
 // The 16-byte chunk c of row r sits at chunk position c ^ ((r >> 1) & 7), so
 // that the operand reads of 16 consecutive rows fall on distinct banks; a
 // lane fetches the global chunk that belongs at the position it writes. Rows
 // past N or M and chunks past K read zeros (their offset is past the buffer).
+// One 16x16x128 MFMA is a whole group of a tile, so its result is scaled and
+// added (4 FMAs a lane) while the next row tile's MFMAs run.
 // kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
 template <int WN, int WM, int TN, int TM, bool kWide>
 __global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
     const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
     int tiles_n) {
-    constexpr int BN = 32 * WN * TN, BM = 32 * WM * TM, NW = WN * WM, kThreads = 64 * NW;
+    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, NW = WN * WM, kThreads = 64 * NW;
     using Stage = F8Stage<BN, BM>;
+    using Frag = std::conditional_t<kWide, F8Wide, F8Codes>;
     __shared__ __attribute__((aligned(16))) Stage st0;
     __shared__ __attribute__((aligned(16))) Stage st1;
     __shared__ __attribute__((aligned(16))) float bias_s[BN];
@@ -112,151 +143,154 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % WN;
     const int wm = wave / WN;
-    const int r32 = lane & 31;
-    const int lh = lane >> 5;
+    const int r16 = lane & 15;
+    const int q4 = lane >> 4;
     const int S = (K + kF8Block - 1) / kF8Block;
 
     const __amdgpu_buffer_rsrc_t ra = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(BN, N - n0) * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rb = fp8_rsrc(qx + (size_t)m0 * K, (uint32_t)min(BM, M - m0) * (uint32_t)K);
 
     // load j of a stage fills staged rows 8 j .. 8 j + 7 (the weights' rows
-    // first, then the activations'), lane l row 8 j + l / 8 at position l % 8
+    // first, then the activations'), lane l row 8 j + l / 8 at position l % 8;
+    // rows 8 j and 8 j + 16 share their chunk order
     constexpr int kLoads = (BN + BM) / 8 / NW;
-    uint32_t gbase[kLoads];
-    int gchunk[kLoads];
+    static_assert((BN / 8) % kLoads == 0 && kLoads % 2 == 0, "a wave loads pairs of rows of one operand");
+    const bool loads_a = wave * kLoads < BN / 8;
+    const int row0 = (loads_a ? wave * kLoads : wave * kLoads - BN / 8) * 8;
+    int gchunk[2];
+    uint32_t gbase[2];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int j = wave * kLoads + i;
-        const int r = (j < BN / 8 ? j : j - BN / 8) * 8 + lane / 8;
+    for (int i = 0; i < 2; ++i) {
+        const int r = row0 + 8 * i + lane / 8;
         gchunk[i] = ((lane % 8) ^ ((r >> 1) & 7)) * 16;
         gbase[i] = (uint32_t)r * (uint32_t)K + (uint32_t)gchunk[i];
     }
-    const bool loads_a = wave * kLoads < BN / 8;  // a wave's loads are all of one operand
-    static_assert((BN / 8) % kLoads == 0, "a wave loads one operand");
-    const int dst0 = (loads_a ? wave * kLoads : wave * kLoads - BN / 8) * 1024;
     auto issue_stage = [&](int s, Stage &st) __attribute__((always_inline)) {
         const int k0 = s * kF8Block;
-        const bool part = k0 + kF8Block > K;
-        uint8_t *dst = (loads_a ? st.a : st.b) + dst0;
+        uint8_t *dst = (loads_a ? st.a : st.b) + row0 * kF8Block;
+        uint32_t off[2];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            uint32_t off = gbase[i] + (uint32_t)k0;
-            if (part && k0 + gchunk[i] >= K) off = kF8Oob;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(loads_a ? ra : rb, (f8_lds_void *)(dst + i * 1024), 16, off, 0,
-                                                     0, 0);
-        }
+        for (int i = 0; i < 2; ++i) off[i] = k0 + gchunk[i] < K ? gbase[i] + (uint32_t)k0 : kF8Oob;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(loads_a ? ra : rb, (f8_lds_void *)(dst + i * 1024), 16,
+                                                     off[i & 1] + (uint32_t)(i / 2) * 16u * (uint32_t)K, 0, 0, 0);
     };
-    // a lane's operand of one half (64 k) of a group: chunks 4 h + lh and 4 h + 2 + lh of row r
-    auto frag = [&](const uint8_t *base, int r, int h) __attribute__((always_inline)) {
-        const int x = (r >> 1) & 7;
-        const u32x4 lo = *reinterpret_cast<const u32x4 *>(base + r * kF8Block + ((4 * h + lh) ^ x) * 16);
-        const u32x4 hi = *reinterpret_cast<const u32x4 *>(base + r * kF8Block + ((4 * h + 2 + lh) ^ x) * 16);
-        return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    // a lane's operand of row tile i: chunks q4 and 4 + q4 of row 16 i + l % 16
+    const int x = (r16 >> 1) & 7;
+    const int c_lo = r16 * kF8Block + (q4 ^ x) * 16, c_hi = r16 * kF8Block + ((4 + q4) ^ x) * 16;
+    auto read = [&](Frag &f, const uint8_t *base, int i) __attribute__((always_inline)) {
+        f.set(*reinterpret_cast<const u32x4 *>(base + i * 16 * kF8Block + c_lo),
+              *reinterpret_cast<const u32x4 *>(base + i * 16 * kF8Block + c_hi));
     };
 
-    f32x16 acc[TN][TM];
+    f32x4 acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int j = 0; j < TM; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+        for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // this wave's columns lie in one block of 128: one weight scale a group
-    const float *swr = sw + (size_t)((n0 + wn * 32 * TN) / kF8Block < (N + kF8Block - 1) / kF8Block
-                                         ? (n0 + wn * 32 * TN) / kF8Block
-                                         : 0) * S;
+    static_assert(kF8Block % (16 * TN) == 0, "a wave's columns lie in one block");
+    const int wblock = (n0 + wn * 16 * TN) / kF8Block;
+    const float *swr = sw + (size_t)(wblock < (N + kF8Block - 1) / kF8Block ? wblock : 0) * S;
     int mrow[TM];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) mrow[i] = min(m0 + (wm * TM + i) * 32 + r32, M - 1);
-    auto scales = [&](int s, float (&out)[TM]) __attribute__((always_inline)) {
-        const float w = swr[s];
+    for (int j = 0; j < TM; ++j) mrow[j] = min(m0 + (wm * TM + j) * 16 + r16, M - 1);
+    float raw[TM], raw_w, sc[TM];
+    auto load_scales = [&](int s) __attribute__((always_inline)) {
+        raw_w = swr[s];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) out[i] = sx[(size_t)s * M + mrow[i]] * w;
+        for (int j = 0; j < TM; ++j) raw[j] = sx[(size_t)s * M + mrow[j]];
     };
 
     for (int i = tid; i < BN; i += kThreads)
         bias_s[i] = bias && n0 + i < N ? bf16_bits_to_f32(bias[n0 + i]) : 0.0f;
     issue_stage(0, st0);
-    float sc[TM], sc_next[TM];
-    scales(0, sc);
+    load_scales(0);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
 
+    Frag fa[2], fb[TM];
+    f32x4 p[2][TM];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        p[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        sc[j] = 0.0f;
+        read(fb[j], st0.b, wm * TM + j);
+    }
+    read(fa[0], st0.a, wn * TN);
+    static_assert(TN % 2 == 0, "row tiles alternate between two sets");
+    // On entry: the operands of stage s's tokens and first row tile are being
+    // read, its scales are in raw, and the last row tile of stage s - 1 is in
+    // p[1], not yet scaled (sc: that stage's scales). Stages run in pairs
+    // without a branch: a stage past K loads zeros and adds none.
     auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
-        if (s + 1 < S) {
-            scales(s + 1, sc_next);
-            issue_stage(s + 1, nxt);
-        }
-        i32x8 b[TM][2];
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) b[j][h] = frag(cur.b, (wm * TM + j) * 32 + r32, h);
+        issue_stage(s + 1, nxt);
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
-            const int r = (wn * TN + i) * 32 + r32;
-            const i32x8 a0 = frag(cur.a, r, 0), a1 = frag(cur.a, r, 1);
+            if (i + 1 < TN) read(fa[(i + 1) & 1], cur.a, wn * TN + i + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                f32x16 p;
+            for (int j = 0; j < TM; ++j) p[i & 1][j] = Frag::product(fa[i & 1], fb[j]);
+            const int d = i == 0 ? TN - 1 : i - 1;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) p[e] = 0.0f;
-                if constexpr (kWide) {
-                    p = mfma_wide_32x32x64(a0, b[j][0], p);
-                    p = mfma_wide_32x32x64(a1, b[j][1], p);
-                } else {
-                    p = mfma_fp8_32x32x64(a0, b[j][0], p);
-                    p = mfma_fp8_32x32x64(a1, b[j][1], p);
-                }
+            for (int j = 0; j < TM; ++j)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(sc[j], p[e], acc[i][j][e]);
+                for (int e = 0; e < 4; ++e) acc[d][j][e] = __builtin_fmaf(sc[j], p[d & 1][j][e], acc[d][j][e]);
+            if (i == 0) {
+#pragma unroll
+                for (int j = 0; j < TM; ++j) sc[j] = raw[j] * raw_w;
+                load_scales(min(s + 1, S - 1));
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int j = 0; j < TM; ++j) sc[j] = sc_next[j];
-        // stage s + 1 has landed, and everyone is done with stage s
+        // stage s + 1 has landed, and everyone has read stage s
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
+#pragma unroll
+        for (int j = 0; j < TM; ++j) read(fb[j], nxt.b, wm * TM + j);
+        read(fa[0], nxt.a, wn * TN);
     };
-    int s = 0;
-    for (; s + 1 < S; s += 2) {
+    for (int s = 0; s < S; s += 2) {
         run_stage(s, st0, st1);
         run_stage(s + 1, st1, st0);
     }
-    if (s < S) run_stage(s, st0, st1);
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[TN - 1][j][e] = __builtin_fmaf(sc[j], p[1][j][e], acc[TN - 1][j][e]);
 
     // Output: 32 tokens x BN columns at a time through LDS (the waves of one
     // wm write, everyone stores whole row segments), alternating between the
     // two stages.
     constexpr int wide = kWide ? 4 : 2;
     constexpr int pitch = BN * wide + 16;
-    static_assert(sizeof(Stage) >= 32 * pitch, "LDS too small for the output tile");
+    static_assert(sizeof(Stage) >= 32 * pitch && TM % 2 == 0, "LDS too small for the output tile");
     constexpr int pieces = BN * wide / 16;  // 16-byte pieces of a row
 #pragma unroll
-    for (int p = 0; p < WM * TM; ++p) {
-        uint8_t *buf = reinterpret_cast<uint8_t *>((p & 1) ? &st1 : &st0);
-        if (wm == p / TM) {
+    for (int pass = 0; pass < WM * TM / 2; ++pass) {
+        uint8_t *buf = reinterpret_cast<uint8_t *>((pass & 1) ? &st1 : &st0);
+        if (wm == pass / (TM / 2)) {
 #pragma unroll
-            for (int i = 0; i < TN; ++i)
+            for (int i = 0; i < TN; ++i) {
+                const int nl = (wn * TN + i) * 16 + 4 * q4;
+                const f32x4 bv = *reinterpret_cast<const f32x4 *>(bias_s + nl);
 #pragma unroll
-                for (int qq = 0; qq < 4; ++qq) {
-                    const int nl = (wn * TN + i) * 32 + 8 * qq + 4 * lh;
-                    const f32x4 bv = *reinterpret_cast<const f32x4 *>(bias_s + nl);
-                    f32x4 v;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) v[t] = acc[i][p % TM][4 * qq + t] + bv[t];
+                for (int jj = 0; jj < 2; ++jj) {
+                    const f32x4 v = acc[i][pass % (TM / 2) * 2 + jj] + bv;
+                    uint8_t *to = buf + (jj * 16 + r16) * pitch + nl * wide;
                     if constexpr (kWide)
-                        *reinterpret_cast<f32x4 *>(buf + r32 * pitch + nl * 4) = v;
+                        *reinterpret_cast<f32x4 *>(to) = v;
                     else
-                        *reinterpret_cast<u32x2 *>(buf + r32 * pitch + nl * 2) =
-                            u32x2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
+                        *reinterpret_cast<u32x2 *>(to) = u32x2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
                 }
+            }
         }
         __syncthreads();
         for (int c = tid; c < 32 * pieces; c += kThreads) {
             const int row = c / pieces, piece = c % pieces;
-            const int m = m0 + 32 * p + row;
+            const int m = m0 + 32 * pass + row;
             const int64_t n = n0 + piece * (16 / wide);
             if (m < M && n < N)
                 *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(Y) + ((int64_t)m * N + n) * wide) =
@@ -366,7 +400,7 @@ hipError_t launch_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx,
 template <int WN, int WM, int TN, int TM, bool kWide>
 static hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                               const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
-    constexpr int BN = 32 * WN * TN, BM = 32 * WM * TM;
+    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM;
     const int tiles_n = (N + BN - 1) / BN, tiles_m = (M + BM - 1) / BM;
     hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, TN, TM, kWide>), dim3(tiles_n * tiles_m), dim3(64 * WN * WM), 0,
                        stream, qx, sx, qw, sw, bias, M, N, K, Y, tiles_n);
@@ -392,11 +426,11 @@ static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t 
     const int64_t big = (int64_t)((N + 255) / 256) * ((M + 255) / 256);
     if (big >= 128) {
         if constexpr (kWide)
-            return launch_tile<2, 2, 2, 2, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+            return launch_tile<2, 2, 4, 4, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
         else
-            return launch_tile<2, 4, 4, 2, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+            return launch_tile<2, 4, 8, 4, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     }
-    return launch_tile<2, 2, 1, 1, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+    return launch_tile<2, 2, 2, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
 }
 
 hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
