@@ -75,6 +75,7 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
 // ---- the product, many tokens ----------------------------------------------
 
 constexpr uint32_t kF8Oob = 0x80000000u;
+constexpr int kF8Cus = 256;  // compute units
 
 typedef __attribute__((address_space(3))) void f8_lds_void;
 
@@ -122,22 +123,13 @@ struct F8Wide {
 // One 16x16x128 MFMA is a whole group of a tile, so its result is scaled and
 // added (4 FMAs a lane) while the next row tile's MFMAs run.
 // kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
-template <int WN, int WM, int TN, int TM, bool kWide>
-__global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
-    const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
-    const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
-    int tiles_n) {
+template <int WN, int WM, int TN, int TM, bool kWide, class Stage>
+__device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, const uint8_t *__restrict__ qx,
+                                         const float *__restrict__ sx, const uint8_t *__restrict__ qw,
+                                         const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N,
+                                         int K, void *__restrict__ Y, int n0, int m0) {
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, NW = WN * WM, kThreads = 64 * NW;
-    using Stage = F8Stage<BN, BM>;
     using Frag = std::conditional_t<kWide, F8Wide, F8Codes>;
-    __shared__ __attribute__((aligned(16))) Stage st0;
-    __shared__ __attribute__((aligned(16))) Stage st1;
-    __shared__ __attribute__((aligned(16))) float bias_s[BN];
-
-    int tile_n, tile_m;
-    fp8_tile_of_block(blockIdx.x, gridDim.x, tiles_n, tile_n, tile_m);
-    const int n0 = tile_n * BN;
-    const int m0 = tile_m * BM;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -150,31 +142,36 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
     const __amdgpu_buffer_rsrc_t ra = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(BN, N - n0) * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rb = fp8_rsrc(qx + (size_t)m0 * K, (uint32_t)min(BM, M - m0) * (uint32_t)K);
 
-    // load j of a stage fills staged rows 8 j .. 8 j + 7 (the weights' rows
-    // first, then the activations'), lane l row 8 j + l / 8 at position l % 8;
-    // rows 8 j and 8 j + 16 share their chunk order
-    constexpr int kLoads = (BN + BM) / 8 / NW;
-    static_assert((BN / 8) % kLoads == 0 && kLoads % 2 == 0, "a wave loads pairs of rows of one operand");
-    const bool loads_a = wave * kLoads < BN / 8;
-    const int row0 = (loads_a ? wave * kLoads : wave * kLoads - BN / 8) * 8;
+    // Each wave loads kA KB of the weights' rows and kB of the activations':
+    // a load fills 8 staged rows r, r + 1, ... (lane l row r + l / 8 at chunk
+    // position l % 8), rows 16 apart share their chunk order
+    constexpr int kA = BN / 8 / NW, kB = BM / 8 / NW, kLoads = kA + kB;
+    static_assert(kA % 2 == 0 && kB % 2 == 0, "a wave loads pairs of 8 rows");
     int gchunk[2];
-    uint32_t gbase[2];
+    uint32_t ga[2], gb[2], oa[2], ob[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = row0 + 8 * i + lane / 8;
+        const int r = 8 * i + lane / 8;
         gchunk[i] = ((lane % 8) ^ ((r >> 1) & 7)) * 16;
-        gbase[i] = (uint32_t)r * (uint32_t)K + (uint32_t)gchunk[i];
+        ga[i] = (uint32_t)(wave * kA * 8 + r) * (uint32_t)K + (uint32_t)gchunk[i];
+        gb[i] = (uint32_t)(wave * kB * 8 + r) * (uint32_t)K + (uint32_t)gchunk[i];
     }
-    auto issue_stage = [&](int s, Stage &st) __attribute__((always_inline)) {
+    // offsets of stage s, and its load i into st
+    auto aim = [&](int s) __attribute__((always_inline)) {
         const int k0 = s * kF8Block;
-        uint8_t *dst = (loads_a ? st.a : st.b) + row0 * kF8Block;
-        uint32_t off[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) off[i] = k0 + gchunk[i] < K ? gbase[i] + (uint32_t)k0 : kF8Oob;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(loads_a ? ra : rb, (f8_lds_void *)(dst + i * 1024), 16,
-                                                     off[i & 1] + (uint32_t)(i / 2) * 16u * (uint32_t)K, 0, 0, 0);
+        for (int i = 0; i < 2; ++i) {
+            const bool in = k0 + gchunk[i] < K;
+            oa[i] = in ? ga[i] + (uint32_t)k0 : kF8Oob;
+            ob[i] = in ? gb[i] + (uint32_t)k0 : kF8Oob;
+        }
+    };
+    auto issue = [&](Stage &st, int i) __attribute__((always_inline)) {
+        const bool a = i < kA;
+        const int n = a ? i : i - kA;
+        uint8_t *dst = a ? st.a + (wave * kA + n) * 1024 : st.b + (wave * kB + n) * 1024;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? ra : rb, (f8_lds_void *)dst, 16,
+                                                 (a ? oa : ob)[n & 1] + (uint32_t)(n / 2) * 16u * (uint32_t)K, 0, 0, 0);
     };
     // a lane's operand of row tile i: chunks q4 and 4 + q4 of row 16 i + l % 16
     const int x = (r16 >> 1) & 7;
@@ -206,60 +203,98 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
 
     for (int i = tid; i < BN; i += kThreads)
         bias_s[i] = bias && n0 + i < N ? bf16_bits_to_f32(bias[n0 + i]) : 0.0f;
-    issue_stage(0, st0);
+    aim(0);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) issue(st0, i);
     load_scales(0);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
 
-    Frag fa[2], fb[TM];
-    f32x4 p[2][TM];
+    // kRing row tiles' operands in registers, tile i in slot i % kRing; the
+    // products of MFMA t of a stage (t = row tile * TM + token tile) in slot
+    // t % 4 of p, scaled and added kDelay MFMAs later
+    constexpr int kRing = TN % 4 == 0 && !kWide ? 4 : 2, kLate = kRing - 1, kDelay = TM >= 4 ? 3 : 2;
+    static_assert(TN % kRing == 0 && TN * TM % 4 == 0, "slots are the same in every stage");
+    Frag fa[kRing], fb[TM];
+    f32x4 p[4];
+    const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-        p[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         sc[j] = 0.0f;
-        read(fb[j], st0.b, wm * TM + j);
+        fb[j].set(zero, zero);
     }
-    read(fa[0], st0.a, wn * TN);
-    static_assert(TN % 2 == 0, "row tiles alternate between two sets");
-    // On entry: the operands of stage s's tokens and first row tile are being
-    // read, its scales are in raw, and the last row tile of stage s - 1 is in
-    // p[1], not yet scaled (sc: that stage's scales). Stages run in pairs
-    // without a branch: a stage past K loads zeros and adds none.
-    auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
-        issue_stage(s + 1, nxt);
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            if (i + 1 < TN) read(fa[(i + 1) & 1], cur.a, wn * TN + i + 1);
-            __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < kRing; ++i) fa[i].set(zero, zero);
 #pragma unroll
-            for (int j = 0; j < TM; ++j) p[i & 1][j] = Frag::product(fa[i & 1], fb[j]);
-            const int d = i == 0 ? TN - 1 : i - 1;
+    for (int t = 0; t < 4; ++t) p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int t) __attribute__((always_inline)) {
+        const int i = t / TM, j = t % TM;
 #pragma unroll
-            for (int j = 0; j < TM; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[d][j][e] = __builtin_fmaf(sc[j], p[d & 1][j][e], acc[d][j][e]);
-            if (i == 0) {
-#pragma unroll
-                for (int j = 0; j < TM; ++j) sc[j] = raw[j] * raw_w;
-                load_scales(min(s + 1, S - 1));
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        // stage s + 1 has landed, and everyone has read stage s
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(sc[j], p[t % 4][e], acc[i][j][e]);
+    };
+    auto multiply = [&](int i, int j) __attribute__((always_inline)) {
+        const int t = i * TM + j;
+        __builtin_amdgcn_sched_barrier(0);
+        add((t + TN * TM - kDelay) % (TN * TM));
+        __builtin_amdgcn_s_setprio(1);
+        p[t % 4] = Frag::product(fa[i % kRing], fb[j]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // stage s has landed and everyone has read stage s - 1
+    auto next_stage = [&]() __attribute__((always_inline)) {
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
+    };
+    // The last kLate row tiles of stage s - 1 are multiplied after the barrier
+    // that opens stage s, from operands read before it, so that stage s's
+    // first operands are read under their MFMAs: a token tile's as soon as
+    // its last MFMA has issued. The loads of stage s + 1 are spread over the
+    // MFMAs, TM / 2 apart (issued together they block the wave until the
+    // load unit has taken them all: 5 % slower at 32760 x 5120 x 5120). Stages
+    // run in pairs without a branch: a stage past K loads zeros and adds none.
+    static_assert(2 * TN >= kLoads, "the loads of a stage fit between its MFMAs");
+    auto load_before = [&](Stage &nxt, int u) __attribute__((always_inline)) {
+        if (u % (TM / 2) == 0 && u / (TM / 2) < kLoads) issue(nxt, u / (TM / 2));
+    };
+    auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
+        next_stage();
+        aim(s + 1);
+        read(fa[0], cur.a, wn * TN);
 #pragma unroll
-        for (int j = 0; j < TM; ++j) read(fb[j], nxt.b, wm * TM + j);
-        read(fa[0], nxt.a, wn * TN);
+        for (int r = 0; r < kLate; ++r) {
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                load_before(nxt, r * TM + j);
+                multiply(TN - kLate + r, j);
+                if (r == kLate - 1) read(fb[j], cur.b, wm * TM + j);
+            }
+            read(fa[r + 1], cur.a, wn * TN + r + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < TN - kLate; ++i) {
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                load_before(nxt, (kLate + i) * TM + j);
+                multiply(i, j);
+                if (i * TM + j == kDelay - 1) {  // stage s - 1 is all added
+#pragma unroll
+                    for (int k = 0; k < TM; ++k) sc[k] = raw[k] * raw_w;
+                    load_scales(min(s + 1, S - 1));
+                }
+            }
+            if (i + kRing < TN) read(fa[i % kRing], cur.a, wn * TN + i + kRing);
+        }
     };
     for (int s = 0; s < S; s += 2) {
         run_stage(s, st0, st1);
         run_stage(s + 1, st1, st0);
     }
 #pragma unroll
-    for (int j = 0; j < TM; ++j)
+    for (int r = 0; r < kLate; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[TN - 1][j][e] = __builtin_fmaf(sc[j], p[1][j][e], acc[TN - 1][j][e]);
+        for (int j = 0; j < TM; ++j) multiply(TN - kLate + r, j);
+#pragma unroll
+    for (int t = TN * TM - kDelay; t < TN * TM; ++t) add(t);
+    next_stage();
 
     // Output: 32 tokens x BN columns at a time through LDS (the waves of one
     // wm write, everyone stores whole row segments), alternating between the
@@ -296,6 +331,43 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
                 *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(Y) + ((int64_t)m * N + n) * wide) =
                     *reinterpret_cast<const u32x4 *>(buf + row * pitch + piece * 16);
         }
+    }
+}
+
+template <int WN, int WM, int TN, int TM, bool kWide>
+__global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
+    const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
+    const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
+    int tiles_n) {
+    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM;
+    __shared__ __attribute__((aligned(16))) F8Stage<BN, BM> st0;
+    __shared__ __attribute__((aligned(16))) F8Stage<BN, BM> st1;
+    __shared__ __attribute__((aligned(16))) float bias_s[BN];
+    int tile_n, tile_m;
+    fp8_tile_of_block(blockIdx.x, gridDim.x, gridDim.x, tiles_n, tile_n, tile_m);
+    fp8_tile<WN, WM, TN, TM, kWide>(st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * BN, tile_m * BM);
+}
+
+// 256 x 256 tiles, of which the grid's first `whole` blocks take one each; two
+// blocks share each of the others (128 of its tokens each).
+__global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
+    const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
+    const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
+    int tiles_n, int tiles, int whole) {
+    __shared__ __attribute__((aligned(16))) F8Stage<256, 256> st0;
+    __shared__ __attribute__((aligned(16))) F8Stage<256, 256> st1;
+    __shared__ __attribute__((aligned(16))) float bias_s[256];
+    int tile_n, tile_m;
+    const int b = blockIdx.x;
+    if (b < whole) {
+        fp8_tile_of_block(b, whole, tiles, tiles_n, tile_n, tile_m);
+        fp8_tile<2, 4, 8, 4, false>(st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256, tile_m * 256);
+    } else {
+        const int id = whole + (b - whole) / 2, m0_half = (b - whole) % 2 * 128;
+        fp8_tile_at(id, tiles, tiles_n, tile_n, tile_m);
+        if (tile_m * 256 + m0_half < M)
+            fp8_tile<4, 2, 4, 4, false>(st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256,
+                                        tile_m * 256 + m0_half);
     }
 }
 
@@ -424,11 +496,17 @@ static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t 
         return hipGetLastError();
     }
     const int64_t big = (int64_t)((N + 255) / 256) * ((M + 255) / 256);
-    if (big >= 128) {
-        if constexpr (kWide)
+    if (big >= 96) {
+        if constexpr (kWide) {
             return launch_tile<2, 2, 4, 4, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
-        else
-            return launch_tile<2, 4, 8, 4, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+        } else {
+            const int tiles_n = (N + 255) / 256, tiles = (int)big;
+            const int rest = tiles % kF8Cus;
+            const int split = rest <= kF8Cus / 2 ? rest : 0;
+            hipLaunchKernelGGL(fp8_gemm256_kernel, dim3(tiles + split), dim3(512), 0, stream, qx, sx, qw, sw, bias, M,
+                               N, K, Y, tiles_n, tiles, tiles - split);
+            return hipGetLastError();
+        }
     }
     return launch_tile<2, 2, 2, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
 }

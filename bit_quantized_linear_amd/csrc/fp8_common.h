@@ -75,19 +75,24 @@ __device__ __forceinline__ u32x2 fp8_codes8(u32x4 v, float r) {
     return out;
 }
 
-// Blocks are dealt to the 8 XCDs round-robin (block b runs on XCD b % 8): XCD
-// c takes a contiguous tile range, walked four token tiles at a time across
-// the columns, so that the tiles an XCD runs together share operand rows in
-// its L2. With T tiles the first T % 8 XCDs have one tile more.
-__device__ __forceinline__ void fp8_tile_of_block(int b, int T, int tiles_n, int &tile_n, int &tile_m) {
-    const int x = b % 8, per = T / 8, more = T % 8;
-    const int id = x * per + min(x, more) + b / 8;
-    const int tiles_m = T / tiles_n;
+// Tile number id of `tiles`: four token tiles at a time across the columns.
+__device__ __forceinline__ void fp8_tile_at(int id, int tiles, int tiles_n, int &tile_n, int &tile_m) {
+    const int tiles_m = tiles / tiles_n;
     const int group = id / (4 * tiles_n);
     const int gm = min(4, tiles_m - group * 4);
     const int in_group = id - group * 4 * tiles_n;
     tile_m = group * 4 + in_group % gm;
     tile_n = in_group / gm;
+}
+
+// The tile of block b of the first `blocks`. Blocks are dealt to the 8 XCDs
+// round-robin (block b runs on XCD b % 8): XCD c takes a contiguous range of
+// tile numbers, so that the tiles an XCD runs together share operand rows in
+// its L2. The first blocks % 8 XCDs have one tile more.
+__device__ __forceinline__ void fp8_tile_of_block(int b, int blocks, int tiles, int tiles_n, int &tile_n,
+                                                  int &tile_m) {
+    const int x = b % 8, per = blocks / 8, more = blocks % 8;
+    fp8_tile_at(x * per + min(x, more) + b / 8, tiles, tiles_n, tile_n, tile_m);
 }
 
 }  // namespace svdq
