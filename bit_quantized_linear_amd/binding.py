@@ -168,6 +168,9 @@ def _stream(stream):
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
 
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:  # the same handle without a Stream object: 0.4 us a call instead of 3.0
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
