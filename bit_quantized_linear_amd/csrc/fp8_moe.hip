@@ -7,11 +7,11 @@
 //   h[t, j] = silu(X[t] Wg) * (X[t] Wu) of expert e = idx[t, j]
 //   Y[t]    = sum_j w[t, j] (h[t, j] Wd), rounded once to bf16
 //
-// Launches: the router's logits; with more than kRouteInUp tokens one block
-// that makes the choices and the lists of the reached experts; the gate and up
-// projections, one block per reached expert and 16 intermediate columns; the
-// down projection with the weighted sum, one block per 16 output columns. Each
-// reached expert's weights are read once, so the layer is bound by HBM.
+// Launches: the router's logits; the choices (where the up kernel's blocks do
+// not make them themselves); the gate and up projections, one block per reached
+// expert and 16 intermediate columns; the down projection with the weighted
+// sum, one block per 16 output columns. Each reached expert's weights are read
+// once, so the layer is bound by HBM.
 
 #include <hip/hip_runtime.h>
 
@@ -29,8 +29,6 @@ constexpr int kUpThreads = 512;
 constexpr int kUpWaves = kUpThreads / 64;
 constexpr int kDownThreads = 1024;
 constexpr int kDownWaves = kDownThreads / 64;
-constexpr int kRouteThreads = 1024;
-constexpr int kRouteInUp = kUpWaves;  // tokens that the up kernel's blocks route themselves, one per wave
 constexpr int kMaxPairs = SVDQ_FP8_MOE_MAX_TOKENS * SVDQ_FP8_MOE_MAX_TOP_K;
 constexpr uint32_t kMoeOob = 0x80000000u;
 
@@ -41,13 +39,13 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) 
 // ---- router logits -----------------------------------------------------------
 
 constexpr int kLogitWaves = 4;
-constexpr int kLogitExperts = 4;  // per block
+constexpr int kLogitExperts = 2;  // per block
 
-// One block: 4 experts x TB tokens; its waves take steps of 512 features in
-// turn, a lane 8 of them. bf16 values are widened to fp64 and multiplied and
-// added there, so that the order of two logits is the exact one up to 2^-50.
-// The lanes' sums are folded together so that each step halves the sums a lane
-// holds (TB 4 - 1 exchanges instead of 6 TB 4), the waves' through LDS.
+// One block: 2 experts x TB tokens; its waves take steps of 512 features in
+// turn, 8 a lane. bf16 values are widened to fp64 and multiplied and added
+// there, so that the order of two logits is the exact one up to 2^-50. The
+// lanes' sums are folded so that each step halves the sums a lane holds, the
+// waves' added in LDS in order.
 template <int TB>
 __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits_kernel(const uint16_t *__restrict__ X,
                                                                       const uint16_t *__restrict__ wr, int T, int H,
@@ -59,7 +57,8 @@ __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits_kernel(const uint
     double sum[kSums];
 #pragma unroll
     for (int i = 0; i < kSums; ++i) sum[i] = 0.0;
-    for (int h = wave * 512 + lane * 8; h < H; h += kLogitWaves * 512) {
+#pragma unroll 2
+    for (int h = (wave * 64 + lane) * 8; h < H; h += 512 * kLogitWaves) {
         u32x4 w[kLogitExperts], x[TB];
 #pragma unroll
         for (int i = 0; i < kLogitExperts; ++i)
@@ -84,22 +83,23 @@ __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits_kernel(const uint
             }
         }
     }
-    // after the steps with n sums left a lane holds those of its own low bits
-    int n = kSums, d = 32;
+    // fold: lanes with bit 32 / n of the number of sums left keep the upper half
 #pragma unroll
-    for (; n > 1 && d > 0; n >>= 1, d >>= 1) {
-        const bool up = lane & d;
+    for (int step = 0; step < 6; ++step) {
+        const int n = kSums >> step, d = 32 >> step;
+        if (n > 1) {
+            const bool up = lane & d;
 #pragma unroll
-        for (int i = 0; i < n / 2; ++i) {
-            const double give = up ? sum[i] : sum[i + n / 2], keep = up ? sum[i + n / 2] : sum[i];
-            sum[i] = keep + __shfl_xor(give, d);
+            for (int i = 0; i < n / 2; ++i) {
+                const double give = up ? sum[i] : sum[i + n / 2], keep = up ? sum[i + n / 2] : sum[i];
+                sum[i] = keep + __shfl_xor(give, d);
+            }
+        } else {
+            sum[0] += __shfl_xor(sum[0], d);
         }
     }
-#pragma unroll
-    for (; d > 0; d >>= 1) sum[0] += __shfl_xor(sum[0], d);
-    // lane l holds sum number (its top log2 kSums bits)
-    constexpr int kShift = 64 / kSums;
-    if (lane % kShift == 0) part[wave][lane / kShift] = sum[0];
+    constexpr int kLanes = 64 / kSums;  // lanes that hold the same sum
+    if (lane % kLanes == 0) part[wave][lane / kLanes] = sum[0];
     __syncthreads();
     if (threadIdx.x < kSums) {
         double v = 0.0;
@@ -112,352 +112,478 @@ __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits_kernel(const uint
 
 // ---- the choice ----------------------------------------------------------------
 
-// One wave: the top_k largest of a token's logits and their softmax weights.
-// Lane l holds experts l, l + 64, ...; top_k rounds of a wave-wide maximum over
-// (logit, lowest expert), each expert chosen at most once whatever its logit;
-// NaN orders below every number. idx and gate may be in LDS.
-__device__ __forceinline__ void choose(const double *__restrict__ logit, int E, int top_k, bool renorm, int lane,
-                                       int32_t *idx, float *gate) {
-    constexpr int kPer = SVDQ_FP8_MOE_MAX_EXPERTS / 64;
-    constexpr double kLowest = -1.7976931348623157e308;
-    double raw[kPer], v[kPer];
-    bool open[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        open[i] = lane + 64 * i < E;
-        raw[i] = open[i] ? logit[lane + 64 * i] : kLowest;
-        v[i] = raw[i] >= kLowest ? raw[i] : kLowest;  // NaN, -inf
+// NaN and -inf order below every number, alike.
+__device__ __forceinline__ double order_key(double l) { return l > -__builtin_inf() ? l : -__builtin_inf(); }
+
+// The place of expert e among its token's: how many have a larger logit, or
+// the same and a lower number. A permutation, so the first top_k places are
+// the choice, in order, with no rounds that wait for each other.
+__device__ __forceinline__ int place(const double *key, int E, int e) {
+    const double mine = key[e];
+    int before = 0;
+#pragma unroll 4
+    for (int o = 0; o < E; ++o) {
+        const double v = key[o];
+        before += v > mine || (v == mine && o < e) ? 1 : 0;
     }
-    double top = 0.0;
-    float chosen = 0.0f, mine = 0.0f;
-    int mine_e = 0;
-    for (int j = 0; j < top_k; ++j) {
-        double best = kLowest, best_raw = 0.0;
-        int at = 1 << 30;
+    return before;
+}
+
+// Weight numerators of a token's choices, in fp32: exp(l - largest l).
+__device__ __forceinline__ float numerator(double l, double top) { return expf((float)(l - top)); }
+
+// The weights' denominator: the sum of the chosen numerators in order, or of
+// all experts' (a wave's lanes take experts l, l + 64, ... and are folded).
+__device__ __forceinline__ float all_numerators(const double *logit, double top, int E, int lane) {
+    float sum = 0.0f;
+    for (int o = lane; o < E; o += 64) sum += numerator(logit[o], top);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (open[i] && (at == 1 << 30 || v[i] > best)) {
-                best = v[i];
-                best_raw = raw[i];
-                at = lane + 64 * i;
-            }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) {
-            const double ob = __shfl_xor(best, d);
-            const int oa = __shfl_xor(at, d);
-            if (oa != 1 << 30 && (at == 1 << 30 || ob > best || (ob == best && oa < at))) {
-                best = ob;
-                at = oa;
-            }
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    return sum;
+}
+
+// The choices of `tokens` tokens by one block (a thread per token and expert
+// at a time, then a wave per token): idx and gate [tokens][top_k], which may be
+// in LDS. logit, key and first are LDS of the block: [tokens][E], [tokens][E],
+// [tokens][top_k].
+__device__ __forceinline__ void choose(const double *__restrict__ logits, int tokens, int E, int top_k, bool renorm,
+                                       int threads, double *logit, double *key, int32_t *first, int32_t *idx,
+                                       float *gate) {
+    for (int i = threadIdx.x; i < tokens * E; i += threads) {
+        logit[i] = logits[i];
+        key[i] = order_key(logit[i]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < tokens * E; i += threads) {
+        const int t = i / E, e = i % E;
+        const int j = place(key + t * E, E, e);
+        if (j < top_k) first[t * top_k + j] = e;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 63;
+    for (int t = threadIdx.x >> 6; t < tokens; t += threads / 64) {
+        const double *l = logit + t * E;
+        const int32_t *f = first + t * top_k;
+        const double top = l[f[0]];
+        float total = 0.0f;
+        if (renorm)
+            for (int j = 0; j < top_k; ++j) total += numerator(l[f[j]], top);
+        else
+            total = all_numerators(l, top, E, lane);
+        if (lane < top_k) {
+            idx[t * top_k + lane] = f[lane];
+            gate[t * top_k + lane] = numerator(l[f[lane]], top) / total;
         }
-        best_raw = __shfl(best_raw, at & 63);  // the winner is its lane's own best
-        if (j == 0) top = best_raw;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (at == lane + 64 * i) open[i] = false;
-        const float e = expf((float)(best_raw - top));
-        chosen += e;
-        if (lane == j) {
-            mine = e;
-            mine_e = at;
-        }
-    }
-    float total = chosen;
-    if (!renorm) {
-        total = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 64 * i < E) total += expf((float)(raw[i] - top));
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d);
-    }
-    if (lane < top_k) {
-        idx[lane] = mine_e;
-        gate[lane] = mine / total;
     }
 }
 
-// The reached experts of a batch, ascending, each with its pairs t top_k + j,
-// ascending.
-struct MoeLists {
-    int32_t *reached;  // [1] how many
-    int32_t *experts;  // [reached]
-    int32_t *counts;   // [reached]
-    int32_t *pairs;    // [reached][T]
+constexpr int kRouteThreads = 256;
+
+// One block per token.
+__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *__restrict__ logits, int E, int top_k,
+                                                                  int renorm, int32_t *__restrict__ idx,
+                                                                  float *__restrict__ gate) {
+    __shared__ double logit[SVDQ_FP8_MOE_MAX_EXPERTS], key[SVDQ_FP8_MOE_MAX_EXPERTS];
+    __shared__ int32_t first[SVDQ_FP8_MOE_MAX_TOP_K];
+    const int t = blockIdx.x;
+    choose(logits + (size_t)t * E, 1, E, top_k, renorm, kRouteThreads, logit, key, first, idx + (size_t)t * top_k,
+           gate + (size_t)t * top_k);
+}
+
+// Up to this many (token, expert) pairs the up kernel's blocks make the choices
+// themselves, a thread per pair.
+constexpr int kRouteInUp = 128;
+
+// ---- the reached experts ---------------------------------------------------------
+
+// The reached experts in ascending order and the pairs t top_k + j sorted by
+// expert, then token: reached expert number a has pairs pair[from[a]] ..
+// pair[from[a + 1] - 1]. Written down for the down projection as it is.
+struct MoeTable {
+    int32_t reached;
+    uint16_t expert[SVDQ_FP8_MOE_MAX_EXPERTS];
+    uint16_t from[SVDQ_FP8_MOE_MAX_EXPERTS + 2];
+    uint16_t pair[kMaxPairs];
 };
+static_assert(sizeof(MoeTable) % 4 == 0, "copied in dwords");
 
-// The a-th reached expert, or -1, and the number of reached ones, from a bit
-// per expert.
-__device__ __forceinline__ int reached_expert(const uint32_t *bits, int a, int &reached) {
-    int e = -1;
-    reached = 0;
+// Built by a whole block from the choices. tokens: [256] of LDS, the set of an
+// expert's tokens as a bit each; an expert is at most once among a token's
+// choices, so a pair's place is the number of its expert's earlier tokens.
+__device__ __forceinline__ void build_table(const int32_t *idx, int T, int E, int top_k, int threads,
+                                            unsigned long long *tokens, MoeTable &table) {
+    static_assert(SVDQ_FP8_MOE_MAX_TOKENS <= 64, "a bit per token");
+    const int lane = threadIdx.x & 63;
+    for (int e = threadIdx.x; e < SVDQ_FP8_MOE_MAX_EXPERTS; e += threads) tokens[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < T * top_k; p += threads) atomicOr(&tokens[idx[p]], 1ull << (p / top_k));
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        int reached = 0, start = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int n = __popcll(tokens[e0 + lane]);
+            int sum = n;  // of the experts up to this one
 #pragma unroll
-    for (int i = 0; i < SVDQ_FP8_MOE_MAX_EXPERTS / 32; ++i) {
-        uint32_t w = bits[i];
-        const int c = __popc(w);
-        if (e < 0 && a < reached + c) {
-            for (int skip = a - reached; skip > 0; --skip) w &= w - 1;
-            e = 32 * i + __ffs((int)w) - 1;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(sum, d);
+                if (lane >= d) sum += o;
+            }
+            const uint64_t hit = __ballot(n > 0);
+            if (n > 0) {
+                const int a = reached + __popcll(hit & ((1ull << lane) - 1));
+                table.expert[a] = (uint16_t)(e0 + lane);
+                table.from[a] = (uint16_t)(start + sum - n);
+            }
+            reached += __popcll(hit);
+            start += __shfl(sum, 63);
         }
-        reached += c;
-    }
-    return e;
-}
-
-// One wave: the pairs of expert e, in order; their number.
-__device__ __forceinline__ int collect_pairs(const int32_t *idx, int pairs, int e, int lane, int32_t *list) {
-    int n = 0;
-    for (int p0 = 0; p0 < pairs; p0 += 64) {
-        const bool hit = p0 + lane < pairs && idx[p0 + lane] == e;
-        const uint64_t mask = __ballot(hit);
-        if (hit) list[n + __popcll(mask & ((1ull << lane) - 1))] = p0 + lane;
-        n += __popcll(mask);
-    }
-    return n;
-}
-
-// One block for a batch of more than kRouteInUp tokens: the choices, one wave
-// per token at a time, and the lists, one wave per reached expert.
-__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *__restrict__ logits, int T, int E,
-                                                                  int top_k, int renorm, int32_t *__restrict__ idx,
-                                                                  float *__restrict__ gate, MoeLists lists) {
-    __shared__ int32_t idx_s[kMaxPairs];
-    __shared__ uint32_t bits[SVDQ_FP8_MOE_MAX_EXPERTS / 32];
-    constexpr int kWaves = kRouteThreads / 64;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int pairs = T * top_k;
-    if (threadIdx.x < SVDQ_FP8_MOE_MAX_EXPERTS / 32) bits[threadIdx.x] = 0u;
-    for (int t = wave; t < T; t += kWaves)
-        choose(logits + (size_t)t * E, E, top_k, renorm, lane, idx_s + t * top_k, gate + t * top_k);
-    __syncthreads();
-    if ((int)threadIdx.x < pairs) {
-        const int e = idx_s[threadIdx.x];
-        idx[threadIdx.x] = e;
-        atomicOr(&bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    static_assert(kMaxPairs <= kRouteThreads, "a thread per pair");
-    int reached;
-    reached_expert(bits, 0, reached);
-    for (int a = wave; a < reached; a += kWaves) {
-        int n;
-        const int e = reached_expert(bits, a, n);
-        n = collect_pairs(idx_s, pairs, e, lane, lists.pairs + (size_t)a * T);
         if (lane == 0) {
-            lists.experts[a] = e;
-            lists.counts[a] = n;
+            table.from[reached] = (uint16_t)start;
+            table.reached = reached;
         }
     }
-    if (threadIdx.x == 0) *lists.reached = reached;
+    __syncthreads();
+    // a thread per reached expert and token
+    for (int i = threadIdx.x; i < table.reached * T; i += threads) {
+        const int a = i / T, t = i % T, e = table.expert[a];
+        const uint64_t set = tokens[e];
+        if (set >> t & 1) {
+            int j = 0;
+            while (idx[t * top_k + j] != e) ++j;  // it is there
+            table.pair[table.from[a] + __popcll(set & ((1ull << t) - 1))] = (uint16_t)(t * top_k + j);
+        }
+    }
+    __syncthreads();
 }
 
 // ---- gate and up projections ------------------------------------------------
 
-constexpr int kUpAhead = 4;  // groups of weights in flight per wave
+constexpr int kUpBlocks = 256;  // one per compute unit
+constexpr int kUpRing = 3;      // steps under way per wave
 
-// One block: the a-th reached expert, 16 intermediate columns of gate and up.
-// The waves take the groups of H in turn, their weights straight from global
-// memory into the operands of the bf16 MFMA (an E4M3 value is exact in bf16),
-// and add their sums in LDS. h is written as the sum of two bf16 numbers (hi +
-// lo, 16 significant bits), so that its rounding stays far below that of Y.
-// kRoute: few tokens; every block makes the choices itself (one wave per
-// token), which saves a launch, and the blocks of column tile 0 write the
-// choices and lists down.
+// Blocks take items in turn: a reached expert and 16 intermediate columns of
+// gate and up. The waves share H, a group each per step, and add their sums in
+// LDS at an item's end. Weights and activations go straight from global memory
+// into the operands of the bf16 MFMA (an E4M3 value is exact in bf16), kUpRing
+// steps ahead of their use and across items, so that loads are under way all
+// the time. h is written as the sum of two bf16 numbers (hi + lo, 16
+// significant bits), so that its rounding stays far below that of Y. kRoute:
+// every block also makes the choices, which saves a launch. Block 0 writes the
+// table down for the down projection.
 template <bool kRoute>
 __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     const uint16_t *__restrict__ X, const uint8_t *__restrict__ w13, const float *__restrict__ s13,
     const double *__restrict__ logits, int32_t *__restrict__ idx, float *__restrict__ gate, int T, int H, int I, int E,
-    int top_k, int renorm, uint16_t *__restrict__ h_hi, uint16_t *__restrict__ h_lo, MoeLists lists) {
-    __shared__ int32_t list[SVDQ_FP8_MOE_MAX_TOKENS];
-    __shared__ f32x4 red[kUpWaves][2][64];
+    int top_k, int renorm, uint16_t *__restrict__ h_hi, uint16_t *__restrict__ h_lo, MoeTable *__restrict__ table_out) {
+    __shared__ f32x4 red[2][kUpWaves][2][64];
+    __shared__ unsigned long long tokens[SVDQ_FP8_MOE_MAX_EXPERTS];
+    __shared__ MoeTable table;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int a = blockIdx.y;
-    const int i0 = blockIdx.x * 16;
-    int e, count;
-    if constexpr (kRoute) {
-        __shared__ int32_t idx_s[kRouteInUp * SVDQ_FP8_MOE_MAX_TOP_K];
-        __shared__ float gate_s[kRouteInUp * SVDQ_FP8_MOE_MAX_TOP_K];
-        __shared__ uint32_t bits[SVDQ_FP8_MOE_MAX_EXPERTS / 32];
-        const int pairs = T * top_k;
-        if (threadIdx.x < SVDQ_FP8_MOE_MAX_EXPERTS / 32) bits[threadIdx.x] = 0u;
-        if (wave < T)
-            choose(logits + (size_t)wave * E, E, top_k, renorm, lane, idx_s + wave * top_k, gate_s + wave * top_k);
-        __syncthreads();
-        static_assert(kRouteInUp * SVDQ_FP8_MOE_MAX_TOP_K <= kUpThreads, "a thread per pair");
-        if ((int)threadIdx.x < pairs) {
-            const int ei = idx_s[threadIdx.x];
-            atomicOr(&bits[ei >> 5], 1u << (ei & 31));
-            if (blockIdx.x == 0 && a == 0) {
-                idx[threadIdx.x] = ei;
-                gate[threadIdx.x] = gate_s[threadIdx.x];
-            }
-        }
-        __syncthreads();
-        int reached;
-        e = __builtin_amdgcn_readfirstlane(reached_expert(bits, a, reached));
-        if (blockIdx.x == 0 && a == 0 && threadIdx.x == 0) *lists.reached = reached;
-        if (e < 0) return;  // the same for every thread of the block
-        // every wave writes the same list
-        count = __builtin_amdgcn_readfirstlane(collect_pairs(idx_s, pairs, e, lane, list));
-        if (blockIdx.x == 0 && wave == 0) {
-            if (lane < count) lists.pairs[(size_t)a * T + lane] = list[lane];
-            if (lane == 0) {
-                lists.experts[a] = e;
-                lists.counts[a] = count;
-            }
-        }
-    } else {
-        if (a >= *lists.reached) return;
-        e = __builtin_amdgcn_readfirstlane(lists.experts[a]);
-        count = __builtin_amdgcn_readfirstlane(lists.counts[a]);
-        if ((int)threadIdx.x < count) list[threadIdx.x] = lists.pairs[(size_t)a * T + threadIdx.x];
-    }
-    __syncthreads();
     const int r16 = lane & 15, q4 = lane >> 4;
-    const int G = (H + kF8Block - 1) / kF8Block, gi = (I + kF8Block - 1) / kF8Block;
-    const uint8_t *we = w13 + (size_t)e * 2 * I * H;
-    const __amdgpu_buffer_rsrc_t rg = fp8_rsrc(we + (size_t)i0 * H, 16u * (uint32_t)H);
-    const __amdgpu_buffer_rsrc_t ru = fp8_rsrc(we + (size_t)(I + i0) * H, 16u * (uint32_t)H);
-    const float *sg = s13 + ((size_t)e * 2 * gi + i0 / kF8Block) * G;
-    const float *su = sg + (size_t)gi * G;
-    const uint32_t row = (uint32_t)r16 * (uint32_t)H;
-    for (int m0 = 0; m0 < count; m0 += 16) {
-        const uint16_t *x = X + (size_t)(list[min(m0 + r16, count - 1)] / top_k) * H;
-        f32x4 accg = {0.f, 0.f, 0.f, 0.f}, accu = accg;
-        for (int g0 = wave; g0 < G; g0 += kUpWaves * kUpAhead) {
-            u32x4 cg[kUpAhead][2], cu[kUpAhead][2];
-#pragma unroll
-            for (int n = 0; n < kUpAhead; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int k = (g0 + n * kUpWaves) * kF8Block + 64 * i + 16 * q4;
-                    const uint32_t off = k < H ? row + (uint32_t)k : kMoeOob;  // zeros past H
-                    cg[n][i] = load16(rg, off);
-                    cu[n][i] = load16(ru, off);
-                }
-#pragma unroll
-            for (int n = 0; n < kUpAhead; ++n) {
-                const int g = g0 + n * kUpWaves;
-                if (g >= G) break;
-                f32x4 pg = {0.f, 0.f, 0.f, 0.f}, pu = pg;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int k = g * kF8Block + 64 * i + 16 * q4;
-                    u32x4 x0 = {0u, 0u, 0u, 0u}, x1 = x0;
-                    if (k < H) {
-                        x0 = *reinterpret_cast<const u32x4 *>(x + k);
-                        x1 = *reinterpret_cast<const u32x4 *>(x + k + 8);
-                    }
-                    const bf16x8 b0 = __builtin_bit_cast(bf16x8, x0), b1 = __builtin_bit_cast(bf16x8, x1);
-                    pg = mfma_bf16_16x16x32(fp8_widen8(cg[n][i][0], cg[n][i][1]), b0, pg);
-                    pu = mfma_bf16_16x16x32(fp8_widen8(cu[n][i][0], cu[n][i][1]), b0, pu);
-                    pg = mfma_bf16_16x16x32(fp8_widen8(cg[n][i][2], cg[n][i][3]), b1, pg);
-                    pu = mfma_bf16_16x16x32(fp8_widen8(cu[n][i][2], cu[n][i][3]), b1, pu);
-                }
-                const float wg = sg[g], wu = su[g];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    accg[i] = __builtin_fmaf(wg, pg[i], accg[i]);
-                    accu[i] = __builtin_fmaf(wu, pu[i], accu[i]);
-                }
-            }
-        }
-        if (m0) __syncthreads();  // the sums of the tokens before have been read
-        red[wave][0][lane] = accg;
-        red[wave][1][lane] = accu;
+    if constexpr (kRoute) {
+        __shared__ double logit[kRouteInUp], key[kRouteInUp];
+        __shared__ int32_t first[kRouteInUp], idx_s[kRouteInUp];
+        __shared__ float gate_s[kRouteInUp];
+        choose(logits, T, E, top_k, renorm, kUpThreads, logit, key, first, idx_s, gate_s);
         __syncthreads();
+        if (blockIdx.x == 0 && (int)threadIdx.x < T * top_k) {
+            idx[threadIdx.x] = idx_s[threadIdx.x];
+            gate[threadIdx.x] = gate_s[threadIdx.x];
+        }
+        build_table(idx_s, T, E, top_k, kUpThreads, tokens, table);
+    } else {
+        build_table(idx, T, E, top_k, kUpThreads, tokens, table);
+    }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < (int)sizeof(MoeTable) / 4; i += kUpThreads)
+            reinterpret_cast<uint32_t *>(table_out)[i] = reinterpret_cast<const uint32_t *>(&table)[i];
+
+    const int G = (H + kF8Block - 1) / kF8Block, gi = (I + kF8Block - 1) / kF8Block;
+    const int tiles = I / 16, steps = (G + kUpWaves - 1) / kUpWaves;
+    const int items = __builtin_amdgcn_readfirstlane(table.reached) * tiles;
+    const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(X, (uint32_t)T * (uint32_t)H * 2u);
+
+    // A place in a wave's work: step `step` of the item for its tokens m0 ...
+    // (all waves of a block take the same number of steps; past H they load
+    // zeros).
+    struct Place {
+        int item, m0, step;
+        int e, i0, from, count;
+    };
+    auto enter = [&](Place &p, int item) __attribute__((always_inline)) {
+        p.item = item;
+        p.m0 = p.step = 0;
+        const int a = min(item, items - 1) / tiles;
+        p.i0 = min(item, items - 1) % tiles * 16;
+        p.e = __builtin_amdgcn_readfirstlane(table.expert[a]);
+        p.from = __builtin_amdgcn_readfirstlane(table.from[a]);
+        p.count = __builtin_amdgcn_readfirstlane(table.from[a + 1]) - p.from;
+    };
+    auto advance = [&](Place &p) __attribute__((always_inline)) {
+        if (++p.step < steps) return;
+        p.step = 0;
+        p.m0 += 16;
+        if (p.m0 < p.count) return;
+        enter(p, p.item + (int)gridDim.x);
+    };
+    struct Step {
+        u32x4 g[2], u[2], x[2][2];
+    };
+    // the operands of place p's step, and on to the next place
+    auto load = [&](Step &to, Place &p, uint32_t &xrow) __attribute__((always_inline)) {
+        const uint8_t *we = w13 + (size_t)p.e * 2 * I * H;
+        const __amdgpu_buffer_rsrc_t rg = fp8_rsrc(we + (size_t)p.i0 * H, 16u * (uint32_t)H);
+        const __amdgpu_buffer_rsrc_t ru = fp8_rsrc(we + (size_t)(I + p.i0) * H, 16u * (uint32_t)H);
+        if (p.step == 0)  // the lane's token, as a byte offset; lanes without one read zeros
+            xrow = p.m0 + r16 < p.count ? (uint32_t)(table.pair[p.from + p.m0 + r16] / top_k) * (uint32_t)H * 2u
+                                        : kMoeOob;
+        const int k0 = (p.step * kUpWaves + wave) * kF8Block + 16 * q4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = k0 + 64 * i;
+            const bool in = k < H && p.item < items;
+            const uint32_t off = in ? (uint32_t)r16 * (uint32_t)H + (uint32_t)k : kMoeOob;
+            const uint32_t xoff = in ? xrow + 2u * (uint32_t)k : kMoeOob;
+            to.g[i] = load16(rg, off);
+            to.u[i] = load16(ru, off);
+            to.x[i][0] = load16(rx, xoff);
+            to.x[i][1] = load16(rx, xoff + 16);
+        }
+        advance(p);
+    };
+    f32x4 accg = {0.f, 0.f, 0.f, 0.f}, accu = accg;
+    int turn = 0;
+    // one step: its products; the sums and the output behind an item's last one
+    auto compute = [&](const Step &now, Place &p) __attribute__((always_inline)) {
+        const int g = min(p.step * kUpWaves + wave, G - 1);
+        const size_t block = ((size_t)p.e * 2 * gi + p.i0 / kF8Block) * G + g;
+        const float wg = s13[block], wu = s13[block + (size_t)gi * G];
+        f32x4 pg = {0.f, 0.f, 0.f, 0.f}, pu = pg;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bf16x8 b0 = __builtin_bit_cast(bf16x8, now.x[i][0]), b1 = __builtin_bit_cast(bf16x8, now.x[i][1]);
+            pg = mfma_bf16_16x16x32(fp8_widen8(now.g[i][0], now.g[i][1]), b0, pg);
+            pu = mfma_bf16_16x16x32(fp8_widen8(now.u[i][0], now.u[i][1]), b0, pu);
+            pg = mfma_bf16_16x16x32(fp8_widen8(now.g[i][2], now.g[i][3]), b1, pg);
+            pu = mfma_bf16_16x16x32(fp8_widen8(now.u[i][2], now.u[i][3]), b1, pu);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            accg[i] = __builtin_fmaf(wg, pg[i], accg[i]);
+            accu[i] = __builtin_fmaf(wu, pu[i], accu[i]);
+        }
+    };
+    auto finish = [&](const Place &p) __attribute__((always_inline)) {
+        // two sets of sums take turns: one barrier per item
+        red[turn][wave][0][lane] = accg;
+        red[turn][wave][1][lane] = accu;
+        accg = accu = f32x4{0.f, 0.f, 0.f, 0.f};
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); the loads stay under way
+        __builtin_amdgcn_s_barrier();
         if (threadIdx.x < 256) {
             const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
             const int src = 16 * (c >> 2) + m;
             float g = 0.0f, u = 0.0f;
 #pragma unroll
             for (int w = 0; w < kUpWaves; ++w) {
-                g += red[w][0][src][c & 3];
-                u += red[w][1][src][c & 3];
+                g += red[turn][w][0][src][c & 3];
+                u += red[turn][w][1][src][c & 3];
             }
-            if (m0 + m < count) {
+            if (p.m0 + m < p.count) {
                 const float h = g / (1.0f + expf(-g)) * u;
                 const uint32_t hi = f32_to_bf16_bits(h);
-                const size_t at = (size_t)list[m0 + m] * I + i0 + c;
+                const size_t at = (size_t)table.pair[p.from + p.m0 + m] * I + p.i0 + c;
                 h_hi[at] = (uint16_t)hi;
                 // no remainder of an infinity or NaN
                 h_lo[at] = (hi & 0x7F80u) == 0x7F80u ? 0 : (uint16_t)f32_to_bf16_bits(h - bf16_bits_to_f32(hi));
             }
         }
+        turn ^= 1;
+    };
+    Place at, ahead;
+    enter(at, blockIdx.x);
+    ahead = at;
+    Step ring[kUpRing];
+    uint32_t xrow = 0;
+#pragma unroll
+    for (int n = 0; n < kUpRing; ++n) load(ring[n], ahead, xrow);
+    while (at.item < items) {
+#pragma unroll
+        for (int n = 0; n < kUpRing; ++n) {
+            if (at.item >= items) break;
+            compute(ring[n], at);
+            load(ring[n], ahead, xrow);
+            if (at.step == steps - 1) finish(at);
+            advance(at);
+        }
     }
 }
 
+// ---- rows of activations through LDS -----------------------------------------------
+
+// The activations of a few tokens reach the MFMA through LDS: 4 tokens' 128
+// features are one 1 KB load (a slot), where loads straight into the operand
+// registers take four, mostly of lanes without a token. (Per load the address
+// unit spends 16 cycles whatever its lanes hold: with 4 tokens per expert the
+// straight loads cost the down projection as much as its weights.) Lane l
+// brings the 16-byte chunk c of token l / 16 to chunk position c ^ 4 (l / 16),
+// so that the four tokens' equal chunks are on different banks.
+typedef __attribute__((address_space(3))) void moe_lds_void;
+constexpr int kSlot = 1024;
+
+__device__ __forceinline__ uint32_t slot_chunk(int lane) { return ((lane & 15) ^ (4 * (lane >> 4))) * 16; }
+
+__device__ __forceinline__ void load_slot(__amdgpu_buffer_rsrc_t r, uint8_t *slot, uint32_t row, int k, int K,
+                                          uint32_t chunk) {
+    const int at = 2 * k + (int)chunk;  // bytes into the row; zeros past its end
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (moe_lds_void *)slot, 16, at < 2 * K ? row + (uint32_t)at : kMoeOob, 0,
+                                             0, 0);
+}
+
+// Chunk c (of 16) of the lane's token (slots one after another, 4 tokens each).
+__device__ __forceinline__ bf16x8 slot_read(const uint8_t *slots, int token, int c) {
+    return *reinterpret_cast<const bf16x8 *>(slots + token * 256 + ((c ^ (4 * (token & 3))) * 16));
+}
+
+// Slots per group for at most 8 tokens.
+__device__ __forceinline__ int slots_of(int tokens) { return tokens <= 4 ? 1 : 2; }
+
 // ---- down projection and weighted sum ----------------------------------------
 
-constexpr int kDownAhead = 4;  // groups of weights in flight per wave
+constexpr int kDownAhead = 4;  // groups of weights per set; two sets take turns
+constexpr int kDownSlots = 2;  // per wave, each of hi and lo
+constexpr int kDownTokens = 4 * kDownSlots;  // of an expert at a time
 
 // One block: 16 output columns of every token. A wave takes one reached expert
-// and one of `splits` shares of I at a time, reads its 16 weight rows once and
-// leaves each pair's 16 sums in LDS at its own place; then each output is the
-// weighted sum over its token's pairs in order, so the result does not depend
-// on which wave came first.
+// and one of `splits` shares of I at a time (a unit), reads its 16 weight rows
+// once, a batch of groups ahead of their use, and leaves each pair's 16 sums in
+// LDS at its own place; then each output is the weighted sum over its token's
+// pairs in order, so the result does not depend on which wave came first.
 __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     const uint8_t *__restrict__ w2, const float *__restrict__ s2, const uint16_t *__restrict__ h_hi,
-    const uint16_t *__restrict__ h_lo, const float *__restrict__ gate, MoeLists lists, int T, int H, int I,
-    int top_k, int splits, uint16_t *__restrict__ Y) {
-    extern __shared__ __align__(16) float out[];  // [splits][T top_k][16]
+    const uint16_t *__restrict__ h_lo, const float *__restrict__ gate, const MoeTable *__restrict__ table_in, int T,
+    int H, int I, int top_k, int splits, uint16_t *__restrict__ Y) {
+    __shared__ MoeTable table;
+    extern __shared__ __align__(16) uint8_t smem[];  // slots [waves][2][kDownSlots], then sums [splits][T top_k][16]
+    float *out = reinterpret_cast<float *>(smem + kDownWaves * 2 * kDownSlots * kSlot);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint8_t *slots = smem + wave * 2 * kDownSlots * kSlot;
     const int r16 = lane & 15, q4 = lane >> 4;
     const int n0 = blockIdx.x * 16;
     const int pairs = T * top_k;
     const int G = (I + kF8Block - 1) / kF8Block, gh = (H + kF8Block - 1) / kF8Block;
-    const uint32_t row = (uint32_t)r16 * (uint32_t)I;
-    const int units = *lists.reached * splits;
-    for (int unit = wave; unit < units; unit += kDownWaves) {
-        const int a = unit / splits, s = unit % splits;
-        const int e = __builtin_amdgcn_readfirstlane(lists.experts[a]);
-        const int count = __builtin_amdgcn_readfirstlane(lists.counts[a]);
-        const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(w2 + ((size_t)e * H + n0) * I, 16u * (uint32_t)I);
-        const float *sw = s2 + ((size_t)e * gh + n0 / kF8Block) * G;
-        for (int m0 = 0; m0 < count; m0 += 16) {
-            const int pair = lists.pairs[(size_t)a * T + min(m0 + r16, count - 1)];
-            const uint16_t *hh = h_hi + (size_t)pair * I, *hl = h_lo + (size_t)pair * I;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            for (int g0 = s; g0 < G; g0 += splits * kDownAhead) {
-                u32x4 c[kDownAhead][2];
-#pragma unroll
-                for (int n = 0; n < kDownAhead; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = (g0 + n * splits) * kF8Block + 64 * i + 16 * q4;
-                        c[n][i] = load16(rw, k < I ? row + (uint32_t)k : kMoeOob);  // zeros past I
-                    }
-#pragma unroll
-                for (int n = 0; n < kDownAhead; ++n) {
-                    const int g = g0 + n * splits;
-                    if (g >= G) break;
-                    f32x4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = g * kF8Block + 64 * i + 16 * q4;
-                        u32x4 x0 = {0u, 0u, 0u, 0u}, x1 = x0, y0 = x0, y1 = x0;
-                        if (k < I) {
-                            x0 = *reinterpret_cast<const u32x4 *>(hh + k);
-                            x1 = *reinterpret_cast<const u32x4 *>(hh + k + 8);
-                            y0 = *reinterpret_cast<const u32x4 *>(hl + k);
-                            y1 = *reinterpret_cast<const u32x4 *>(hl + k + 8);
-                        }
-                        const bf16x8 a0 = fp8_widen8(c[n][i][0], c[n][i][1]), a1 = fp8_widen8(c[n][i][2], c[n][i][3]);
-                        p = mfma_bf16_16x16x32(a0, __builtin_bit_cast(bf16x8, y0), p);
-                        p = mfma_bf16_16x16x32(a1, __builtin_bit_cast(bf16x8, y1), p);
-                        p = mfma_bf16_16x16x32(a0, __builtin_bit_cast(bf16x8, x0), p);
-                        p = mfma_bf16_16x16x32(a1, __builtin_bit_cast(bf16x8, x1), p);
-                    }
-                    const float w = sw[g];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w, p[i], acc[i]);
-                }
-            }
-            if (m0 + r16 < count)
-                *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + pair) * 16 + 4 * q4) = acc;
+    const __amdgpu_buffer_rsrc_t rh = fp8_rsrc(h_hi, (uint32_t)pairs * (uint32_t)I * 2u);
+    const __amdgpu_buffer_rsrc_t rl = fp8_rsrc(h_lo, (uint32_t)pairs * (uint32_t)I * 2u);
+    const uint32_t chunk = slot_chunk(lane);
+    for (int i = threadIdx.x; i < (int)sizeof(MoeTable) / 4; i += kDownThreads)
+        reinterpret_cast<uint32_t *>(&table)[i] = reinterpret_cast<const uint32_t *>(table_in)[i];
+    __syncthreads();
+    const int units = __builtin_amdgcn_readfirstlane(table.reached) * splits;
+
+    // where a wave is: batch `first` (of the unit's groups) for tokens m0 ...
+    struct Place {
+        int unit, e, from, count, m0, first;
+    };
+    auto enter = [&](Place &p) __attribute__((always_inline)) {
+        if (p.unit < units) {
+            const int a = p.unit / splits;
+            p.e = __builtin_amdgcn_readfirstlane(table.expert[a]);
+            p.from = __builtin_amdgcn_readfirstlane(table.from[a]);
+            p.count = __builtin_amdgcn_readfirstlane(table.from[a + 1]) - p.from;
         }
+        p.m0 = p.first = 0;
+    };
+    auto groups = [&](const Place &p) __attribute__((always_inline)) {
+        const int s = p.unit % splits;
+        return (G - s + splits - 1) / splits;
+    };
+    auto advance = [&](Place &p) __attribute__((always_inline)) {
+        p.first += kDownAhead;
+        if (p.first < groups(p)) return;
+        p.first = 0;
+        p.m0 += kDownTokens;
+        if (p.m0 < p.count) return;
+        p.unit += kDownWaves;
+        enter(p);
+    };
+    auto load_weights = [&](u32x4(&to)[kDownAhead][2], const Place &p) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(w2 + ((size_t)p.e * H + n0) * I, 16u * (uint32_t)I);
+        const int s = p.unit % splits;
+#pragma unroll
+        for (int n = 0; n < kDownAhead; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = (s + (p.first + n) * splits) * kF8Block + 64 * i + 16 * q4;
+                to[n][i] = load16(rw, k < I ? (uint32_t)r16 * (uint32_t)I + (uint32_t)k : kMoeOob);  // zeros past I
+            }
+    };
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    // one batch from `now`, the next one's weights to `next`
+    auto batch = [&](Place &p, const u32x4(&now)[kDownAhead][2], u32x4(&next)[kDownAhead][2])
+                     __attribute__((always_inline)) {
+        const int s = p.unit % splits, all = groups(p);
+        const int here = min(kDownTokens, p.count - p.m0), per = slots_of(here);
+        const Place at = p;
+        uint32_t row[kDownSlots];
+#pragma unroll
+        for (int q = 0; q < kDownSlots; ++q)
+            row[q] = (uint32_t)table.pair[at.from + at.m0 + min(4 * q + q4, here - 1)] * (uint32_t)I * 2u;
+        const float *sw = s2 + ((size_t)at.e * gh + n0 / kF8Block) * G;
+        if (at.first == 0) acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        advance(p);
+#pragma unroll
+        for (int n = 0; n < kDownAhead; ++n) {
+            if (n * per % kDownSlots == 0) {  // the slots are empty: fill them, lo behind hi
+                __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what they held has been read
+#pragma unroll
+                for (int q = 0; q < kDownSlots; ++q) {
+                    const int k = (s + (at.first + n + q / per) * splits) * kF8Block;
+                    load_slot(rh, slots + q * kSlot, q % per ? row[1] : row[0], k, I, chunk);
+                    load_slot(rl, slots + (kDownSlots + q) * kSlot, q % per ? row[1] : row[0], k, I, chunk);
+                }
+                // the slots are there; the next batch's 2 kDownAhead loads may stay under way
+                __builtin_amdgcn_sched_barrier(0);
+                if (n == 0 && p.unit < units) {
+                    load_weights(next, p);
+                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * kDownAhead);  // vmcnt(2 kDownAhead)
+                } else {
+                    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (at.first + n >= all) break;
+            const uint8_t *hi = slots + n * per % kDownSlots * kSlot, *lo = hi + kDownSlots * kSlot;
+            const int token = r16 & (4 * per - 1);
+            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bf16x8 a0 = fp8_widen8(now[n][i][0], now[n][i][1]), a1 = fp8_widen8(now[n][i][2], now[n][i][3]);
+                const int c = 8 * i + 2 * q4;
+                sum = mfma_bf16_16x16x32(a0, slot_read(lo, token, c), sum);
+                sum = mfma_bf16_16x16x32(a1, slot_read(lo, token, c + 1), sum);
+                sum = mfma_bf16_16x16x32(a0, slot_read(hi, token, c), sum);
+                sum = mfma_bf16_16x16x32(a1, slot_read(hi, token, c + 1), sum);
+            }
+            const float w = sw[s + (at.first + n) * splits];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w, sum[i], acc[i]);
+        }
+        if (at.first + kDownAhead >= all && r16 < here)
+            *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + table.pair[at.from + at.m0 + r16]) * 16 + 4 * q4) =
+                acc;
+    };
+    Place p;
+    p.unit = wave;
+    enter(p);
+    u32x4 c0[kDownAhead][2], c1[kDownAhead][2];
+    if (p.unit < units) load_weights(c0, p);
+    while (p.unit < units) {
+        batch(p, c0, c1);
+        if (p.unit >= units) break;
+        batch(p, c1, c0);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < T * 16; i += kDownThreads) {
@@ -474,17 +600,17 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace: h (hi, lo planes of [pairs][I]), the logits, the reached experts'
-// lists, and room for the choices and weights of a call that does not ask for
+// Workspace: h (hi, lo planes of [pairs][I]), the logits, the table of
+// reached experts, and room for the choices and weights of a call that does not ask for
 // them.
 struct Layout {
-    size_t h_lo, logits, lists, idx, gate, bytes;
+    size_t h_lo, logits, table, idx, gate, bytes;
     Layout(int T, int I, int E, int top_k) {
-        const size_t pairs = (size_t)T * top_k, lists_n = std::min((size_t)E, pairs);
+        const size_t pairs = (size_t)T * top_k;
         h_lo = align256(pairs * I * 2);
         logits = 2 * h_lo;
-        lists = logits + align256((size_t)T * E * 8);
-        idx = lists + align256(4 * (lists_n * (2 + (size_t)T) + 1));
+        table = logits + align256((size_t)T * E * 8);
+        idx = table + align256(sizeof(MoeTable));
         gate = idx + align256(4 * pairs);
         bytes = gate + align256(4 * pairs);
     }
@@ -498,12 +624,11 @@ hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *
                           const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k, bool renorm,
                           int32_t *idx, float *gate, void *workspace, uint16_t *Y, hipStream_t stream) {
     const Layout at(T, I, E, top_k);
-    const int pairs = T * top_k, lists_n = std::min(E, pairs);
+    const int pairs = T * top_k, most = std::min(E, pairs);  // most: experts reached at the most
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     uint16_t *h_hi = reinterpret_cast<uint16_t *>(ws), *h_lo = reinterpret_cast<uint16_t *>(ws + at.h_lo);
     double *logits = reinterpret_cast<double *>(ws + at.logits);
-    int32_t *l = reinterpret_cast<int32_t *>(ws + at.lists);
-    const MoeLists lists{l, l + 1, l + 1 + lists_n, l + 1 + 2 * lists_n};
+    MoeTable *table = reinterpret_cast<MoeTable *>(ws + at.table);
     if (!idx) idx = reinterpret_cast<int32_t *>(ws + at.idx);
     if (!gate) gate = reinterpret_cast<float *>(ws + at.gate);
 
@@ -515,27 +640,28 @@ hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *
                            E, logits);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const dim3 up(I / 16, lists_n);
-    if (T <= kRouteInUp) {
+    const dim3 up((unsigned)std::min<int64_t>((int64_t)most * (I / 16), kUpBlocks));
+    if (T * E <= kRouteInUp) {
         hipLaunchKernelGGL(moe_up_kernel<true>, up, dim3(kUpThreads), 0, stream, X, w13, s13, logits, idx, gate, T, H,
-                           I, E, top_k, renorm ? 1 : 0, h_hi, h_lo, lists);
+                           I, E, top_k, renorm ? 1 : 0, h_hi, h_lo, table);
     } else {
-        hipLaunchKernelGGL(moe_route_kernel, dim3(1), dim3(kRouteThreads), 0, stream, logits, T, E, top_k,
-                           renorm ? 1 : 0, idx, gate, lists);
+        hipLaunchKernelGGL(moe_route_kernel, dim3(T), dim3(kRouteThreads), 0, stream, logits, E, top_k,
+                           renorm ? 1 : 0, idx, gate);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
         hipLaunchKernelGGL(moe_up_kernel<false>, up, dim3(kUpThreads), 0, stream, X, w13, s13, logits, idx, gate, T,
-                           H, I, E, top_k, renorm ? 1 : 0, h_hi, h_lo, lists);
+                           H, I, E, top_k, renorm ? 1 : 0, h_hi, h_lo, table);
     }
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     // as many shares of I as give every wave a unit, at most one per group and
     // what 32 KB of LDS hold
     const int G = fp8_blocks(I);
-    int splits = std::min((kDownWaves + lists_n - 1) / lists_n, G);
+    int splits = std::min((kDownWaves + most - 1) / most, G);
     while (splits > 1 && splits * pairs * 64 > (32 << 10)) --splits;
-    hipLaunchKernelGGL(moe_down_kernel, dim3(H / 16), dim3(kDownThreads), (size_t)splits * pairs * 64, stream, w2, s2,
-                       h_hi, h_lo, gate, lists, T, H, I, top_k, splits, Y);
+    const size_t lds = (size_t)kDownWaves * 2 * kDownSlots * kSlot + (size_t)splits * pairs * 64;
+    hipLaunchKernelGGL(moe_down_kernel, dim3(H / 16), dim3(kDownThreads), lds, stream, w2, s2, h_hi, h_lo, gate, table,
+                       T, H, I, top_k, splits, Y);
     return hipGetLastError();
 }
 
