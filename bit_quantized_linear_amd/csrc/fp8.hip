@@ -53,12 +53,7 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
     }
 #pragma unroll
     for (int i = 0; i < kF8QGroups; ++i) {
-        uint32_t mx = kF8TinyBits;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx = max(mx, max(v[i][j] & 0x7FFFu, (v[i][j] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
-        const float a = bf16_bits_to_f32(mx);
+        const float a = fp8_block_top(v[i]);
         const float r = kF8Max / a;
         if (part == 0) sxs[i][row] = a / kF8Max;
         const int k = (g0 + i) * kF8Block + part * 8;
@@ -76,13 +71,20 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
 
 constexpr uint32_t kF8Oob = 0x80000000u;
 constexpr int kF8Cus = 256;  // compute units
+constexpr int kF8SkinnyTokens = 16;  // one MFMA tile: 20 x 5120 x 5120 takes 14.6 us with two, 11.4 in tiles of 64
+// the linear in one launch: tokens, and LDS for their codes and scales
+constexpr int kF8FusedTokens = 4;
+constexpr size_t kF8FusedLds = 40 << 10;
 
 typedef __attribute__((address_space(3))) void f8_lds_void;
 
-template <int BN, int BM>
+// One stage: KW groups of 128 bytes of K, the rows of both operands.
+template <int BN, int BM, int KW>
 struct F8Stage {
-    uint8_t a[BN * kF8Block];
-    uint8_t b[BM * kF8Block];
+    struct Group {
+        uint8_t a[BN * kF8Block];
+        uint8_t b[BM * kF8Block];
+    } group[KW];
 };
 
 // Operands of one 16-row tile and group: the codes, or their bf16 values.
@@ -123,21 +125,22 @@ struct F8Wide {
 // One 16x16x128 MFMA is a whole group of a tile, so its result is scaled and
 // added (4 FMAs a lane) while the next row tile's MFMAs run.
 // kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
-template <int WN, int WM, int TN, int TM, bool kWide, class Stage>
-__device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, const uint8_t *__restrict__ qx,
+template <int WN, int WM, int TN, int TM, int NS, int KW, bool kWide, class Stage>
+__device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Stage &st3, float *bias_s, const uint8_t *__restrict__ qx,
                                          const float *__restrict__ sx, const uint8_t *__restrict__ qw,
                                          const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N,
                                          int K, void *__restrict__ Y, int n0, int m0) {
-    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, NW = WN * WM, kThreads = 64 * NW;
+    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, NW = WN * WM, kThreads = 64 * NW * KW;
     using Frag = std::conditional_t<kWide, F8Wide, F8Codes>;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kw = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 6) / NW;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % NW;
     const int wn = wave % WN;
     const int wm = wave / WN;
     const int r16 = lane & 15;
     const int q4 = lane >> 4;
-    const int S = (K + kF8Block - 1) / kF8Block;
+    const int G = (K + kF8Block - 1) / kF8Block, S = (G + KW - 1) / KW;
 
     const __amdgpu_buffer_rsrc_t ra = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(BN, N - n0) * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rb = fp8_rsrc(qx + (size_t)m0 * K, (uint32_t)min(BM, M - m0) * (uint32_t)K);
@@ -158,7 +161,7 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
     }
     // offsets of stage s, and its load i into st
     auto aim = [&](int s) __attribute__((always_inline)) {
-        const int k0 = s * kF8Block;
+        const int k0 = (s * KW + kw) * kF8Block;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bool in = k0 + gchunk[i] < K;
@@ -169,7 +172,7 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
     auto issue = [&](Stage &st, int i) __attribute__((always_inline)) {
         const bool a = i < kA;
         const int n = a ? i : i - kA;
-        uint8_t *dst = a ? st.a + (wave * kA + n) * 1024 : st.b + (wave * kB + n) * 1024;
+        uint8_t *dst = a ? st.group[kw].a + (wave * kA + n) * 1024 : st.group[kw].b + (wave * kB + n) * 1024;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? ra : rb, (f8_lds_void *)dst, 16,
                                                  (a ? oa : ob)[n & 1] + (uint32_t)(n / 2) * 16u * (uint32_t)K, 0, 0, 0);
     };
@@ -190,23 +193,29 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
     // this wave's columns lie in one block of 128: one weight scale a group
     static_assert(kF8Block % (16 * TN) == 0, "a wave's columns lie in one block");
     const int wblock = (n0 + wn * 16 * TN) / kF8Block;
-    const float *swr = sw + (size_t)(wblock < (N + kF8Block - 1) / kF8Block ? wblock : 0) * S;
+    const float *swr = sw + (size_t)(wblock < (N + kF8Block - 1) / kF8Block ? wblock : 0) * G;
     int mrow[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) mrow[j] = min(m0 + (wm * TM + j) * 16 + r16, M - 1);
-    float raw[TM], raw_w, sc[TM];
-    auto load_scales = [&](int s) __attribute__((always_inline)) {
-        raw_w = swr[s];
+    // the token scales of a stage, loaded with it (into raw[its slot] where
+    // stages stay under way for more than one)
+    constexpr int kRaw = NS == 2 ? 1 : NS;
+    float raw[kRaw][TM], sc[TM];
+    auto load_scales = [&](int s, int i) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TM; ++j) raw[j] = sx[(size_t)s * M + mrow[j]];
+        for (int j = 0; j < TM; ++j) raw[i % kRaw][j] = sx[(size_t)min(s * KW + kw, G - 1) * M + mrow[j]];
     };
 
     for (int i = tid; i < BN; i += kThreads)
         bias_s[i] = bias && n0 + i < N ? bf16_bits_to_f32(bias[n0 + i]) : 0.0f;
-    aim(0);
+    auto stage = [&](int i) -> Stage & { return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3; };
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) issue(st0, i);
-    load_scales(0);
+    for (int f = 0; f < NS - 1; ++f) {
+        aim(f);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) issue(stage(f), i);
+        load_scales(f, f);
+    }
 
     // kRing row tiles' operands in registers, tile i in slot i % kRing; the
     // products of MFMA t of a stage (t = row tile * TM + token tile) in slot
@@ -239,35 +248,45 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // stage s has landed and everyone has read stage s - 1
+    // stage s has landed (the NS - 2 behind it may be under way) and everyone
+    // has read stage s - 1
+    constexpr int kPending = (NS - 2) * (kLoads + TM);
+    static_assert(kPending < 64, "what a wait can count");
     auto next_stage = [&]() __attribute__((always_inline)) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (NS == 2)
+            __builtin_amdgcn_s_waitcnt(0);
+        else  // vmcnt(kPending) lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt((kPending & 15) | (7 << 4) | (0 << 8) | ((kPending >> 4) << 14));
+        fp8_barrier();
+        __builtin_amdgcn_sched_barrier(0);
     };
     // The last kLate row tiles of stage s - 1 are multiplied after the barrier
     // that opens stage s, from operands read before it, so that stage s's
     // first operands are read under their MFMAs: a token tile's as soon as
-    // its last MFMA has issued. The loads of stage s + 1 are spread over the
-    // MFMAs, TM / 2 apart (issued together they block the wave until the
-    // load unit has taken them all: 5 % slower at 32760 x 5120 x 5120). Stages
-    // run in pairs without a branch: a stage past K loads zeros and adds none.
+    // its last MFMA has issued. The loads of stage s + NS - 1 are spread over
+    // the MFMAs, TM / 2 apart (issued together they block the wave until the
+    // load unit has taken them all: 5 % slower at 32760 x 5120 x 5120). Two
+    // stages run in pairs without a branch (a stage past K loads zeros and adds
+    // none): with one the compiler spills.
     static_assert(2 * TN >= kLoads, "the loads of a stage fit between its MFMAs");
     auto load_before = [&](Stage &nxt, int u) __attribute__((always_inline)) {
         if (u % (TM / 2) == 0 && u / (TM / 2) < kLoads) issue(nxt, u / (TM / 2));
     };
-    auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
+    auto run_stage = [&](int s, int slot, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
         next_stage();
-        aim(s + 1);
-        read(fa[0], cur.a, wn * TN);
+        const float weight_scale = swr[min(s * KW + kw, G - 1)];
+        aim(s + NS - 1);
+        read(fa[0], cur.group[kw].a, wn * TN);
 #pragma unroll
         for (int r = 0; r < kLate; ++r) {
 #pragma unroll
             for (int j = 0; j < TM; ++j) {
                 load_before(nxt, r * TM + j);
                 multiply(TN - kLate + r, j);
-                if (r == kLate - 1) read(fb[j], cur.b, wm * TM + j);
+                if (r == kLate - 1) read(fb[j], cur.group[kw].b, wm * TM + j);
             }
-            read(fa[r + 1], cur.a, wn * TN + r + 1);
+            read(fa[r + 1], cur.group[kw].a, wn * TN + r + 1);
         }
 #pragma unroll
         for (int i = 0; i < TN - kLate; ++i) {
@@ -277,16 +296,26 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
                 multiply(i, j);
                 if (i * TM + j == kDelay - 1) {  // stage s - 1 is all added
 #pragma unroll
-                    for (int k = 0; k < TM; ++k) sc[k] = raw[k] * raw_w;
-                    load_scales(min(s + 1, S - 1));
+                    for (int k = 0; k < TM; ++k) sc[k] = raw[slot % kRaw][k] * weight_scale;
+                    load_scales(s + NS - 1, slot + NS - 1 < NS ? slot + NS - 1 : slot - 1);
                 }
             }
-            if (i + kRing < TN) read(fa[i % kRing], cur.a, wn * TN + i + kRing);
+            if (i + kRing < TN) read(fa[i % kRing], cur.group[kw].a, wn * TN + i + kRing);
         }
     };
-    for (int s = 0; s < S; s += 2) {
-        run_stage(s, st0, st1);
-        run_stage(s + 1, st1, st0);
+    if constexpr (NS == 2) {
+        for (int s = 0; s < S; s += 2) {
+            run_stage(s, 0, st0, st1);
+            run_stage(s + 1, 0, st1, st0);
+        }
+    } else {
+        for (int s = 0; s < S;) {  // stage s in slot s % NS
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                run_stage(s, i, stage(i), stage((i + NS - 1) % NS));
+                if (++s >= S) break;
+            }
+        }
     }
 #pragma unroll
     for (int r = 0; r < kLate; ++r)
@@ -294,7 +323,21 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
         for (int j = 0; j < TM; ++j) multiply(TN - kLate + r, j);
 #pragma unroll
     for (int t = TN * TM - kDelay; t < TN * TM; ++t) add(t);
-    next_stage();
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    // the waves of one part of K give their sums to those of the first
+    if constexpr (KW > 1) {
+        static_assert(KW == 2 && sizeof(Stage) >= sizeof(f32x4) * TN * TM * 64 * NW, "two parts, through one stage");
+        f32x4 *sums = reinterpret_cast<f32x4 *>(&st0) + wave * TN * TM * 64 + lane;
+        if (kw)
+#pragma unroll
+            for (int t = 0; t < TN * TM; ++t) sums[t * 64] = acc[t / TM][t % TM];
+        __syncthreads();
+        if (!kw)
+#pragma unroll
+            for (int t = 0; t < TN * TM; ++t) acc[t / TM][t % TM] += sums[t * 64];
+        __syncthreads();
+    }
 
     // Output: 32 tokens x BN columns at a time through LDS (the waves of one
     // wm write, everyone stores whole row segments), alternating between the
@@ -306,7 +349,7 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
 #pragma unroll
     for (int pass = 0; pass < WM * TM / 2; ++pass) {
         uint8_t *buf = reinterpret_cast<uint8_t *>((pass & 1) ? &st1 : &st0);
-        if (wm == pass / (TM / 2)) {
+        if (kw == 0 && wm == pass / (TM / 2)) {
 #pragma unroll
             for (int i = 0; i < TN; ++i) {
                 const int nl = (wn * TN + i) * 16 + 4 * q4;
@@ -334,18 +377,31 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, float *bias_s, 
     }
 }
 
-template <int WN, int WM, int TN, int TM, bool kWide>
-__global__ __launch_bounds__(64 * WN * WM, 1) void fp8_gemm_kernel(
+template <int WN, int WM, int TN, int TM, int NS, int KW, bool kWide>
+__global__ __launch_bounds__(64 * WN * WM * KW, 1) void fp8_gemm_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
     const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
     int tiles_n) {
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM;
-    __shared__ __attribute__((aligned(16))) F8Stage<BN, BM> st0;
-    __shared__ __attribute__((aligned(16))) F8Stage<BN, BM> st1;
+    using Stage = F8Stage<BN, BM, KW>;
+    __shared__ __attribute__((aligned(16))) Stage st0;
+    __shared__ __attribute__((aligned(16))) Stage st1;
     __shared__ __attribute__((aligned(16))) float bias_s[BN];
     int tile_n, tile_m;
     fp8_tile_of_block(blockIdx.x, gridDim.x, gridDim.x, tiles_n, tile_n, tile_m);
-    fp8_tile<WN, WM, TN, TM, kWide>(st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * BN, tile_m * BM);
+    if constexpr (NS == 2) {
+        fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * BN,
+                                            tile_m * BM);
+    } else {
+        __shared__ __attribute__((aligned(16))) Stage st2;
+        __shared__ __attribute__((aligned(16))) std::conditional_t<(NS > 3), Stage, char> st3;
+        if constexpr (NS == 3)
+            fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st2, st0, bias_s, qx, sx, qw, sw, bias, M, N, K, Y,
+                                                tile_n * BN, tile_m * BM);
+        else
+            fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st2, st3, bias_s, qx, sx, qw, sw, bias, M, N, K, Y,
+                                                tile_n * BN, tile_m * BM);
+    }
 }
 
 // 256 x 256 tiles, of which the grid's first `whole` blocks take one each; two
@@ -354,19 +410,19 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
     const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
     int tiles_n, int tiles, int whole) {
-    __shared__ __attribute__((aligned(16))) F8Stage<256, 256> st0;
-    __shared__ __attribute__((aligned(16))) F8Stage<256, 256> st1;
+    __shared__ __attribute__((aligned(16))) F8Stage<256, 256, 1> st0;
+    __shared__ __attribute__((aligned(16))) F8Stage<256, 256, 1> st1;
     __shared__ __attribute__((aligned(16))) float bias_s[256];
     int tile_n, tile_m;
     const int b = blockIdx.x;
     if (b < whole) {
         fp8_tile_of_block(b, whole, tiles, tiles_n, tile_n, tile_m);
-        fp8_tile<2, 4, 8, 4, false>(st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256, tile_m * 256);
+        fp8_tile<2, 4, 8, 4, 2, 1, false>(st0, st1, st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256, tile_m * 256);
     } else {
         const int id = whole + (b - whole) / 2, m0_half = (b - whole) % 2 * 128;
         fp8_tile_at(id, tiles, tiles_n, tile_n, tile_m);
         if (tile_m * 256 + m0_half < M)
-            fp8_tile<4, 2, 4, 4, false>(st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256,
+            fp8_tile<4, 2, 4, 4, 2, 1, false>(st0, st1, st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256,
                                         tile_m * 256 + m0_half);
     }
 }
@@ -374,37 +430,44 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 // ---- the product, few tokens -----------------------------------------------
 
 // One block computes 16 output columns of at most 16 MT tokens; its W waves
-// take the groups of K in turn (wave w groups w, w + W, ...), kF8Ahead of them
+// take the groups of K in turn (wave w groups w, w + W, ...), `Ahead` of them
 // in flight, straight from global memory into the operands of the 16x16x128
 // MFMA (weights as A: row = output column; tokens as B), and add their sums in
 // LDS in a fixed order. The weight is read once: HBM-bound.
-constexpr int kF8Ahead = 4;
-
-template <int W, int MT, bool kWide>
+// kFused (MT 1): from bf16 activations. While its first weights are on their
+// way, each block quantizes all tokens' features into LDS, exactly as the
+// activation pass does, which saves that launch; dynamic LDS: the codes
+// [M][K rounded up to groups], then the scales [G][M].
+template <int W, int MT, int Ahead, bool kWide, bool kFused>
 __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(const uint8_t *__restrict__ qx,
                                                             const float *__restrict__ sx,
+                                                            const uint16_t *__restrict__ X,
                                                             const uint8_t *__restrict__ qw,
                                                             const float *__restrict__ sw,
                                                             const uint16_t *__restrict__ bias, int M, int N, int K,
                                                             void *__restrict__ Y) {
     __shared__ f32x4 red[W][MT][64];
+    extern __shared__ __align__(16) uint8_t codes_s[];
     const int n0 = blockIdx.x * 16;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q4 = lane >> 4;
     const int G = (K + kF8Block - 1) / kF8Block;
     const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(16, N - n0) * (uint32_t)K);
-    const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(qx, (uint32_t)M * (uint32_t)K);
+    const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(qx, kFused ? 0u : (uint32_t)M * (uint32_t)K);
     const float *swr = sw + (size_t)(n0 / kF8Block) * G;
+    float *scales_s = reinterpret_cast<float *>(codes_s + (size_t)M * G * kF8Block);
 
+    auto join = [](u32x4 lo, u32x4 hi) __attribute__((always_inline)) {
+        return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    };
     // a lane's 32 codes of a group: chunks of 16 at k = 16 q4 and 64 + 16 q4
     auto operand = [&](__amdgpu_buffer_rsrc_t r, int row, int g) __attribute__((always_inline)) {
         const int k = g * kF8Block + 16 * q4;
         const uint32_t off = (uint32_t)row * (uint32_t)K + (uint32_t)k;
-        const u32x4 lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k < K ? off : kF8Oob, 0, 0));
-        const u32x4 hi =
-            __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k + 64 < K ? off + 64 : kF8Oob, 0, 0));
-        return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        return join(
+            __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k < K ? off : kF8Oob, 0, 0)),
+            __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k + 64 < K ? off + 64 : kF8Oob, 0, 0)));
     };
 
     f32x4 acc[MT];
@@ -414,22 +477,49 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(const uint8_t *__res
 #pragma unroll
     for (int j = 0; j < MT; ++j) mrow[j] = min(16 * j + r16, M - 1);
 
-    for (int g0 = wave; g0 < G; g0 += W * kF8Ahead) {
-        i32x8 a[kF8Ahead], b[kF8Ahead][MT];
-        float s[kF8Ahead][MT];
+    i32x8 a[Ahead];
 #pragma unroll
-        for (int u = 0; u < kF8Ahead; ++u) {
-            const int g = g0 + W * u;  // past K: every chunk reads zeros
-            a[u] = operand(rw, r16, g);
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                b[u][j] = operand(rx, mrow[j], g);
-                s[u][j] = sx[(size_t)min(g, G - 1) * M + mrow[j]] * swr[min(g, G - 1)];
-            }
+    for (int u = 0; u < Ahead; ++u) a[u] = operand(rw, r16, wave + W * u);  // past K: zeros
+    if constexpr (kFused) {
+        // 16 threads per token and group, 8 features each
+        const int part = threadIdx.x & 15;
+        for (int i = threadIdx.x >> 4; i < M * G; i += 4 * W) {
+            const int m = i / G, g = i % G, k = g * kF8Block + part * 8;
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (k < K) v = *reinterpret_cast<const u32x4 *>(X + (size_t)m * K + k);
+            const float top = fp8_block_top(v);
+            *reinterpret_cast<u32x2 *>(codes_s + (size_t)i * kF8Block + part * 8) = fp8_codes8(v, kF8Max / top);
+            if (part == 0) scales_s[g * M + m] = top / kF8Max;
         }
+        __syncthreads();
+    }
+    for (int g0 = wave; g0 < G; g0 += W * Ahead) {
+        if (g0 != wave) {
 #pragma unroll
-        for (int u = 0; u < kF8Ahead; ++u) {
-            if (g0 + W * u >= G) break;
+            for (int u = 0; u < Ahead; ++u) a[u] = operand(rw, r16, g0 + W * u);
+        }
+        i32x8 b[Ahead][MT];
+        float s[Ahead][MT];
+        if constexpr (!kFused) {
+#pragma unroll
+            for (int u = 0; u < Ahead; ++u)
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    const int g = g0 + W * u;
+                    b[u][j] = operand(rx, mrow[j], g);
+                    s[u][j] = sx[(size_t)min(g, G - 1) * M + mrow[j]] * swr[min(g, G - 1)];
+                }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // all of them under way before the first is used
+        // groups past K: zero weights add nothing, so no branch waits on them
+#pragma unroll
+        for (int u = 0; u < Ahead; ++u) {
+            if constexpr (kFused) {
+                const int g = min(g0 + W * u, G - 1);
+                const uint8_t *at = codes_s + ((size_t)mrow[0] * G + g) * kF8Block + 16 * q4;
+                b[u][0] = join(*reinterpret_cast<const u32x4 *>(at), *reinterpret_cast<const u32x4 *>(at + 64));
+                s[u][0] = scales_s[g * M + mrow[0]] * swr[g];
+            }
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -445,11 +535,11 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(const uint8_t *__res
     for (int i = threadIdx.x; i < 256 * MT; i += 64 * W) {
         const int m = i >> 4, c = i & 15;  // consecutive threads: consecutive columns of a token
         const int src = 16 * (c >> 2) + (m & 15);
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) v += red[w][m >> 4][src][c & 3];
         const int n = n0 + c;
         if (m < M && n < N) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) v += red[w][m >> 4][src][c & 3];
             if (bias) v += bf16_bits_to_f32(bias[n]);
             if constexpr (kWide)
                 static_cast<float *>(Y)[(size_t)m * N + n] = v;
@@ -469,12 +559,12 @@ hipError_t launch_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx,
     return hipGetLastError();
 }
 
-template <int WN, int WM, int TN, int TM, bool kWide>
+template <int WN, int WM, int TN, int TM, int NS, int KW, bool kWide>
 static hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                               const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM;
     const int tiles_n = (N + BN - 1) / BN, tiles_m = (M + BM - 1) / BM;
-    hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, TN, TM, kWide>), dim3(tiles_n * tiles_m), dim3(64 * WN * WM), 0,
+    hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, TN, TM, NS, KW, kWide>), dim3(tiles_n * tiles_m), dim3(64 * WN * WM * KW), 0,
                        stream, qx, sx, qw, sw, bias, M, N, K, Y, tiles_n);
     return hipGetLastError();
 }
@@ -482,33 +572,55 @@ static hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t 
 template <bool kWide>
 static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                               const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
-    if (M <= 64) {
-        const dim3 grid((N + 15) / 16), block(512);
-        auto go = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, grid, block, 0, stream, qx, sx, qw, sw, bias, M, N, K, Y);
-        };
-        if (M <= 16)
-            go(fp8_skinny_kernel<8, 1, kWide>);
-        else if (M <= 32)
-            go(fp8_skinny_kernel<8, 2, kWide>);
-        else
-            go(fp8_skinny_kernel<8, 4, kWide>);
+    if (M <= kF8SkinnyTokens) {
+        hipLaunchKernelGGL((fp8_skinny_kernel<8, 1, 2, kWide, false>), dim3((N + 15) / 16), dim3(512), 0, stream, qx, sx,
+                           nullptr, qw, sw, bias, M, N, K, Y);
         return hipGetLastError();
     }
-    const int64_t big = (int64_t)((N + 255) / 256) * ((M + 255) / 256);
-    if (big >= 96) {
-        if constexpr (kWide) {
-            return launch_tile<2, 2, 4, 4, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
-        } else {
-            const int tiles_n = (N + 255) / 256, tiles = (int)big;
-            const int rest = tiles % kF8Cus;
-            const int split = rest <= kF8Cus / 2 ? rest : 0;
-            hipLaunchKernelGGL(fp8_gemm256_kernel, dim3(tiles + split), dim3(512), 0, stream, qx, sx, qw, sw, bias, M,
-                               N, K, Y, tiles_n, tiles, tiles - split);
-            return hipGetLastError();
-        }
+    // Tiles of t x t: the larger, the less each operand is read; the smaller,
+    // the more compute units have one. Times in us for M x 5120 x 5120, by the
+    // rule / the next smaller or larger tile: bf16, M = 128 12.8 / 16.6, 256
+    // 19.6 / 24.1, 512 24.7 / 28.7, 1024 39.9 / 45.8, 2048 58.6 / 71.8.
+    const auto tiles = [&](int64_t tn, int64_t tm) { return ((N + tn - 1) / tn) * ((M + tm - 1) / tm); };
+    const int64_t small = tiles(64, 64);
+    if (small <= kF8Cus) return launch_tile<2, 2, 2, 2, 3, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+    if constexpr (kWide) {
+        // fp32: M = 256 30.9 / 33.6, 1024 68.4 / 77.3, 2048 132 / 151, 4608 234 / 298
+        if (small <= 6 * kF8Cus) return launch_tile<2, 2, 2, 2, 3, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+        return launch_tile<2, 2, 4, 4, 2, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+    } else {
+        const int64_t medium = tiles(128, 128), big = tiles(256, 256);
+        if (medium < kF8Cus / 2) return launch_tile<2, 2, 2, 2, 3, 1, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+        // three stages of a 128 x 128 tile fill a compute unit's LDS, of two
+        // stages two blocks share it
+        if (medium <= kF8Cus) return launch_tile<2, 2, 4, 4, 3, 1, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+        if (big < kF8Cus / 2) return launch_tile<2, 2, 4, 4, 2, 1, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+        // the tiles of a last round that would leave half the compute units
+        // idle are shared by two blocks each
+        const int rest = (int)(big % kF8Cus), split = rest <= kF8Cus / 2 ? rest : 0;
+        hipLaunchKernelGGL(fp8_gemm256_kernel, dim3((unsigned)(big + split)), dim3(512), 0, stream, qx, sx, qw, sw,
+                           bias, M, N, K, Y, (N + 255) / 256, (int)big, (int)big - split);
+        return hipGetLastError();
     }
-    return launch_tile<2, 2, 2, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+}
+
+template <bool kWide>
+static hipError_t launch_few(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias, int M, int N,
+                             int K, void *Y, hipStream_t stream) {
+    const size_t lds = (size_t)M * fp8_blocks(K) * (kF8Block + sizeof(float));
+    hipLaunchKernelGGL((fp8_skinny_kernel<8, 1, 3, kWide, true>), dim3((N + 15) / 16), dim3(512), lds, stream, nullptr,
+                       nullptr, X, qw, sw, bias, M, N, K, Y);
+    return hipGetLastError();
+}
+
+bool fp8_linear_in_one(int M, int K) {
+    return M <= kF8FusedTokens && (size_t)M * fp8_blocks(K) * (kF8Block + sizeof(float)) <= kF8FusedLds;
+}
+
+hipError_t launch_fp8_linear_in_one(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias,
+                                    int M, int N, int K, void *Y, bool y_f32, hipStream_t stream) {
+    return y_f32 ? launch_few<true>(X, qw, sw, bias, M, N, K, Y, stream)
+                 : launch_few<false>(X, qw, sw, bias, M, N, K, Y, stream);
 }
 
 hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,

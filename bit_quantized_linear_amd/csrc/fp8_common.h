@@ -20,6 +20,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t fp8_rsrc(const void *p, uint32
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
 }
 
+// A barrier of the block that leaves global loads under way (as __syncthreads()
+// does not): the caller has waited for its own LDS accesses. The empty asm
+// keeps the compiler from moving memory accesses across.
+__device__ __forceinline__ void fp8_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // E4M3 x E4M3 with fp32 accumulation, unscaled. A lane's operand is 32 codes
 // of one row (A) or column (B); the 32x32 output layout is that of the other
 // 32x32 MFMAs. The matrix core adds the 8 products of a lane's 8 consecutive
@@ -59,6 +68,18 @@ __device__ __forceinline__ f32x4 mfma_wide_16x16x128(i32x8 a, i32x8 b, f32x4 c) 
 #pragma unroll
     for (int i = 0; i < 8; i += 2) c = mfma_bf16_16x16x32(fp8_widen8(a[i], a[i + 1]), fp8_widen8(b[i], b[i + 1]), c);
     return c;
+}
+
+// The magnitude that a block's scale is made from: the largest of 16 lanes' 8
+// bf16 values each (lanes 16 n .. 16 n + 15), or 2^-100. On the bit patterns an
+// integer maximum orders magnitudes, and puts NaN above all.
+__device__ __forceinline__ float fp8_block_top(u32x4 v) {
+    uint32_t mx = kF8TinyBits;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mx = max(mx, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
+    return bf16_bits_to_f32(mx);
 }
 
 // The E4M3 codes (nearest even; NaN for NaN) of 8 bf16 values times r.

@@ -379,8 +379,9 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
         red[turn][wave][0][lane] = accg;
         red[turn][wave][1][lane] = accu;
         accg = accu = f32x4{0.f, 0.f, 0.f, 0.f};
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); the loads stay under way
-        __builtin_amdgcn_s_barrier();
+        fp8_barrier();
         if (threadIdx.x < 256) {
             const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
             const int src = 16 * (c >> 2) + m;
