@@ -115,14 +115,16 @@ __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits_kernel(const uint
 // NaN and -inf order below every number, alike.
 __device__ __forceinline__ double order_key(double l) { return l > -__builtin_inf() ? l : -__builtin_inf(); }
 
-// The place of expert e among its token's: how many have a larger logit, or
-// the same and a lower number. A permutation, so the first top_k places are
-// the choice, in order, with no rounds that wait for each other.
-__device__ __forceinline__ int place(const double *key, int E, int e) {
+// How many of the experts part, part + kParts, ... come before expert e: with a
+// larger logit, or the same and a lower number. The sum over the parts is e's
+// place, a permutation, so the first top_k places are the choice, in order,
+// with no rounds that wait for each other.
+constexpr int kParts = 4;
+__device__ __forceinline__ int place(const double *key, int E, int e, int part) {
     const double mine = key[e];
     int before = 0;
 #pragma unroll 4
-    for (int o = 0; o < E; ++o) {
+    for (int o = part; o < E; o += kParts) {
         const double v = key[o];
         before += v > mine || (v == mine && o < e) ? 1 : 0;
     }
@@ -132,8 +134,7 @@ __device__ __forceinline__ int place(const double *key, int E, int e) {
 // Weight numerators of a token's choices, in fp32: exp(l - largest l).
 __device__ __forceinline__ float numerator(double l, double top) { return expf((float)(l - top)); }
 
-// The weights' denominator: the sum of the chosen numerators in order, or of
-// all experts' (a wave's lanes take experts l, l + 64, ... and are folded).
+// All experts' numerators (lane l takes experts l, l + 64, ...; then a fold).
 __device__ __forceinline__ float all_numerators(const double *logit, double top, int E, int lane) {
     float sum = 0.0f;
     for (int o = lane; o < E; o += 64) sum += numerator(logit[o], top);
@@ -142,24 +143,32 @@ __device__ __forceinline__ float all_numerators(const double *logit, double top,
     return sum;
 }
 
-// The choices of `tokens` tokens by one block (a thread per token and expert
-// at a time, then a wave per token): idx and gate [tokens][top_k], which may be
-// in LDS. logit, key and first are LDS of the block: [tokens][E], [tokens][E],
-// [tokens][top_k].
-__device__ __forceinline__ void choose(const double *__restrict__ logits, int tokens, int E, int top_k, bool renorm,
-                                       int threads, double *logit, double *key, int32_t *first, int32_t *idx,
-                                       float *gate) {
+// The choices of `tokens` tokens by one block, kParts threads per token and
+// expert at a time: first [tokens][top_k], in LDS like logit and key
+// [tokens][E]. The block is in step afterwards.
+__device__ __forceinline__ void choose(const double *__restrict__ logits, int tokens, int E, int top_k, int threads,
+                                       double *logit, double *key, int32_t *first) {
     for (int i = threadIdx.x; i < tokens * E; i += threads) {
         logit[i] = logits[i];
         key[i] = order_key(logit[i]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < tokens * E; i += threads) {
-        const int t = i / E, e = i % E;
-        const int j = place(key + t * E, E, e);
-        if (j < top_k) first[t * top_k + j] = e;
+    const int items = tokens * E;
+    for (int i0 = 0; i0 < items; i0 += threads / kParts) {
+        const int i = i0 + (int)threadIdx.x / kParts;
+        const int t = min(i, items - 1) / E, e = min(i, items - 1) % E;
+        int j = place(key + t * E, E, e, threadIdx.x % kParts);
+#pragma unroll
+        for (int d = 1; d < kParts; d <<= 1) j += __shfl_xor(j, d);
+        if (i < items && j < top_k && threadIdx.x % kParts == 0) first[t * top_k + j] = e;
     }
     __syncthreads();
+}
+
+// The choices and their weights to idx and gate, a wave per token. The weights'
+// denominator is the sum of the chosen numerators in order, or of all.
+__device__ __forceinline__ void write_choices(const double *logit, const int32_t *first, int tokens, int E, int top_k,
+                                              bool renorm, int threads, int32_t *idx, float *gate) {
     const int lane = threadIdx.x & 63;
     for (int t = threadIdx.x >> 6; t < tokens; t += threads / 64) {
         const double *l = logit + t * E;
@@ -186,19 +195,20 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *
     __shared__ double logit[SVDQ_FP8_MOE_MAX_EXPERTS], key[SVDQ_FP8_MOE_MAX_EXPERTS];
     __shared__ int32_t first[SVDQ_FP8_MOE_MAX_TOP_K];
     const int t = blockIdx.x;
-    choose(logits + (size_t)t * E, 1, E, top_k, renorm, kRouteThreads, logit, key, first, idx + (size_t)t * top_k,
-           gate + (size_t)t * top_k);
+    choose(logits + (size_t)t * E, 1, E, top_k, kRouteThreads, logit, key, first);
+    write_choices(logit, first, 1, E, top_k, renorm, kRouteThreads, idx + (size_t)t * top_k, gate + (size_t)t * top_k);
 }
 
 // Up to this many (token, expert) pairs the up kernel's blocks make the choices
-// themselves, a thread per pair.
+// themselves.
 constexpr int kRouteInUp = 128;
 
 // ---- the reached experts ---------------------------------------------------------
 
-// The reached experts in ascending order and the pairs t top_k + j sorted by
-// expert, then token: reached expert number a has pairs pair[from[a]] ..
-// pair[from[a + 1] - 1]. Written down for the down projection as it is.
+// The reached experts (ascending; a single token's in the order of its choices)
+// and the pairs t top_k + j sorted by expert, then token: reached expert number
+// a has pairs pair[from[a]] .. pair[from[a + 1] - 1]. Written down for the down
+// projection as it is.
 struct MoeTable {
     int32_t reached;
     uint16_t expert[SVDQ_FP8_MOE_MAX_EXPERTS];
@@ -214,6 +224,15 @@ __device__ __forceinline__ void build_table(const int32_t *idx, int T, int E, in
                                             unsigned long long *tokens, MoeTable &table) {
     static_assert(SVDQ_FP8_MOE_MAX_TOKENS <= 64, "a bit per token");
     const int lane = threadIdx.x & 63;
+    if (T == 1) {  // each choice another expert: any order does
+        for (int j = threadIdx.x; j <= top_k; j += threads) {
+            if (j < top_k) table.expert[j] = (uint16_t)idx[j];
+            table.from[j] = table.pair[j] = (uint16_t)j;
+        }
+        if (threadIdx.x == 0) table.reached = top_k;
+        __syncthreads();
+        return;
+    }
     for (int e = threadIdx.x; e < SVDQ_FP8_MOE_MAX_EXPERTS; e += threads) tokens[e] = 0;
     __syncthreads();
     for (int p = threadIdx.x; p < T * top_k; p += threads) atomicOr(&tokens[idx[p]], 1ull << (p / top_k));
@@ -283,15 +302,10 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     const int r16 = lane & 15, q4 = lane >> 4;
     if constexpr (kRoute) {
         __shared__ double logit[kRouteInUp], key[kRouteInUp];
-        __shared__ int32_t first[kRouteInUp], idx_s[kRouteInUp];
-        __shared__ float gate_s[kRouteInUp];
-        choose(logits, T, E, top_k, renorm, kUpThreads, logit, key, first, idx_s, gate_s);
-        __syncthreads();
-        if (blockIdx.x == 0 && (int)threadIdx.x < T * top_k) {
-            idx[threadIdx.x] = idx_s[threadIdx.x];
-            gate[threadIdx.x] = gate_s[threadIdx.x];
-        }
-        build_table(idx_s, T, E, top_k, kUpThreads, tokens, table);
+        __shared__ int32_t first[kRouteInUp];
+        choose(logits, T, E, top_k, kUpThreads, logit, key, first);
+        if (blockIdx.x == 0) write_choices(logit, first, T, E, top_k, renorm, kUpThreads, idx, gate);
+        build_table(first, T, E, top_k, kUpThreads, tokens, table);
     } else {
         build_table(idx, T, E, top_k, kUpThreads, tokens, table);
     }
