@@ -84,16 +84,26 @@ svdq_status check_w4a4_shape(int M, int K, int rank, int group) {
 }
 
 // Block-scaled FP8: a tile's rows are addressed with 32-bit offsets (256 rows
-// of K bytes).
+// of K bytes); rows and columns rounded up to a tile stay below 2^31.
 constexpr int kFp8MaxK = 1 << 22;
+constexpr int kFp8MaxRows = 0x7FFFFFFF - 511;
 
 svdq_status check_fp8_linear_shape(int M, int N, int K, int y_dtype) {
     if (M < 0 || N <= 0 || K <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
-    if (K % 16 || N % 8 || K >= kFp8MaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 || N % 8 || K >= kFp8MaxK || M > kFp8MaxRows || N > kFp8MaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     if (y_dtype != SVDQ_BF16 && y_dtype != SVDQ_F32) return SVDQ_ERR_INVALID_ARGUMENT;
     // tiles (64 x 64 at the least) are numbered in one grid dimension
     if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) >= ((int64_t)1 << 31)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     return SVDQ_OK;
+}
+
+svdq_status check_fp8_moe_shape(int T, int H, int I, int E, int top_k) {
+    if (T < 0 || H <= 0 || I <= 0 || E <= 0 || top_k <= 0 || top_k > E) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (H % 16 || I % 16 || H >= kFp8MaxK || I >= kFp8MaxK || T > SVDQ_FP8_MOE_MAX_TOKENS ||
+        E > SVDQ_FP8_MOE_MAX_EXPERTS || top_k > SVDQ_FP8_MOE_MAX_TOP_K)
+        return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    // the pairs' intermediate rows are addressed with 32-bit offsets
+    return fits_buffer((int64_t)T * top_k, 2LL * I) ? SVDQ_OK : SVDQ_ERR_UNSUPPORTED_SHAPE;
 }
 
 }  // namespace
@@ -475,7 +485,7 @@ svdq_status svdq_mx_linear(const uint8_t *qx, const uint8_t *ux, const uint16_t 
 
 svdq_status svdq_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, void *stream) {
     if (M < 0 || K <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
-    if (K % 16 || K >= kFp8MaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 || K >= kFp8MaxK || M > kFp8MaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     if (M > 0 && (!X || !qx || !sx)) return SVDQ_ERR_INVALID_ARGUMENT;
     if (!aligned16(X) || !aligned16(qx) || !aligned16(sx)) return SVDQ_ERR_MISALIGNED;
     const svdq_status st = current_device_ok();
@@ -528,7 +538,7 @@ svdq_status svdq_fp8_linear(const uint16_t *X, const uint8_t *qw, const float *s
 }
 
 size_t svdq_fp8_moe_workspace_bytes(int T, int I, int E, int top_k) {
-    if (T < 0 || I <= 0 || E <= 0 || top_k <= 0) return 0;
+    if (T < 0 || check_fp8_moe_shape(T, 16, I, E, top_k) != SVDQ_OK) return 0;
     return svdq::fp8_moe_workspace_size(T, I, E, top_k);
 }
 
@@ -536,16 +546,14 @@ svdq_status svdq_fp8_moe_layer(const uint16_t *X, const uint16_t *wr, const uint
                                const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k,
                                int renormalize, int32_t *idx, float *gate, void *workspace, size_t workspace_bytes,
                                uint16_t *Y, void *stream) {
-    if (T < 0 || H <= 0 || I <= 0 || E <= 0 || top_k <= 0 || top_k > E) return SVDQ_ERR_INVALID_ARGUMENT;
-    if (H % 16 || I % 16 || H >= kFp8MaxK || I >= kFp8MaxK || T > SVDQ_FP8_MOE_MAX_TOKENS ||
-        E > SVDQ_FP8_MOE_MAX_EXPERTS || top_k > SVDQ_FP8_MOE_MAX_TOP_K)
-        return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    svdq_status st = check_fp8_moe_shape(T, H, I, E, top_k);
+    if (st != SVDQ_OK) return st;
     if (!wr || !w13 || !s13 || !w2 || !s2 || (T > 0 && (!X || !Y || !workspace))) return SVDQ_ERR_INVALID_ARGUMENT;
     if (T > 0 && workspace_bytes < svdq::fp8_moe_workspace_size(T, I, E, top_k)) return SVDQ_ERR_INVALID_ARGUMENT;
     if (!aligned16(X) || !aligned16(wr) || !aligned16(w13) || !aligned16(s13) || !aligned16(w2) || !aligned16(s2) ||
         !aligned16(idx) || !aligned16(gate) || !aligned16(workspace) || !aligned16(Y))
         return SVDQ_ERR_MISALIGNED;
-    const svdq_status st = current_device_ok();
+    st = current_device_ok();
     if (st != SVDQ_OK) return st;
     if (T == 0) return SVDQ_OK;
     return launched(svdq::launch_fp8_moe(X, wr, w13, s13, w2, s2, T, H, I, E, top_k, renormalize != 0, idx, gate,

@@ -78,12 +78,14 @@ constexpr size_t kF8FusedLds = 40 << 10;
 
 typedef __attribute__((address_space(3))) void f8_lds_void;
 
-// One stage: KW groups of 128 bytes of K, the rows of both operands.
-template <int BN, int BM, int KW>
+// One stage: KW groups of 128 bytes of K, the rows of both operands, and each
+// wave's token scales.
+template <int BN, int BM, int NW, int KW>
 struct F8Stage {
     struct Group {
         uint8_t a[BN * kF8Block];
         uint8_t b[BM * kF8Block];
+        float scale[NW][64];
     } group[KW];
 };
 
@@ -194,16 +196,18 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
     static_assert(kF8Block % (16 * TN) == 0, "a wave's columns lie in one block");
     const int wblock = (n0 + wn * 16 * TN) / kF8Block;
     const float *swr = sw + (size_t)(wblock < (N + kF8Block - 1) / kF8Block ? wblock : 0) * G;
-    int mrow[TM];
-#pragma unroll
-    for (int j = 0; j < TM; ++j) mrow[j] = min(m0 + (wm * TM + j) * 16 + r16, M - 1);
-    // the token scales of a stage, loaded with it (into raw[its slot] where
-    // stages stay under way for more than one)
-    constexpr int kRaw = NS == 2 ? 1 : NS;
-    float raw[kRaw][TM], sc[TM];
-    auto load_scales = [&](int s, int i) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < TM; ++j) raw[i % kRaw][j] = sx[(size_t)min(s * KW + kw, G - 1) * M + mrow[j]];
+    // The scales of the wave's 16 TM tokens go to LDS with the stage, one load
+    // of 4 bytes a lane (zeros past M); a wave's loads per stage are kLoads and
+    // this one, all of them to LDS, so that a wait can count them.
+    static_assert(TM <= 4, "a lane per token");
+    float raw[TM], sc[TM];
+    const int first_m = m0 + wm * TM * 16;
+    auto load_scales = [&](int s, Stage &st) __attribute__((always_inline)) {
+        const int g = min(s * KW + kw, G - 1);
+        const __amdgpu_buffer_rsrc_t r =
+            fp8_rsrc(sx + (size_t)g * M + min(first_m, M - 1), 4u * (uint32_t)max(0, min(16 * TM, M - first_m)));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (f8_lds_void *)st.group[kw].scale[wave], 4, 4u * (uint32_t)lane, 0,
+                                                 0, 0);
     };
 
     for (int i = tid; i < BN; i += kThreads)
@@ -214,7 +218,7 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
         aim(f);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) issue(stage(f), i);
-        load_scales(f, f);
+        load_scales(f, stage(f));
     }
 
     // kRing row tiles' operands in registers, tile i in slot i % kRing; the
@@ -248,16 +252,16 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // stage s has landed (the NS - 2 behind it may be under way) and everyone
-    // has read stage s - 1
-    constexpr int kPending = (NS - 2) * (kLoads + TM);
-    static_assert(kPending < 64, "what a wait can count");
+    // stage s has landed (the NS - 2 behind it may be under way; loads return
+    // in order) and everyone has read stage s - 1
+    constexpr int kPending = (NS - 2) * (kLoads + 1);
+    static_assert(kPending < 16, "what the wait below can count");
     auto next_stage = [&]() __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (NS == 2)
             __builtin_amdgcn_s_waitcnt(0);
         else  // vmcnt(kPending) lgkmcnt(0)
-            __builtin_amdgcn_s_waitcnt((kPending & 15) | (7 << 4) | (0 << 8) | ((kPending >> 4) << 14));
+            __builtin_amdgcn_s_waitcnt(kPending | (7 << 4) | (0 << 8));
         fp8_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -273,10 +277,13 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
     auto load_before = [&](Stage &nxt, int u) __attribute__((always_inline)) {
         if (u % (TM / 2) == 0 && u / (TM / 2) < kLoads) issue(nxt, u / (TM / 2));
     };
-    auto run_stage = [&](int s, int slot, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
+    auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
         next_stage();
         const float weight_scale = swr[min(s * KW + kw, G - 1)];
         aim(s + NS - 1);
+        load_scales(s + NS - 1, nxt);
+#pragma unroll
+        for (int k = 0; k < TM; ++k) raw[k] = cur.group[kw].scale[wave][k * 16 + r16];
         read(fa[0], cur.group[kw].a, wn * TN);
 #pragma unroll
         for (int r = 0; r < kLate; ++r) {
@@ -296,8 +303,7 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
                 multiply(i, j);
                 if (i * TM + j == kDelay - 1) {  // stage s - 1 is all added
 #pragma unroll
-                    for (int k = 0; k < TM; ++k) sc[k] = raw[slot % kRaw][k] * weight_scale;
-                    load_scales(s + NS - 1, slot + NS - 1 < NS ? slot + NS - 1 : slot - 1);
+                    for (int k = 0; k < TM; ++k) sc[k] = raw[k] * weight_scale;
                 }
             }
             if (i + kRing < TN) read(fa[i % kRing], cur.group[kw].a, wn * TN + i + kRing);
@@ -305,14 +311,14 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
     };
     if constexpr (NS == 2) {
         for (int s = 0; s < S; s += 2) {
-            run_stage(s, 0, st0, st1);
-            run_stage(s + 1, 0, st1, st0);
+            run_stage(s, st0, st1);
+            run_stage(s + 1, st1, st0);
         }
     } else {
         for (int s = 0; s < S;) {  // stage s in slot s % NS
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                run_stage(s, i, stage(i), stage((i + NS - 1) % NS));
+                run_stage(s, stage(i), stage((i + NS - 1) % NS));
                 if (++s >= S) break;
             }
         }
@@ -390,7 +396,7 @@ __global__ __launch_bounds__(64 * WN * WM * KW, 1) void fp8_gemm_kernel(
     const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
     int tiles_n) {
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM;
-    using Stage = F8Stage<BN, BM, KW>;
+    using Stage = F8Stage<BN, BM, WN * WM, KW>;
     __shared__ __attribute__((aligned(16))) Stage st0;
     __shared__ __attribute__((aligned(16))) Stage st1;
     __shared__ __attribute__((aligned(16))) float bias_s[BN];
@@ -417,8 +423,8 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
     const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
     int tiles_n, int tiles, int whole) {
-    __shared__ __attribute__((aligned(16))) F8Stage<256, 256, 1> st0;
-    __shared__ __attribute__((aligned(16))) F8Stage<256, 256, 1> st1;
+    __shared__ __attribute__((aligned(16))) F8Stage<256, 256, 8, 1> st0;
+    __shared__ __attribute__((aligned(16))) F8Stage<256, 256, 8, 1> st1;
     __shared__ __attribute__((aligned(16))) float bias_s[256];
     int tile_n, tile_m;
     const int b = blockIdx.x;

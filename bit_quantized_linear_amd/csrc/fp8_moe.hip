@@ -226,7 +226,7 @@ __device__ __forceinline__ void build_table(const int32_t *idx, int T, int E, in
     const int lane = threadIdx.x & 63;
     if (T == 1) {  // each choice another expert: any order does
         for (int j = threadIdx.x; j <= top_k; j += threads) {
-            if (j < top_k) table.expert[j] = (uint16_t)idx[j];
+            if (j < top_k) table.expert[j] = (uint16_t)min((unsigned)idx[j], (unsigned)E - 1);
             table.from[j] = table.pair[j] = (uint16_t)j;
         }
         if (threadIdx.x == 0) table.reached = top_k;
@@ -235,7 +235,11 @@ __device__ __forceinline__ void build_table(const int32_t *idx, int T, int E, in
     }
     for (int e = threadIdx.x; e < SVDQ_FP8_MOE_MAX_EXPERTS; e += threads) tokens[e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < T * top_k; p += threads) atomicOr(&tokens[idx[p]], 1ull << (p / top_k));
+    // the choices are in range; where a caller's other work writes the buffer
+    // meanwhile, the clamp and the bounded search below keep every access and
+    // loop inside the table
+    auto choice = [&](int p) { return min((unsigned)idx[p], (unsigned)E - 1); };
+    for (int p = threadIdx.x; p < T * top_k; p += threads) atomicOr(&tokens[choice(p)], 1ull << (p / top_k));
     __syncthreads();
     if (threadIdx.x < 64) {
         int reached = 0, start = 0;
@@ -268,7 +272,7 @@ __device__ __forceinline__ void build_table(const int32_t *idx, int T, int E, in
         const uint64_t set = tokens[e];
         if (set >> t & 1) {
             int j = 0;
-            while (idx[t * top_k + j] != e) ++j;  // it is there
+            while (j < top_k - 1 && (int)choice(t * top_k + j) != e) ++j;
             table.pair[table.from[a] + __popcll(set & ((1ull << t) - 1))] = (uint16_t)(t * top_k + j);
         }
     }

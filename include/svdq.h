@@ -482,7 +482,8 @@ svdq_status w4a16_linear(const uint16_t *X, const uint8_t *packed,
  *   infinite scale and a NaN code for it: its token's outputs are NaN.
  * In:  X [M, K] bf16.
  * Out: qx [M, K] E4M3 bytes; sx [ceil(K/128), M] fp32.
- * Shapes: M >= 0 (M == 0 launches nothing), K % 16 == 0.
+ * Shapes: M >= 0 (M == 0 launches nothing), K % 16 == 0, K < 2^22,
+ *      M < 2^31 - 511.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
  *      HIP. */
 svdq_status svdq_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, void *stream);
@@ -499,7 +500,7 @@ svdq_status svdq_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, 
  * In:  qx, sx (svdq_fp8_quantize_act); qw, sw (svdq_fp8_prepare_weights);
  *      bias [N] bf16 or NULL; y_dtype SVDQ_BF16 or SVDQ_F32.
  * Out: Y [M, N]. Shapes: M >= 0 (M == 0 launches nothing), K % 16 == 0,
- *      N % 8 == 0, K < 2^22. Deterministic.
+ *      N % 8 == 0, K < 2^22, M and N < 2^31 - 511. Deterministic.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
  *      HIP. */
 svdq_status svdq_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
@@ -545,10 +546,13 @@ size_t svdq_fp8_moe_workspace_bytes(int T, int I, int E, int top_k);
  *      that may overlap in time need one each.
  * Shapes: 0 <= T <= SVDQ_FP8_MOE_MAX_TOKENS (T == 0 launches nothing),
  *      H % 16 == 0, I % 16 == 0, 1 <= E <= SVDQ_FP8_MOE_MAX_EXPERTS,
- *      1 <= top_k <= min(E, SVDQ_FP8_MOE_MAX_TOP_K), H < 2^22, I < 2^22.
- * The weights of the experts that some token chose are read once (those of an
- * expert with more than 16 tokens once per 16). Deterministic; a token's
- * outputs depend on its own row of X only.
+ *      1 <= top_k <= min(E, SVDQ_FP8_MOE_MAX_TOP_K), H < 2^22, I < 2^22,
+ *      T * top_k * I < 2^30.
+ * The weights of the experts that some token chose are read once (w13 of an
+ * expert with more than 16 tokens once per 16, w2 with more than 8 once per 8).
+ * Deterministic; a token's outputs depend on its own row of X only. A token
+ * with logits that are not finite has a full choice of experts all the same;
+ * its weights and outputs may be NaN.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
  *      HIP. */
 svdq_status svdq_fp8_moe_layer(const uint16_t *X, const uint16_t *wr, const uint8_t *w13, const float *s13,

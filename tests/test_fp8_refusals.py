@@ -34,14 +34,15 @@ def moe(X=FAKE, wr=FAKE, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, T=2, H=64, I=32, 
     (quantize, {"K": 1 << 22}, SHAPE), (quantize, {"X": None}, INVALID), (quantize, {"sx": None}, INVALID),
     (quantize, {"qx": MISALIGNED}, MIS),
     (gemm, {"M": -1}, INVALID), (gemm, {"N": 0}, INVALID), (gemm, {"K": 72}, SHAPE), (gemm, {"N": 60}, SHAPE),
-    (gemm, {"K": 1 << 22}, SHAPE), (gemm, {"M": 2147483647, "N": 2147483640}, SHAPE), (gemm, {"dt": 2}, INVALID),
+    (gemm, {"K": 1 << 22}, SHAPE), (gemm, {"M": 2147483647, "N": 8}, SHAPE), (gemm, {"M": 1, "N": 2147483640}, SHAPE),
+    (quantize, {"M": 2147483647}, SHAPE), (gemm, {"M": 2147483647, "N": 2147483640}, SHAPE), (gemm, {"dt": 2}, INVALID),
     (gemm, {"qw": None}, INVALID), (gemm, {"sx": None}, INVALID), (gemm, {"Y": None}, INVALID),
     (gemm, {"bias": MISALIGNED}, MIS), (gemm, {"sw": MISALIGNED}, MIS),
     (linear, {"wb": 16 * 128}, INVALID), (linear, {"ws": None}, INVALID), (linear, {"X": None}, INVALID),
     (linear, {"X": MISALIGNED}, MIS), (linear, {"N": 4}, SHAPE), (linear, {"K": 24}, SHAPE),
     (moe, {"T": -1}, INVALID), (moe, {"T": 65}, SHAPE), (moe, {"H": 72}, SHAPE), (moe, {"I": 40}, SHAPE),
     (moe, {"E": 257}, SHAPE), (moe, {"k": 0}, INVALID), (moe, {"k": 5}, INVALID),
-    (moe, {"E": 64, "k": 17}, SHAPE), (moe, {"wb": 64}, INVALID), (moe, {"ws": None}, INVALID),
+    (moe, {"E": 64, "k": 17}, SHAPE), (moe, {"T": 64, "E": 64, "k": 16, "I": 1 << 20}, SHAPE), (moe, {"wb": 64}, INVALID), (moe, {"ws": None}, INVALID),
     (moe, {"w13": None}, INVALID), (moe, {"s2": None}, INVALID), (moe, {"X": None}, INVALID),
     (moe, {"Y": None}, INVALID), (moe, {"idx": MISALIGNED}, MIS), (moe, {"w2": MISALIGNED}, MIS),
 ], ids=str)
@@ -63,7 +64,8 @@ def test_workspace_bytes():
     assert b.svdq_fp8_workspace_bytes(0, 144) == 0 and b.svdq_fp8_workspace_bytes(-1, 144) == 0
     assert b.svdq_fp8_workspace_bytes(3, 100) == 0
     assert b.svdq_fp8_moe_workspace_bytes(2, 32, 4, 2) >= 2 * 2 * 2 * 32 * 2
-    assert b.svdq_fp8_moe_workspace_bytes(2, 32, 0, 2) == 0
+    for bad in ((-1, 32, 4, 2), (65, 32, 4, 2), (2, 40, 4, 2), (2, 32, 0, 2), (2, 32, 257, 2), (2, 32, 4, 5)):
+        assert b.svdq_fp8_moe_workspace_bytes(*bad) == 0
 
 
 def _case(name):
