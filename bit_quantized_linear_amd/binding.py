@@ -126,10 +126,16 @@ def _np_ptr(a, dtype):
     return a.ctypes.data
 
 
-def _current_device():
-    import torch
+_device_of = None
 
-    return torch.cuda.current_device()
+
+def _current_device():
+    global _device_of
+    if _device_of is None:
+        import torch
+
+        _device_of = torch.cuda.current_device
+    return _device_of()
 
 
 def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None):
@@ -163,15 +169,21 @@ def _shape2(t, name):
     return int(t.shape[0]), int(t.shape[1])
 
 
+_raw_stream = None
+
+
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
 
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:  # the same handle without a Stream object: 0.4 us a call instead of 3.0
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle, where torch has it without a Stream
+        # object (3 us a call)
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+        _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 # ------------------------------------------------------------------ info --

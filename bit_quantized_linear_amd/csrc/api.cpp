@@ -526,7 +526,7 @@ svdq_status svdq_fp8_linear(const uint16_t *X, const uint8_t *qw, const float *s
     st = current_device_ok();
     if (st != SVDQ_OK) return st;
     if (M == 0) return SVDQ_OK;
-    if (svdq::fp8_linear_in_one(M, K))
+    if (svdq::fp8_linear_in_one(M, N, K))
         return launched(svdq::launch_fp8_linear_in_one(X, qw, sw, bias, M, N, K, Y, y_dtype == SVDQ_F32,
                                                        (hipStream_t)stream));
     uint8_t *qx = static_cast<uint8_t *>(workspace);

@@ -72,9 +72,7 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
 constexpr uint32_t kF8Oob = 0x80000000u;
 constexpr int kF8Cus = 256;  // compute units
 constexpr int kF8SkinnyTokens = 16;  // one MFMA tile: 20 x 5120 x 5120 takes 14.6 us with two, 11.4 in tiles of 64
-// the linear in one launch: tokens, and LDS for their codes and scales
-constexpr int kF8FusedTokens = 4;
-constexpr size_t kF8FusedLds = 40 << 10;
+constexpr size_t kF8FusedLds = 40 << 10;  // the linear in one launch: LDS for its codes and scales
 
 typedef __attribute__((address_space(3))) void f8_lds_void;
 
@@ -626,8 +624,15 @@ static hipError_t launch_few(const uint16_t *X, const uint8_t *qw, const float *
     return hipGetLastError();
 }
 
-bool fp8_linear_in_one(int M, int K) {
-    return M <= kF8FusedTokens && (size_t)M * fp8_blocks(K) * (kF8Block + sizeof(float)) <= kF8FusedLds;
+// Every block quantizes all tokens anew, so one launch pays where a compute unit
+// does not do it for too many token groups. Times of a call in us, in one / two
+// launches: 4 x 5120 x 5120 (200 groups a unit) 11.5 / 12.8, 2 x 12288 x 5120
+// (240) 13.0 / 15.5, 8 x 2048 x 2048 (128) 5.6 / 7.9, 16 x 1024 x 12288 (384)
+// 9.5 / 9.1, 8 x 5120 x 5120 (400) 15.4 / 13.4.
+bool fp8_linear_in_one(int M, int N, int K) {
+    const int64_t groups = (int64_t)M * fp8_blocks(K);
+    return M <= kF8SkinnyTokens && groups * std::max(N, 16 * kF8Cus) <= (int64_t)256 * 16 * kF8Cus &&
+           groups * (kF8Block + sizeof(float)) <= kF8FusedLds;
 }
 
 hipError_t launch_fp8_linear_in_one(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias,

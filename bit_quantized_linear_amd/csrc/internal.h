@@ -107,7 +107,7 @@ hipError_t launch_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx,
 hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                            const uint16_t *bias, int M, int N, int K, void *Y, bool y_f32, hipStream_t stream);
 // few tokens: the linear from bf16 activations in one launch
-bool fp8_linear_in_one(int M, int K);
+bool fp8_linear_in_one(int M, int N, int K);
 hipError_t launch_fp8_linear_in_one(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias,
                                     int M, int N, int K, void *Y, bool y_f32, hipStream_t stream);
 size_t fp8_moe_workspace_size(int T, int I, int E, int top_k);
