@@ -186,7 +186,7 @@ __device__ __forceinline__ void write_choices(const double *logit, const int32_t
     }
 }
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = kParts * SVDQ_FP8_MOE_MAX_EXPERTS;
 
 // One block per token.
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *__restrict__ logits, int E, int top_k,
@@ -200,7 +200,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *
 }
 
 // Up to this many (token, expert) pairs the up kernel's blocks make the choices
-// themselves.
+// themselves (one token of 64 experts: 22.8 us in three launches, 26.5 in four;
+// 23 of 40: 35.3 and 31.6, as every block does all the comparisons).
 constexpr int kRouteInUp = 128;
 
 // ---- the reached experts ---------------------------------------------------------
