@@ -84,13 +84,15 @@ svdq_status check_w4a4_shape(int M, int K, int rank, int group) {
 }
 
 // Block-scaled FP8: a tile's rows are addressed with 32-bit offsets (256 rows
-// of K bytes); rows and columns rounded up to a tile stay below 2^31.
+// of K bytes); columns rounded up to a tile stay below 2^31; a launch has fewer
+// than 2^32 threads along its grid's first dimension, 16 per token at the most.
 constexpr int kFp8MaxK = 1 << 22;
-constexpr int kFp8MaxRows = 0x7FFFFFFF - 511;
+constexpr int kFp8MaxTokens = (1 << 28) - 16;
+constexpr int kFp8MaxColumns = 0x7FFFFFFF - 511;
 
 svdq_status check_fp8_linear_shape(int M, int N, int K, int y_dtype) {
     if (M < 0 || N <= 0 || K <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
-    if (K % 16 || N % 8 || K >= kFp8MaxK || M > kFp8MaxRows || N > kFp8MaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 || N % 8 || K >= kFp8MaxK || M > kFp8MaxTokens || N > kFp8MaxColumns) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     if (y_dtype != SVDQ_BF16 && y_dtype != SVDQ_F32) return SVDQ_ERR_INVALID_ARGUMENT;
     // tiles (64 x 64 at the least) are numbered in one grid dimension
     if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) >= ((int64_t)1 << 31)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
@@ -485,7 +487,7 @@ svdq_status svdq_mx_linear(const uint8_t *qx, const uint8_t *ux, const uint16_t 
 
 svdq_status svdq_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, void *stream) {
     if (M < 0 || K <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
-    if (K % 16 || K >= kFp8MaxK || M > kFp8MaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 || K >= kFp8MaxK || M > kFp8MaxTokens) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     if (M > 0 && (!X || !qx || !sx)) return SVDQ_ERR_INVALID_ARGUMENT;
     if (!aligned16(X) || !aligned16(qx) || !aligned16(sx)) return SVDQ_ERR_MISALIGNED;
     const svdq_status st = current_device_ok();

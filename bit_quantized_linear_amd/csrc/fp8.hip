@@ -71,6 +71,7 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
 
 constexpr uint32_t kF8Oob = 0x80000000u;
 constexpr int kF8Cus = 256;  // compute units
+constexpr int kF8SkinnyWaves = 8;
 constexpr int kF8SkinnyTokens = 16;  // one MFMA tile: 20 x 5120 x 5120 takes 14.6 us with two, 11.4 in tiles of 64
 constexpr size_t kF8FusedLds = 40 << 10;  // the linear in one launch: LDS for its codes and scales
 
@@ -126,10 +127,11 @@ struct F8Wide {
 // added (4 FMAs a lane) while the next row tile's MFMAs run.
 // kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
 template <int WN, int WM, int TN, int TM, int NS, int KW, bool kWide, class Stage>
-__device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Stage &st3, float *bias_s, const uint8_t *__restrict__ qx,
-                                         const float *__restrict__ sx, const uint8_t *__restrict__ qw,
-                                         const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N,
-                                         int K, void *__restrict__ Y, int n0, int m0) {
+__device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, float *bias_s,
+                                         const uint8_t *__restrict__ qx, const float *__restrict__ sx,
+                                         const uint8_t *__restrict__ qw, const float *__restrict__ sw,
+                                         const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
+                                         int n0, int m0) {
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, NW = WN * WM, kThreads = 64 * NW * KW;
     using Frag = std::conditional_t<kWide, F8Wide, F8Codes>;
     const int tid = threadIdx.x;
@@ -195,22 +197,24 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
     const int wblock = (n0 + wn * 16 * TN) / kF8Block;
     const float *swr = sw + (size_t)(wblock < (N + kF8Block - 1) / kF8Block ? wblock : 0) * G;
     // The scales of the wave's 16 TM tokens go to LDS with the stage, one load
-    // of 4 bytes a lane (zeros past M); a wave's loads per stage are kLoads and
-    // this one, all of them to LDS, so that a wait can count them.
+    // of 4 bytes a lane (zeros past M, and for a group past K: an infinite scale
+    // would make NaN of its zeros); a wave's loads per stage are kLoads and this
+    // one, all of them to LDS, so that a wait can count them.
     static_assert(TM <= 4, "a lane per token");
     float raw[TM], sc[TM];
     const int first_m = m0 + wm * TM * 16;
     auto load_scales = [&](int s, Stage &st) __attribute__((always_inline)) {
-        const int g = min(s * KW + kw, G - 1);
-        const __amdgpu_buffer_rsrc_t r =
-            fp8_rsrc(sx + (size_t)g * M + min(first_m, M - 1), 4u * (uint32_t)max(0, min(16 * TM, M - first_m)));
+        const int g = s * KW + kw;
+        const __amdgpu_buffer_rsrc_t r = fp8_rsrc(sx + (size_t)min(g, G - 1) * M + min(first_m, M - 1),
+                                                  g < G ? 4u * (uint32_t)max(0, min(16 * TM, M - first_m)) : 0u);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (f8_lds_void *)st.group[kw].scale[wave], 4, 4u * (uint32_t)lane, 0,
                                                  0, 0);
     };
 
     for (int i = tid; i < BN; i += kThreads)
         bias_s[i] = bias && n0 + i < N ? bf16_bits_to_f32(bias[n0 + i]) : 0.0f;
-    auto stage = [&](int i) -> Stage & { return i == 0 ? st0 : i == 1 ? st1 : i == 2 ? st2 : st3; };
+    static_assert(NS == 2 || NS == 3, "stages");
+    auto stage = [&](int i) -> Stage & { return i == 0 ? st0 : i == 1 ? st1 : st2; };
 #pragma unroll
     for (int f = 0; f < NS - 1; ++f) {
         aim(f);
@@ -277,7 +281,8 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, Sta
     };
     auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
         next_stage();
-        const float weight_scale = swr[min(s * KW + kw, G - 1)];
+        const int g = s * KW + kw;
+        const float weight_scale = fp8_scale_within(swr[min(g, G - 1)], g, G);
         aim(s + NS - 1);
         load_scales(s + NS - 1, nxt);
 #pragma unroll
@@ -401,17 +406,12 @@ __global__ __launch_bounds__(64 * WN * WM * KW, 1) void fp8_gemm_kernel(
     int tile_n, tile_m;
     fp8_tile_of_block(blockIdx.x, gridDim.x, gridDim.x, tiles_n, tile_n, tile_m);
     if constexpr (NS == 2) {
-        fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * BN,
+        fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st0, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * BN,
                                             tile_m * BM);
     } else {
         __shared__ __attribute__((aligned(16))) Stage st2;
-        __shared__ __attribute__((aligned(16))) std::conditional_t<(NS > 3), Stage, char> st3;
-        if constexpr (NS == 3)
-            fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st2, st0, bias_s, qx, sx, qw, sw, bias, M, N, K, Y,
-                                                tile_n * BN, tile_m * BM);
-        else
-            fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st2, st3, bias_s, qx, sx, qw, sw, bias, M, N, K, Y,
-                                                tile_n * BN, tile_m * BM);
+        fp8_tile<WN, WM, TN, TM, NS, KW, kWide>(st0, st1, st2, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * BN,
+                                            tile_m * BM);
     }
 }
 
@@ -428,36 +428,35 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
     const int b = blockIdx.x;
     if (b < whole) {
         fp8_tile_of_block(b, whole, tiles, tiles_n, tile_n, tile_m);
-        fp8_tile<2, 4, 8, 4, 2, 1, false>(st0, st1, st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256, tile_m * 256);
+        fp8_tile<2, 4, 8, 4, 2, 1, false>(st0, st1, st0, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256,
+                                          tile_m * 256);
     } else {
         const int id = whole + (b - whole) / 2, m0_half = (b - whole) % 2 * 128;
         fp8_tile_at(id, tiles, tiles_n, tile_n, tile_m);
         if (tile_m * 256 + m0_half < M)
-            fp8_tile<4, 2, 4, 4, 2, 1, false>(st0, st1, st0, st1, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256,
-                                        tile_m * 256 + m0_half);
+            fp8_tile<4, 2, 4, 4, 2, 1, false>(st0, st1, st0, bias_s, qx, sx, qw, sw, bias, M, N, K, Y, tile_n * 256,
+                                              tile_m * 256 + m0_half);
     }
 }
 
 // ---- the product, few tokens -----------------------------------------------
 
-// One block computes 16 output columns of at most 16 MT tokens; its W waves
-// take the groups of K in turn (wave w groups w, w + W, ...), `Ahead` of them
-// in flight, straight from global memory into the operands of the 16x16x128
-// MFMA (weights as A: row = output column; tokens as B), and add their sums in
-// LDS in a fixed order. The weight is read once: HBM-bound.
-// kFused (MT 1): from bf16 activations. While its first weights are on their
-// way, each block quantizes all tokens' features into LDS, exactly as the
-// activation pass does, which saves that launch; dynamic LDS: the codes
-// [M][K rounded up to groups], then the scales [G][M].
-template <int W, int MT, int Ahead, bool kWide, bool kFused>
-__global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(const uint8_t *__restrict__ qx,
-                                                            const float *__restrict__ sx,
-                                                            const uint16_t *__restrict__ X,
-                                                            const uint8_t *__restrict__ qw,
-                                                            const float *__restrict__ sw,
-                                                            const uint16_t *__restrict__ bias, int M, int N, int K,
-                                                            void *__restrict__ Y) {
-    __shared__ f32x4 red[W][MT][64];
+// One block computes 16 output columns of at most 16 tokens; its 8 waves take
+// the groups of K in turn (wave w groups w, w + 8, ...), `Ahead` of them in
+// flight, straight from global memory into the operands of the 16x16x128 MFMA
+// (weights as A: row = output column; tokens as B), and add their sums in LDS
+// in a fixed order. The weight is read once: HBM-bound.
+// kFused: from bf16 activations. While its first weights are on their way, each
+// block quantizes all tokens' features into LDS, exactly as the activation pass
+// does, which saves that launch; dynamic LDS: the codes [M][K rounded up to
+// groups], then the scales [G][M].
+template <int Ahead, bool kWide, bool kFused>
+__global__ __launch_bounds__(64 * kF8SkinnyWaves) void fp8_skinny_kernel(
+    const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint16_t *__restrict__ X,
+    const uint8_t *__restrict__ qw, const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N,
+    int K, void *__restrict__ Y) {
+    constexpr int W = kF8SkinnyWaves;
+    __shared__ f32x4 red[W][64];
     extern __shared__ __align__(16) uint8_t codes_s[];
     const int n0 = blockIdx.x * 16;
     const int lane = threadIdx.x & 63;
@@ -481,12 +480,8 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(const uint8_t *__res
             __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k + 64 < K ? off + 64 : kF8Oob, 0, 0)));
     };
 
-    f32x4 acc[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int mrow[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) mrow[j] = min(16 * j + r16, M - 1);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    const int mrow = min(r16, M - 1);
 
     i32x8 a[Ahead];
 #pragma unroll
@@ -509,48 +504,44 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(const uint8_t *__res
 #pragma unroll
             for (int u = 0; u < Ahead; ++u) a[u] = operand(rw, r16, g0 + W * u);
         }
-        i32x8 b[Ahead][MT];
-        float s[Ahead][MT];
+        i32x8 b[Ahead];
+        float s[Ahead];
         if constexpr (!kFused) {
 #pragma unroll
-            for (int u = 0; u < Ahead; ++u)
-#pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    const int g = g0 + W * u;
-                    b[u][j] = operand(rx, mrow[j], g);
-                    s[u][j] = sx[(size_t)min(g, G - 1) * M + mrow[j]] * swr[min(g, G - 1)];
-                }
+            for (int u = 0; u < Ahead; ++u) {
+                const int g = g0 + W * u;
+                b[u] = operand(rx, mrow, g);
+                s[u] = sx[(size_t)min(g, G - 1) * M + mrow] * swr[min(g, G - 1)];
+            }
         }
         __builtin_amdgcn_sched_barrier(0);  // all of them under way before the first is used
-        // groups past K: zero weights add nothing, so no branch waits on them
+        // groups past K: zero weights and a zero scale add nothing, so no branch
+        // waits on them
 #pragma unroll
         for (int u = 0; u < Ahead; ++u) {
+            const int g = min(g0 + W * u, G - 1);
             if constexpr (kFused) {
-                const int g = min(g0 + W * u, G - 1);
-                const uint8_t *at = codes_s + ((size_t)mrow[0] * G + g) * kF8Block + 16 * q4;
-                b[u][0] = join(*reinterpret_cast<const u32x4 *>(at), *reinterpret_cast<const u32x4 *>(at + 64));
-                s[u][0] = scales_s[g * M + mrow[0]] * swr[g];
+                const uint8_t *at = codes_s + ((size_t)mrow * G + g) * kF8Block + 16 * q4;
+                b[u] = join(*reinterpret_cast<const u32x4 *>(at), *reinterpret_cast<const u32x4 *>(at + 64));
+                s[u] = scales_s[g * M + mrow] * swr[g];
             }
+            const float scale = fp8_scale_within(s[u], g0 + W * u, G);
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            const f32x4 p = kWide ? mfma_wide_16x16x128(a[u], b[u], zero) : mfma_fp8_16x16x128(a[u], b[u], zero);
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                const f32x4 p = kWide ? mfma_wide_16x16x128(a[u], b[u][j], zero) : mfma_fp8_16x16x128(a[u], b[u][j], zero);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(s[u][j], p[e], acc[j][e]);
-            }
+            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(scale, p[e], acc[e]);
         }
     }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) red[wave][j][lane] = acc[j];
+    red[wave][lane] = acc;
     __syncthreads();
-    for (int i = threadIdx.x; i < 256 * MT; i += 64 * W) {
-        const int m = i >> 4, c = i & 15;  // consecutive threads: consecutive columns of a token
-        const int src = 16 * (c >> 2) + (m & 15);
+    if (threadIdx.x < 256) {
+        const int m = threadIdx.x >> 4, c = threadIdx.x & 15;  // consecutive threads: consecutive columns of a token
+        const int src = 16 * (c >> 2) + m;
         const int n = n0 + c;
         if (m < M && n < N) {
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) v += red[w][m >> 4][src][c & 3];
+            for (int w = 0; w < W; ++w) v += red[w][src][c & 3];
             if (bias) v += bf16_bits_to_f32(bias[n]);
             if constexpr (kWide)
                 static_cast<float *>(Y)[(size_t)m * N + n] = v;
@@ -575,8 +566,8 @@ static hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t 
                               const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM;
     const int tiles_n = (N + BN - 1) / BN, tiles_m = (M + BM - 1) / BM;
-    hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, TN, TM, NS, KW, kWide>), dim3(tiles_n * tiles_m), dim3(64 * WN * WM * KW), 0,
-                       stream, qx, sx, qw, sw, bias, M, N, K, Y, tiles_n);
+    hipLaunchKernelGGL((fp8_gemm_kernel<WN, WM, TN, TM, NS, KW, kWide>), dim3(tiles_n * tiles_m),
+                       dim3(64 * WN * WM * KW), 0, stream, qx, sx, qw, sw, bias, M, N, K, Y, tiles_n);
     return hipGetLastError();
 }
 
@@ -584,7 +575,7 @@ template <bool kWide>
 static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                               const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
     if (M <= kF8SkinnyTokens) {
-        hipLaunchKernelGGL((fp8_skinny_kernel<8, 1, 2, kWide, false>), dim3((N + 15) / 16), dim3(512), 0, stream, qx, sx,
+        hipLaunchKernelGGL((fp8_skinny_kernel<2, kWide, false>), dim3((N + 15) / 16), dim3(512), 0, stream, qx, sx,
                            nullptr, qw, sw, bias, M, N, K, Y);
         return hipGetLastError();
     }
@@ -619,7 +610,7 @@ template <bool kWide>
 static hipError_t launch_few(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias, int M, int N,
                              int K, void *Y, hipStream_t stream) {
     const size_t lds = (size_t)M * fp8_blocks(K) * (kF8Block + sizeof(float));
-    hipLaunchKernelGGL((fp8_skinny_kernel<8, 1, 3, kWide, true>), dim3((N + 15) / 16), dim3(512), lds, stream, nullptr,
+    hipLaunchKernelGGL((fp8_skinny_kernel<3, kWide, true>), dim3((N + 15) / 16), dim3(512), lds, stream, nullptr,
                        nullptr, X, qw, sw, bias, M, N, K, Y);
     return hipGetLastError();
 }

@@ -30,8 +30,7 @@ __device__ __forceinline__ void fp8_barrier() {
 }
 
 // E4M3 x E4M3 with fp32 accumulation, unscaled. A lane's operand is 32 codes
-// of one row (A) or column (B); the 32x32 output layout is that of the other
-// 32x32 MFMAs. The matrix core adds the 8 products of a lane's 8 consecutive
+// of one row (A) or column (B). The matrix core adds the 8 products of a lane's 8 consecutive
 // codes aligned to the largest of them and cuts what lies 14 or more bits
 // below its leading one (measured: 2^16 + 2^3 is exact, 2^16 + 7.5 gives
 // 2^16); everything else is summed as in fp32. That is a relative error of
@@ -39,12 +38,14 @@ __device__ __forceinline__ void fp8_barrier() {
 // two hundred times that of fp32, so outputs in fp32 take the bf16 MFMA
 // (mfma_wide_*), whose operands hold E4M3 values exactly and whose sums keep
 // 24 bits.
-__device__ __forceinline__ f32x16 mfma_fp8_32x32x64(i32x8 a, i32x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-
 __device__ __forceinline__ f32x4 mfma_fp8_16x16x128(i32x8 a, i32x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// The scale of group g, or 0 past the last of G groups: an infinite one would
+// make NaN of the zeros there. A mask, as a branch makes the compiler spill.
+__device__ __forceinline__ float fp8_scale_within(float scale, int g, int G) {
+    return __uint_as_float(__float_as_uint(scale) & (uint32_t)((g - G) >> 31));
 }
 
 // Eight E4M3 codes as bf16 values (exact).
@@ -57,13 +58,7 @@ __device__ __forceinline__ bf16x8 fp8_widen8(uint32_t a, uint32_t b) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// The products of the two functions above on bf16 MFMAs.
-__device__ __forceinline__ f32x16 mfma_wide_32x32x64(i32x8 a, i32x8 b, f32x16 c) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) c = mfma_bf16_32x32x16(fp8_widen8(a[i], a[i + 1]), fp8_widen8(b[i], b[i + 1]), c);
-    return c;
-}
-
+// The same product on bf16 MFMAs.
 __device__ __forceinline__ f32x4 mfma_wide_16x16x128(i32x8 a, i32x8 b, f32x4 c) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) c = mfma_bf16_16x16x32(fp8_widen8(a[i], a[i + 1]), fp8_widen8(b[i], b[i + 1]), c);

@@ -375,9 +375,9 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     int turn = 0;
     // one step: its products; the sums and the output behind an item's last one
     auto compute = [&](const Step &now, Place &p) __attribute__((always_inline)) {
-        const int g = min(p.step * kUpWaves + wave, G - 1);
-        const size_t block = ((size_t)p.e * 2 * gi + p.i0 / kF8Block) * G + g;
-        const float wg = s13[block], wu = s13[block + (size_t)gi * G];
+        const int g = p.step * kUpWaves + wave;
+        const size_t block = ((size_t)p.e * 2 * gi + p.i0 / kF8Block) * G + min(g, G - 1);
+        const float wg = fp8_scale_within(s13[block], g, G), wu = fp8_scale_within(s13[block + (size_t)gi * G], g, G);
         f32x4 pg = {0.f, 0.f, 0.f, 0.f}, pu = pg;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -165,6 +165,20 @@ def test_a_token_with_nan_or_inf_stays_alone(M):
     assert np.all(np.isnan(y[[0, 2]])) and np.array_equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(5, 136), (40, 136), (300, 264), (700, 2056), (1800, 2056), (2100, 2056), (4100, 2056)])
+def test_scales_past_the_largest_number_give_infinities(M, N, out):
+    # one and three groups of 128: stages and waves without a group add nothing, not infinity times zero
+    t = H.torch()
+    for K in (128, 384):
+        qx, qw = t.full((M, K), 0x38, dtype=t.uint8, device="cuda"), t.full((N, K), 0xB8, dtype=t.uint8, device="cuda")
+        sx, sw = t.full((K // 128, M), 1e30, device="cuda"), t.full((b.fp8_blocks(N), K // 128), 1e30, device="cuda")
+        Y = out_tensor(M, N, out)
+        b.svdq_fp8_gemm(qx, sx, qw, sw, None, Y[:M])
+        t.cuda.synchronize()
+        assert np.all(np.isneginf(y_of(Y, M, out)))
+
+
 def test_linear_no_tokens():
     t = H.torch()
     qw, sw = weight(128, 16, 1)
@@ -274,6 +288,18 @@ def test_moe_not_finite_tokens_and_experts_stay_alone():
     assert np.array_equal(y2, y[clean])
 
 
+def test_moe_weight_scales_past_the_largest_number():
+    # 3 of 8 waves have a group of H: the others add nothing to gate's infinity, and silu(inf) inf = inf
+    t = H.torch()
+    H_, I, E = 272, 32, 2  # noqa: E741
+    bits = wl.bf16_bits_from_f32(np.full((1, H_), 2.0 ** 20, np.float32))
+    w13, w2 = np.full((E, 2, I, H_), 0x38, np.uint8), np.full((E, H_, I), 0x38, np.uint8)
+    s13, s2 = np.full((E, 2, 1, 3), np.inf, np.float32), np.ones((E, 3, 1), np.float32)
+    wr = wl.bf16_bits_from_f32(np.ones((E, H_), np.float32))
+    Y, idx, gate = run_moe(bits, wr, (w13, s13, w2, s2), 2)
+    assert np.all(np.isposinf(y_of(Y, 1, "bf16"))) and np.all(gate == 0.5)
+
+
 def test_moe_no_tokens():
     t = H.torch()
     wr, *w = experts(4, 64, 32, 1)
@@ -341,6 +367,28 @@ def test_on_another_stream_and_replayed_from_a_graph():
         t.cuda.synchronize()
         assert all(np.array_equal(H.host(d[n]), v) for n, v in zip(("P", "Y", "idx", "gate"), got))
     assert all(np.array_equal(v, u) for v, u in zip(got, want))
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    t = H.torch()
+    layers, want = [], []
+    for T in (9, 40):
+        _, _, _, d = _layer(t, T=T)
+        _run_layer(d)
+        t.cuda.synchronize()
+        want.append([H.host(d[n]).copy() for n in ("P", "Y", "idx", "gate")])
+        layers.append(d)
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    for d in layers:
+        for n in ("P", "Y", "idx", "gate"):
+            d[n].zero_()
+    t.cuda.synchronize()
+    for _ in range(20):
+        for d, s in zip(layers, streams):
+            _run_layer(d, stream=s)
+    t.cuda.synchronize()
+    for d, w in zip(layers, want):
+        assert all(np.array_equal(H.host(d[n]), v) for n, v in zip(("P", "Y", "idx", "gate"), w))
 
 
 @pytest.mark.parametrize("M", [1, 20, 200])
