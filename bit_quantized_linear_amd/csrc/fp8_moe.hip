@@ -208,8 +208,9 @@ constexpr int kRouteInUp = 128;
 
 // The reached experts (ascending; a single token's in the order of its choices)
 // and the pairs t top_k + j sorted by expert, then token: reached expert number
-// a has pairs pair[from[a]] .. pair[from[a + 1] - 1]. Written down for the down
-// projection as it is.
+// a has pairs pair[from[a]] .. pair[from[a + 1] - 1], each as token << 10 | pair
+// (a division in place of it costs as much as a load). Written down for the
+// down projection as it is.
 struct MoeTable {
     int32_t reached;
     uint16_t expert[SVDQ_FP8_MOE_MAX_EXPERTS];
@@ -217,6 +218,9 @@ struct MoeTable {
     uint16_t pair[kMaxPairs];
 };
 static_assert(sizeof(MoeTable) % 4 == 0, "copied in dwords");
+static_assert(kMaxPairs <= 1 << 10 && SVDQ_FP8_MOE_MAX_TOKENS <= 1 << 6, "both in 16 bits");
+__device__ __forceinline__ uint32_t pair_of(uint16_t v) { return v & 1023u; }
+__device__ __forceinline__ uint32_t token_of(uint16_t v) { return v >> 10; }
 
 // Built by a whole block from the choices. tokens: [256] of LDS, the set of an
 // expert's tokens as a bit each; an expert is at most once among a token's
@@ -274,7 +278,7 @@ __device__ __forceinline__ void build_table(const int32_t *idx, int T, int E, in
         if (set >> t & 1) {
             int j = 0;
             while (j < top_k - 1 && (int)choice(t * top_k + j) != e) ++j;
-            table.pair[table.from[a] + __popcll(set & ((1ull << t) - 1))] = (uint16_t)(t * top_k + j);
+            table.pair[table.from[a] + __popcll(set & ((1ull << t) - 1))] = (uint16_t)(t << 10 | (t * top_k + j));
         }
     }
     __syncthreads();
@@ -328,13 +332,12 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     // zeros).
     struct Place {
         int item, m0, step;
-        int e, i0, from, count;
+        int a, i0, e, from, count;  // a: the reached expert's number
     };
-    auto enter = [&](Place &p, int item) __attribute__((always_inline)) {
-        p.item = item;
+    const int next_a = (int)gridDim.x / tiles, next_i0 = (int)gridDim.x % tiles * 16;
+    auto enter = [&](Place &p) __attribute__((always_inline)) {
         p.m0 = p.step = 0;
-        const int a = min(item, items - 1) / tiles;
-        p.i0 = min(item, items - 1) % tiles * 16;
+        const int a = min(p.a, table.reached - 1);
         p.e = __builtin_amdgcn_readfirstlane(table.expert[a]);
         p.from = __builtin_amdgcn_readfirstlane(table.from[a]);
         p.count = __builtin_amdgcn_readfirstlane(table.from[a + 1]) - p.from;
@@ -344,7 +347,14 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
         p.step = 0;
         p.m0 += 16;
         if (p.m0 < p.count) return;
-        enter(p, p.item + (int)gridDim.x);
+        p.item += (int)gridDim.x;
+        p.a += next_a;
+        p.i0 += next_i0;
+        if (p.i0 >= I) {
+            p.i0 -= I;
+            ++p.a;
+        }
+        enter(p);
     };
     struct Step {
         u32x4 g[2], u[2], x[2][2];
@@ -355,7 +365,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
         const __amdgpu_buffer_rsrc_t rg = fp8_rsrc(we + (size_t)p.i0 * H, 16u * (uint32_t)H);
         const __amdgpu_buffer_rsrc_t ru = fp8_rsrc(we + (size_t)(I + p.i0) * H, 16u * (uint32_t)H);
         if (p.step == 0)  // the lane's token, as a byte offset; lanes without one read zeros
-            xrow = p.m0 + r16 < p.count ? (uint32_t)(table.pair[p.from + p.m0 + r16] / top_k) * (uint32_t)H * 2u
+            xrow = p.m0 + r16 < p.count ? token_of(table.pair[p.from + p.m0 + r16]) * (uint32_t)H * 2u
                                         : kMoeOob;
         const int k0 = (p.step * kUpWaves + wave) * kF8Block + 16 * q4;
 #pragma unroll
@@ -413,7 +423,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
             if (p.m0 + m < p.count) {
                 const float h = g / (1.0f + expf(-g)) * u;
                 const uint32_t hi = f32_to_bf16_bits(h);
-                const size_t at = (size_t)table.pair[p.from + p.m0 + m] * I + p.i0 + c;
+                const size_t at = (size_t)pair_of(table.pair[p.from + p.m0 + m]) * I + p.i0 + c;
                 h_hi[at] = (uint16_t)hi;
                 // no remainder of an infinity or NaN
                 h_lo[at] = (hi & 0x7F80u) == 0x7F80u ? 0 : (uint16_t)f32_to_bf16_bits(h - bf16_bits_to_f32(hi));
@@ -422,7 +432,10 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
         turn ^= 1;
     };
     Place at, ahead;
-    enter(at, blockIdx.x);
+    at.item = blockIdx.x;
+    at.a = (int)blockIdx.x / tiles;
+    at.i0 = (int)blockIdx.x % tiles * 16;
+    enter(at);
     ahead = at;
     Step ring[kUpRing];
     uint32_t xrow = 0;
@@ -476,14 +489,15 @@ constexpr int kDownSlots = 2;  // per wave, each of hi and lo
 constexpr int kDownTokens = 4 * kDownSlots;  // of an expert at a time
 
 // One block: 16 output columns of every token. A wave takes one reached expert
-// and one of `splits` shares of I at a time (a unit), reads its 16 weight rows
+// and one of 2^`shift` shares of I at a time (a unit; a wave's are all of the
+// same share), reads its 16 weight rows
 // once, a batch of groups ahead of their use, and leaves each pair's 16 sums in
 // LDS at its own place; then each output is the weighted sum over its token's
 // pairs in order, so the result does not depend on which wave came first.
 __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     const uint8_t *__restrict__ w2, const float *__restrict__ s2, const uint16_t *__restrict__ h_hi,
     const uint16_t *__restrict__ h_lo, const float *__restrict__ gate, const MoeTable *__restrict__ table_in, int T,
-    int H, int I, int top_k, int splits, uint16_t *__restrict__ Y) {
+    int H, int I, int top_k, int shift, uint16_t *__restrict__ Y) {
     __shared__ MoeTable table;
     extern __shared__ __align__(16) uint8_t smem[];  // slots [waves][2][kDownSlots], then sums [splits][T top_k][16]
     float *out = reinterpret_cast<float *>(smem + kDownWaves * 2 * kDownSlots * kSlot);
@@ -500,42 +514,38 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     for (int i = threadIdx.x; i < (int)sizeof(MoeTable) / 4; i += kDownThreads)
         reinterpret_cast<uint32_t *>(&table)[i] = reinterpret_cast<const uint32_t *>(table_in)[i];
     __syncthreads();
-    const int units = __builtin_amdgcn_readfirstlane(table.reached) * splits;
+    const int splits = 1 << shift, s = wave & (splits - 1);
+    const int reached = __builtin_amdgcn_readfirstlane(table.reached);
+    const int all = (G - s + splits - 1) >> shift;  // groups of a unit
 
-    // where a wave is: batch `first` (of the unit's groups) for tokens m0 ...
+    // where a wave is (a: the reached expert's number): batch `first` (of the unit's groups) for tokens m0 ...
     struct Place {
-        int unit, e, from, count, m0, first;
+        int a, e, from, count, m0, first;
     };
     auto enter = [&](Place &p) __attribute__((always_inline)) {
-        if (p.unit < units) {
-            const int a = p.unit / splits;
-            p.e = __builtin_amdgcn_readfirstlane(table.expert[a]);
-            p.from = __builtin_amdgcn_readfirstlane(table.from[a]);
-            p.count = __builtin_amdgcn_readfirstlane(table.from[a + 1]) - p.from;
+        if (p.a < reached) {
+            p.e = __builtin_amdgcn_readfirstlane(table.expert[p.a]);
+            p.from = __builtin_amdgcn_readfirstlane(table.from[p.a]);
+            p.count = __builtin_amdgcn_readfirstlane(table.from[p.a + 1]) - p.from;
         }
         p.m0 = p.first = 0;
     };
-    auto groups = [&](const Place &p) __attribute__((always_inline)) {
-        const int s = p.unit % splits;
-        return (G - s + splits - 1) / splits;
-    };
     auto advance = [&](Place &p) __attribute__((always_inline)) {
         p.first += kDownAhead;
-        if (p.first < groups(p)) return;
+        if (p.first < all) return;
         p.first = 0;
         p.m0 += kDownTokens;
         if (p.m0 < p.count) return;
-        p.unit += kDownWaves;
+        p.a += kDownWaves >> shift;
         enter(p);
     };
     auto load_weights = [&](u32x4(&to)[kDownAhead][2], const Place &p) __attribute__((always_inline)) {
         const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(w2 + ((size_t)p.e * H + n0) * I, 16u * (uint32_t)I);
-        const int s = p.unit % splits;
 #pragma unroll
         for (int n = 0; n < kDownAhead; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int k = (s + (p.first + n) * splits) * kF8Block + 64 * i + 16 * q4;
+                const int k = (s + ((p.first + n) << shift)) * kF8Block + 64 * i + 16 * q4;
                 to[n][i] = load16(rw, k < I ? (uint32_t)r16 * (uint32_t)I + (uint32_t)k : kMoeOob);  // zeros past I
             }
     };
@@ -543,13 +553,12 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     // one batch from `now`, the next one's weights to `next`
     auto batch = [&](Place &p, const u32x4(&now)[kDownAhead][2], u32x4(&next)[kDownAhead][2])
                      __attribute__((always_inline)) {
-        const int s = p.unit % splits, all = groups(p);
         const int here = min(kDownTokens, p.count - p.m0), per = slots_of(here);
         const Place at = p;
         uint32_t row[kDownSlots];
 #pragma unroll
         for (int q = 0; q < kDownSlots; ++q)
-            row[q] = (uint32_t)table.pair[at.from + at.m0 + min(4 * q + q4, here - 1)] * (uint32_t)I * 2u;
+            row[q] = pair_of(table.pair[at.from + at.m0 + min(4 * q + q4, here - 1)]) * (uint32_t)I * 2u;
         const float *sw = s2 + ((size_t)at.e * gh + n0 / kF8Block) * G;
         if (at.first == 0) acc = f32x4{0.f, 0.f, 0.f, 0.f};
         advance(p);
@@ -559,13 +568,13 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what they held has been read
 #pragma unroll
                 for (int q = 0; q < kDownSlots; ++q) {
-                    const int k = (s + (at.first + n + q / per) * splits) * kF8Block;
-                    load_slot(rh, slots + q * kSlot, q % per ? row[1] : row[0], k, I, chunk);
-                    load_slot(rl, slots + (kDownSlots + q) * kSlot, q % per ? row[1] : row[0], k, I, chunk);
+                    const int k = (s + ((at.first + n + (per == 1 ? q : 0)) << shift)) * kF8Block;
+                    load_slot(rh, slots + q * kSlot, q && per > 1 ? row[1] : row[0], k, I, chunk);
+                    load_slot(rl, slots + (kDownSlots + q) * kSlot, q && per > 1 ? row[1] : row[0], k, I, chunk);
                 }
                 // the slots are there; the next batch's 2 kDownAhead loads may stay under way
                 __builtin_amdgcn_sched_barrier(0);
-                if (n == 0 && p.unit < units) {
+                if (n == 0 && p.a < reached) {
                     load_weights(next, p);
                     __builtin_amdgcn_sched_barrier(0);
                     __builtin_amdgcn_s_waitcnt(0x0F70 | 2 * kDownAhead);  // vmcnt(2 kDownAhead)
@@ -587,22 +596,22 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
                 sum = mfma_bf16_16x16x32(a0, slot_read(hi, token, c), sum);
                 sum = mfma_bf16_16x16x32(a1, slot_read(hi, token, c + 1), sum);
             }
-            const float w = sw[s + (at.first + n) * splits];
+            const float w = sw[s + ((at.first + n) << shift)];
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w, sum[i], acc[i]);
         }
         if (at.first + kDownAhead >= all && r16 < here)
-            *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + table.pair[at.from + at.m0 + r16]) * 16 + 4 * q4) =
+            *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + pair_of(table.pair[at.from + at.m0 + r16])) * 16 + 4 * q4) =
                 acc;
     };
     Place p;
-    p.unit = wave;
+    p.a = wave >> shift;
     enter(p);
     u32x4 c0[kDownAhead][2], c1[kDownAhead][2];
-    if (p.unit < units) load_weights(c0, p);
-    while (p.unit < units) {
+    if (p.a < reached) load_weights(c0, p);
+    while (p.a < reached) {
         batch(p, c0, c1);
-        if (p.unit >= units) break;
+        if (p.a >= reached) break;
         batch(p, c1, c0);
     }
     __syncthreads();
@@ -677,11 +686,11 @@ hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *
     // as many shares of I as give every wave a unit, at most one per group and
     // what 32 KB of LDS hold
     const int G = fp8_blocks(I);
-    int splits = std::min((kDownWaves + most - 1) / most, G);
-    while (splits > 1 && splits * pairs * 64 > (32 << 10)) --splits;
-    const size_t lds = (size_t)kDownWaves * 2 * kDownSlots * kSlot + (size_t)splits * pairs * 64;
+    int shift = 0;
+    while (most << shift < kDownWaves && 2 << shift <= G && (2 << shift) * pairs * 64 <= (32 << 10)) ++shift;
+    const size_t lds = (size_t)kDownWaves * 2 * kDownSlots * kSlot + ((size_t)pairs * 64 << shift);
     hipLaunchKernelGGL(moe_down_kernel, dim3(H / 16), dim3(kDownThreads), lds, stream, w2, s2, h_hi, h_lo, gate, table,
-                       T, H, I, top_k, splits, Y);
+                       T, H, I, top_k, shift, Y);
     return hipGetLastError();
 }
 
