@@ -36,6 +36,9 @@ constexpr int kF8QGroups = 4;   // groups of 128 features per block
 // puts NaN above all, so a NaN reaches the scale). All four loads of a thread
 // are in flight together. The scales of the block go through LDS so that 16
 // tokens' scales of a group are stored as one 64-byte segment.
+// HBM-bound: 3 bytes and a group's scale per feature, each once; 32760 x 5120
+// takes 102 us, 5.0 TB/s, the rate of a large copy (16 x 5120: 3.5 us, of which
+// an empty launch is 2 to 3).
 __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_t *__restrict__ X, int M, int K,
                                                                    int G, uint8_t *__restrict__ qx,
                                                                    float *__restrict__ sx) {
@@ -72,7 +75,8 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
 constexpr uint32_t kF8Oob = 0x80000000u;
 constexpr int kF8Cus = 256;  // compute units
 constexpr int kF8SkinnyWaves = 8;
-constexpr int kF8SkinnyTokens = 16;  // one MFMA tile: 20 x 5120 x 5120 takes 14.6 us with two, 11.4 in tiles of 64
+// one MFMA tile: with two, 20 x 5120 x 5120 took 14.6 us, in tiles of 64 it takes 10.8
+constexpr int kF8SkinnyTokens = 16;
 constexpr size_t kF8FusedLds = 40 << 10;  // the linear in one launch: LDS for its codes and scales
 
 typedef __attribute__((address_space(3))) void f8_lds_void;
@@ -124,7 +128,11 @@ struct F8Wide {
 // lane fetches the global chunk that belongs at the position it writes. Rows
 // past N or M and chunks past K read zeros (their offset is past the buffer).
 // One 16x16x128 MFMA is a whole group of a tile, so its result is scaled and
-// added (4 FMAs a lane) while the next row tile's MFMAs run.
+// added (4 FMAs a lane) while the next row tile's MFMAs run: the 16 x 16 x 128
+// MFMA and not the 32 x 32 x 64 one, whose results take two per group and four
+// times the registers (2150 against 2550 TFLOP/s at 32768 x 5120 x 5120).
+// NS stages take turns, loads NS - 1 ahead. KW = 2: two halves of the block
+// share K and add their sums at the end, for grids too small to fill the chip.
 // kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
 template <int WN, int WM, int TN, int TM, int NS, int KW, bool kWide, class Stage>
 __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, float *bias_s,
@@ -416,7 +424,13 @@ __global__ __launch_bounds__(64 * WN * WM * KW, 1) void fp8_gemm_kernel(
 }
 
 // 256 x 256 tiles, of which the grid's first `whole` blocks take one each; two
-// blocks share each of the others (128 of its tokens each).
+// blocks share each of the others (128 of its tokens each). 8 waves, one block
+// per compute unit: 130 KB of LDS hold two stages, and a stage's operands feed
+// 4 times the MFMAs that they take LDS reads for. Bound by the matrix cores: they
+// are busy 61 % of the time, at the clock that their power leaves (32760 x 5120 x
+// 5120: 690 to 725 us, 2.37 to 2.5 PFLOP/s; the library's product of the same
+// codes with one scale for all, 650 us). The rest is the epilogue, which nothing
+// overlaps (one tile's output is 128 KB), and the fill of each tile's first stage.
 __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
     const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N, int K, void *__restrict__ Y,
@@ -445,7 +459,11 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 // the groups of K in turn (wave w groups w, w + 8, ...), `Ahead` of them in
 // flight, straight from global memory into the operands of the 16x16x128 MFMA
 // (weights as A: row = output column; tokens as B), and add their sums in LDS
-// in a fixed order. The weight is read once: HBM-bound.
+// in a fixed order. The weight is read once: bound by HBM, and at these sizes by
+// the way to the first of it (a launch, a load's latency, the sums): 13 x 2048 x
+// 12288 takes 8.2 us (25 MB, 3.1 TB/s), 1 x 5120 x 5120 in one launch 8.9 (26 MB,
+// 2.9 TB/s). More groups in flight than 2 or 3 cost more by the waves that their
+// registers keep out than they hide.
 // kFused: from bf16 activations. While its first weights are on their way, each
 // block quantizes all tokens' features into LDS, exactly as the activation pass
 // does, which saves that launch; dynamic LDS: the codes [M][K rounded up to
@@ -580,14 +598,18 @@ static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t 
         return hipGetLastError();
     }
     // Tiles of t x t: the larger, the less each operand is read; the smaller,
-    // the more compute units have one. Times in us for M x 5120 x 5120, by the
-    // rule / the next smaller or larger tile: bf16, M = 128 12.8 / 16.6, 256
-    // 19.6 / 24.1, 512 24.7 / 28.7, 1024 39.9 / 45.8, 2048 58.6 / 71.8.
+    // the more compute units have one. Times in us for bf16, M x 5120 x 5120, by
+    // the rule / by the next smaller or larger tile: M = 17 10.8 / 14.1, 192 12.7
+    // / 15.7 (64, K in halves / not), 256 19.3 / 22.9, 384 22.1 / 24.9 (64 / K in
+    // halves, 128), 512 24.4 / 28.5, 768 27.2 / 39.4 (128, three stages / 64), 1024
+    // 38.0 / 48.9, 1536 44.3 / 46.6 (128, two stages / three, 256), 2048 57 / 75
+    // (256 / 128), 4096 108 / 123 (the last round's tiles shared / not).
     const auto tiles = [&](int64_t tn, int64_t tm) { return ((N + tn - 1) / tn) * ((M + tm - 1) / tm); };
     const int64_t small = tiles(64, 64);
     if (small <= kF8Cus) return launch_tile<2, 2, 2, 2, 3, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     if constexpr (kWide) {
-        // fp32: M = 256 30.9 / 33.6, 1024 68.4 / 77.3, 2048 132 / 151, 4608 234 / 298
+        // fp32: M = 128 19.1 / 26.4 (K in halves / not), 256 32.1 / 35.7, 1024 68.9 /
+        // 75.1 (64 / K in halves, 128), 1280 75.1 / 89.7, 4608 232 / 292 (128 / 64)
         if (small <= 6 * kF8Cus) return launch_tile<2, 2, 2, 2, 3, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
         return launch_tile<2, 2, 4, 4, 2, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     } else {

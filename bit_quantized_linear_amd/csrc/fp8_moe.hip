@@ -11,7 +11,11 @@
 // not make them themselves); the gate and up projections, one block per reached
 // expert and 16 intermediate columns; the down projection with the weighted
 // sum, one block per 16 output columns. Each reached expert's weights are read
-// once, so the layer is bound by HBM.
+// once, so the layer is bound by HBM: 64 tokens of 128 experts (H 4096, I 1408, 8
+// choices) take 447 us, 4.9 TB/s over all launches; for few bytes by the chain of
+// dependent loads: a token's logits, its choice, the experts' weights, then h and
+// again weights, in three launches about 1.1 us apart (1 token, H 2048, I 768, 8 of
+// 64 experts: 22 us, of which the weights alone would take 7.5).
 
 #include <hip/hip_runtime.h>
 
@@ -45,7 +49,9 @@ constexpr int kLogitExperts = 2;  // per block
 // turn, 8 a lane. bf16 values are widened to fp64 and multiplied and added
 // there, so that the order of two logits is the exact one up to 2^-50. The
 // lanes' sums are folded so that each step halves the sums a lane holds, the
-// waves' added in LDS in order.
+// waves' added in LDS in order. Bound by the fp64 arithmetic and its conversions
+// for many tokens (64 x 4096 x 128: 8.4 us; 4 tokens share a weight's), by
+// latency for one (1 x 2048 x 64: 2.8 us).
 template <int TB>
 __global__ __launch_bounds__(64 * kLogitWaves) void moe_logits_kernel(const uint16_t *__restrict__ X,
                                                                       const uint16_t *__restrict__ wr, int T, int H,
@@ -188,7 +194,7 @@ __device__ __forceinline__ void write_choices(const double *logit, const int32_t
 
 constexpr int kRouteThreads = kParts * SVDQ_FP8_MOE_MAX_EXPERTS;
 
-// One block per token.
+// One block per token. Latency: 4.7 us for 128 experts, 3.6 for 40.
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *__restrict__ logits, int E, int top_k,
                                                                   int renorm, int32_t *__restrict__ idx,
                                                                   float *__restrict__ gate) {
@@ -200,8 +206,9 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *
 }
 
 // Up to this many (token, expert) pairs the up kernel's blocks make the choices
-// themselves (one token of 64 experts: 22.8 us in three launches, 26.5 in four;
-// 23 of 40: 35.3 and 31.6, as every block does all the comparisons).
+// themselves (a layer for one token of 64 experts: 22.8 us in three launches,
+// 26.5 in four; for 23 of 40: 35.3 and 31.6, as every block does all the
+// comparisons).
 constexpr int kRouteInUp = 128;
 
 // ---- the reached experts ---------------------------------------------------------
@@ -297,7 +304,10 @@ constexpr int kUpRing = 3;      // steps under way per wave
 // the time. h is written as the sum of two bf16 numbers (hi + lo, 16
 // significant bits), so that its rounding stays far below that of Y. kRoute:
 // every block also makes the choices, which saves a launch. Block 0 writes the
-// table down for the down projection.
+// table down for the down projection. HBM-bound: 64 tokens, H 4096, I 1408, 128
+// experts 280 us (1.48 GB, 5.3 TB/s); at 4 tokens per expert the activations'
+// loads take the address units as long as the weights', so that more than 3
+// steps ahead, or the next item's weights fetched into the L2, gave nothing.
 template <bool kRoute>
 __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     const uint16_t *__restrict__ X, const uint8_t *__restrict__ w13, const float *__restrict__ s13,
@@ -485,20 +495,25 @@ __device__ __forceinline__ int slots_of(int tokens) { return tokens <= 4 ? 1 : 2
 // ---- down projection and weighted sum ----------------------------------------
 
 constexpr int kDownAhead = 4;  // groups of weights per set; two sets take turns
-constexpr int kDownSlots = 2;  // per wave, each of hi and lo
-constexpr int kDownTokens = 4 * kDownSlots;  // of an expert at a time
+constexpr int kDownTokens = 8;  // of an expert at a time
 
 // One block: 16 output columns of every token. A wave takes one reached expert
-// and one of 2^`shift` shares of I at a time (a unit; a wave's are all of the
-// same share), reads its 16 weight rows
-// once, a batch of groups ahead of their use, and leaves each pair's 16 sums in
-// LDS at its own place; then each output is the weighted sum over its token's
-// pairs in order, so the result does not depend on which wave came first.
+// and one of 2^shift shares of I at a time (a unit; all of a wave's are the same
+// share), reads its 16 weight rows once, a batch of groups ahead of their use,
+// and leaves each pair's 16 sums in LDS at its own place; then each output is the
+// weighted sum over its token's pairs in order, so the result does not depend on
+// which wave came first. 16 waves of 4 groups' weights each are the loads under
+// way; the rows of h come through LDS (above), filling kDownSlots slots at a time,
+// each a wait for memory: 4 slots where the sums leave them room (8 tokens of 64
+// experts 33 us, with 2 slots 34). HBM-bound: 64 tokens, H 4096, I 1408, 128
+// experts 158 us (0.74 GB, 4.7 TB/s).
+template <int kDownSlots>
 __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     const uint8_t *__restrict__ w2, const float *__restrict__ s2, const uint16_t *__restrict__ h_hi,
     const uint16_t *__restrict__ h_lo, const float *__restrict__ gate, const MoeTable *__restrict__ table_in, int T,
     int H, int I, int top_k, int shift, uint16_t *__restrict__ Y) {
     __shared__ MoeTable table;
+    __shared__ float gate_s[kMaxPairs];
     extern __shared__ __align__(16) uint8_t smem[];  // slots [waves][2][kDownSlots], then sums [splits][T top_k][16]
     float *out = reinterpret_cast<float *>(smem + kDownWaves * 2 * kDownSlots * kSlot);
     const int lane = threadIdx.x & 63;
@@ -511,8 +526,13 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     const __amdgpu_buffer_rsrc_t rh = fp8_rsrc(h_hi, (uint32_t)pairs * (uint32_t)I * 2u);
     const __amdgpu_buffer_rsrc_t rl = fp8_rsrc(h_lo, (uint32_t)pairs * (uint32_t)I * 2u);
     const uint32_t chunk = slot_chunk(lane);
-    for (int i = threadIdx.x; i < (int)sizeof(MoeTable) / 4; i += kDownThreads)
-        reinterpret_cast<uint32_t *>(&table)[i] = reinterpret_cast<const uint32_t *>(table_in)[i];
+    // the table, and the choices' weights to wait in a register for their use
+    constexpr int kTableWords = sizeof(MoeTable) / 4;
+    static_assert(kTableWords <= kDownThreads && kMaxPairs == kDownThreads, "one of each for a thread");
+    const uint32_t word = reinterpret_cast<const uint32_t *>(table_in)[min((int)threadIdx.x, kTableWords - 1)];
+    const float weight = gate[min((int)threadIdx.x, pairs - 1)];
+    if (threadIdx.x < kTableWords) reinterpret_cast<uint32_t *>(&table)[threadIdx.x] = word;
+    gate_s[threadIdx.x] = weight;
     __syncthreads();
     const int splits = 1 << shift, s = wave & (splits - 1);
     const int reached = __builtin_amdgcn_readfirstlane(table.reached);
@@ -555,9 +575,9 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
                      __attribute__((always_inline)) {
         const int here = min(kDownTokens, p.count - p.m0), per = slots_of(here);
         const Place at = p;
-        uint32_t row[kDownSlots];
+        uint32_t row[2];
 #pragma unroll
-        for (int q = 0; q < kDownSlots; ++q)
+        for (int q = 0; q < 2; ++q)
             row[q] = pair_of(table.pair[at.from + at.m0 + min(4 * q + q4, here - 1)]) * (uint32_t)I * 2u;
         const float *sw = s2 + ((size_t)at.e * gh + n0 / kF8Block) * G;
         if (at.first == 0) acc = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -568,9 +588,9 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what they held has been read
 #pragma unroll
                 for (int q = 0; q < kDownSlots; ++q) {
-                    const int k = (s + ((at.first + n + (per == 1 ? q : 0)) << shift)) * kF8Block;
-                    load_slot(rh, slots + q * kSlot, q && per > 1 ? row[1] : row[0], k, I, chunk);
-                    load_slot(rl, slots + (kDownSlots + q) * kSlot, q && per > 1 ? row[1] : row[0], k, I, chunk);
+                    const int k = (s + ((at.first + n + (per == 1 ? q : q / 2)) << shift)) * kF8Block;
+                    load_slot(rh, slots + q * kSlot, (q & 1) && per > 1 ? row[1] : row[0], k, I, chunk);
+                    load_slot(rl, slots + (kDownSlots + q) * kSlot, (q & 1) && per > 1 ? row[1] : row[0], k, I, chunk);
                 }
                 // the slots are there; the next batch's 2 kDownAhead loads may stay under way
                 __builtin_amdgcn_sched_barrier(0);
@@ -600,9 +620,10 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w, sum[i], acc[i]);
         }
-        if (at.first + kDownAhead >= all && r16 < here)
-            *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + pair_of(table.pair[at.from + at.m0 + r16])) * 16 + 4 * q4) =
-                acc;
+        if (at.first + kDownAhead >= all && r16 < here) {
+            const uint32_t pair = pair_of(table.pair[at.from + at.m0 + r16]);
+            *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + pair) * 16 + 4 * q4) = acc;
+        }
     };
     Place p;
     p.a = wave >> shift;
@@ -621,7 +642,7 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
         for (int j = 0; j < top_k; ++j) {
             float o = 0.0f;
             for (int s = 0; s < splits; ++s) o += out[((size_t)s * pairs + t * top_k + j) * 16 + c];
-            y = __builtin_fmaf(gate[t * top_k + j], o, y);
+            y = __builtin_fmaf(gate_s[t * top_k + j], o, y);
         }
         Y[(size_t)t * H + n0 + c] = (uint16_t)f32_to_bf16_bits(y);
     }
@@ -688,8 +709,11 @@ hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *
     const int G = fp8_blocks(I);
     int shift = 0;
     while (most << shift < kDownWaves && 2 << shift <= G && (2 << shift) * pairs * 64 <= (32 << 10)) ++shift;
-    const size_t lds = (size_t)kDownWaves * 2 * kDownSlots * kSlot + ((size_t)pairs * 64 << shift);
-    hipLaunchKernelGGL(moe_down_kernel, dim3(H / 16), dim3(kDownThreads), lds, stream, w2, s2, h_hi, h_lo, gate, table,
+    const size_t sums = (size_t)pairs * 64 << shift;
+    const int slots = sums <= (24 << 10) ? 4 : 2;  // in 160 KB, 7 of them the table and weights
+    const size_t lds = (size_t)kDownWaves * 2 * slots * kSlot + sums;
+    const auto down = slots == 4 ? moe_down_kernel<4> : moe_down_kernel<2>;
+    hipLaunchKernelGGL(down, dim3(H / 16), dim3(kDownThreads), lds, stream, w2, s2, h_hi, h_lo, gate, table,
                        T, H, I, top_k, shift, Y);
     return hipGetLastError();
 }
