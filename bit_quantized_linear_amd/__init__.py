@@ -1,4 +1,5 @@
-"""MI355X (gfx950) SVDQuant W4A4 and INT8 tensorwise W8A8 linears.
+"""MI355X (gfx950) quantized linears: SVDQuant W4A4 (INT4 and MXFP4), INT8
+tensorwise W8A8, W4A16, block-scaled FP8 with a mixture-of-experts layer.
 
 The compute lives in the HIP/C++ shared library ``libsvdq.so`` built from
 ``csrc/`` (its C interface is ``include/svdq.h``). ``binding`` is a thin
