@@ -291,6 +291,35 @@ __device__ __forceinline__ void build_table(const int32_t *idx, int T, int E, in
     __syncthreads();
 }
 
+// ---- rows of activations through LDS -----------------------------------------------
+
+// The activations of a few tokens reach the MFMA through LDS: 4 tokens' 128
+// features are one 1 KB load (a slot), where loads straight into the operand
+// registers take four, mostly of lanes without a token. (Per load the address
+// unit spends 16 cycles whatever its lanes hold: with 4 tokens per expert the
+// straight loads cost both projections as much as the weights they meet.) Lane l
+// brings the 16-byte chunk c of token l / 16 to chunk position c ^ 4 (l / 16),
+// so that the four tokens' equal chunks are on different banks.
+typedef __attribute__((address_space(3))) void moe_lds_void;
+constexpr int kSlot = 1024;
+
+__device__ __forceinline__ uint32_t slot_chunk(int lane) { return ((lane & 15) ^ (4 * (lane >> 4))) * 16; }
+
+__device__ __forceinline__ void load_slot(__amdgpu_buffer_rsrc_t r, uint8_t *slot, uint32_t row, int k, int K,
+                                          uint32_t chunk) {
+    const int at = 2 * k + (int)chunk;  // bytes into the row; zeros past its end
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (moe_lds_void *)slot, 16, at < 2 * K ? row + (uint32_t)at : kMoeOob, 0,
+                                             0, 0);
+}
+
+// Chunk c (of 16) of the lane's token (slots one after another, 4 tokens each).
+__device__ __forceinline__ bf16x8 slot_read(const uint8_t *slots, int token, int c) {
+    return *reinterpret_cast<const bf16x8 *>(slots + token * 256 + ((c ^ (4 * (token & 3))) * 16));
+}
+
+// Slots per group for at most 8 tokens.
+__device__ __forceinline__ int slots_of(int tokens) { return tokens <= 4 ? 1 : 2; }
+
 // ---- gate and up projections ------------------------------------------------
 
 constexpr int kUpBlocks = 256;  // one per compute unit
@@ -301,18 +330,23 @@ constexpr int kUpRing = 3;      // steps under way per wave
 // LDS at an item's end. Weights and activations go straight from global memory
 // into the operands of the bf16 MFMA (an E4M3 value is exact in bf16), kUpRing
 // steps ahead of their use and across items, so that loads are under way all
-// the time. h is written as the sum of two bf16 numbers (hi + lo, 16
+// the time; the activations of few tokens come through kSlots slots of LDS,
+// 4 kSlots tokens at a time (0: straight, 16 at a time). h is written as the sum of two bf16 numbers (hi + lo, 16
 // significant bits), so that its rounding stays far below that of Y. kRoute:
 // every block also makes the choices, which saves a launch. Block 0 writes the
 // table down for the down projection. HBM-bound: 64 tokens, H 4096, I 1408, 128
-// experts 280 us (1.48 GB, 5.3 TB/s); at 4 tokens per expert the activations'
-// loads take the address units as long as the weights', so that more than 3
-// steps ahead, or the next item's weights fetched into the L2, gave nothing.
-template <bool kRoute>
+// experts 274 us (1.48 GB, 5.4 TB/s). The address and data units are busy 80 and
+// 90 % of that; with 4 steps ahead 271 us, but 14.4 instead of 13.8 for 23 tokens.
+template <bool kRoute, int kSlots>
 __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     const uint16_t *__restrict__ X, const uint8_t *__restrict__ w13, const float *__restrict__ s13,
     const double *__restrict__ logits, int32_t *__restrict__ idx, float *__restrict__ gate, int T, int H, int I, int E,
     int top_k, int renorm, uint16_t *__restrict__ h_hi, uint16_t *__restrict__ h_lo, MoeTable *__restrict__ table_out) {
+    constexpr int kTokens = kSlots ? 4 * kSlots : 16;  // of an expert at a time
+    constexpr int kSlotBytes = kSlots ? kUpWaves * kSlots * kSlot : 16;
+    // an array per place in the ring, so that a read waits for no other's loads
+    __shared__ __align__(16) uint8_t slots0[kSlotBytes], slots1[kSlotBytes], slots2[kSlotBytes];
+    static_assert(kUpRing == 3, "slots");
     __shared__ f32x4 red[2][kUpWaves][2][64];
     __shared__ unsigned long long tokens[SVDQ_FP8_MOE_MAX_EXPERTS];
     __shared__ MoeTable table;
@@ -355,7 +389,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     auto advance = [&](Place &p) __attribute__((always_inline)) {
         if (++p.step < steps) return;
         p.step = 0;
-        p.m0 += 16;
+        p.m0 += kTokens;
         if (p.m0 < p.count) return;
         p.item += (int)gridDim.x;
         p.a += next_a;
@@ -367,41 +401,71 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
         enter(p);
     };
     struct Step {
-        u32x4 g[2], u[2], x[2][2];
+        u32x4 g[2], u[2], x[kSlots ? 1 : 2][2];
     };
     // the operands of place p's step, and on to the next place
-    auto load = [&](Step &to, Place &p, uint32_t &xrow) __attribute__((always_inline)) {
+    const uint32_t chunk = slot_chunk(lane);
+    uint32_t xrow[kSlots ? kSlots : 1] = {};
+    auto load = [&](Step &to, uint8_t *slots, Place &p) __attribute__((always_inline)) {
         const uint8_t *we = w13 + (size_t)p.e * 2 * I * H;
         const __amdgpu_buffer_rsrc_t rg = fp8_rsrc(we + (size_t)p.i0 * H, 16u * (uint32_t)H);
         const __amdgpu_buffer_rsrc_t ru = fp8_rsrc(we + (size_t)(I + p.i0) * H, 16u * (uint32_t)H);
-        if (p.step == 0)  // the lane's token, as a byte offset; lanes without one read zeros
-            xrow = p.m0 + r16 < p.count ? token_of(table.pair[p.from + p.m0 + r16]) * (uint32_t)H * 2u
-                                        : kMoeOob;
+        if (p.step == 0) {  // the lane's token, as a byte offset; lanes without one read zeros
+            if constexpr (kSlots == 0)
+                xrow[0] = p.m0 + r16 < p.count ? token_of(table.pair[p.from + p.m0 + r16]) * (uint32_t)H * 2u : kMoeOob;
+            else
+#pragma unroll
+                for (int q = 0; q < kSlots; ++q)
+                    xrow[q] = token_of(table.pair[p.from + min(p.m0 + 4 * q + q4, p.count - 1)]) * (uint32_t)H * 2u;
+        }
+        if constexpr (kSlots > 0) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what the slots held has been read
+            const int kx = p.item < items ? (p.step * kUpWaves + wave) * kF8Block : H;
+#pragma unroll
+            for (int q = 0; q < kSlots; ++q) load_slot(rx, slots + (wave * kSlots + q) * kSlot, xrow[q], kx, H, chunk);
+        }
         const int k0 = (p.step * kUpWaves + wave) * kF8Block + 16 * q4;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int k = k0 + 64 * i;
             const bool in = k < H && p.item < items;
             const uint32_t off = in ? (uint32_t)r16 * (uint32_t)H + (uint32_t)k : kMoeOob;
-            const uint32_t xoff = in ? xrow + 2u * (uint32_t)k : kMoeOob;
+            const uint32_t xoff = kSlots == 0 && in ? xrow[0] + 2u * (uint32_t)k : kMoeOob;
             to.g[i] = load16(rg, off);
             to.u[i] = load16(ru, off);
-            to.x[i][0] = load16(rx, xoff);
-            to.x[i][1] = load16(rx, xoff + 16);
+            if constexpr (kSlots == 0) {
+                to.x[i][0] = load16(rx, xoff);
+                to.x[i][1] = load16(rx, xoff + 16);
+            }
         }
         advance(p);
     };
     f32x4 accg = {0.f, 0.f, 0.f, 0.f}, accu = accg;
     int turn = 0;
     // one step: its products; the sums and the output behind an item's last one
-    auto compute = [&](const Step &now, Place &p) __attribute__((always_inline)) {
+    auto compute = [&](const Step &now, const uint8_t *slots, Place &p) __attribute__((always_inline)) {
+        if constexpr (kSlots > 0) {
+            __builtin_amdgcn_sched_barrier(0);
+            // the slots are there; the loads of the later steps may stay under way
+            constexpr int kLater = (kUpRing - 1) * (kSlots + 4);
+            static_assert(kLater < 16, "what the wait below can count");
+            __builtin_amdgcn_s_waitcnt(0x0F70 | kLater);  // vmcnt(kLater)
+            __builtin_amdgcn_sched_barrier(0);
+        }
         const int g = p.step * kUpWaves + wave;
         const size_t block = ((size_t)p.e * 2 * gi + p.i0 / kF8Block) * G + min(g, G - 1);
         const float wg = fp8_scale_within(s13[block], g, G), wu = fp8_scale_within(s13[block + (size_t)gi * G], g, G);
         f32x4 pg = {0.f, 0.f, 0.f, 0.f}, pu = pg;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bf16x8 b0 = __builtin_bit_cast(bf16x8, now.x[i][0]), b1 = __builtin_bit_cast(bf16x8, now.x[i][1]);
+            bf16x8 b0, b1;
+            if constexpr (kSlots == 0) {
+                b0 = __builtin_bit_cast(bf16x8, now.x[i][0]), b1 = __builtin_bit_cast(bf16x8, now.x[i][1]);
+            } else {
+                const int c = 8 * i + 2 * q4, token = r16 & (kTokens - 1);
+                b0 = slot_read(slots + wave * kSlots * kSlot, token, c);
+                b1 = slot_read(slots + wave * kSlots * kSlot, token, c + 1);
+            }
             pg = mfma_bf16_16x16x32(fp8_widen8(now.g[i][0], now.g[i][1]), b0, pg);
             pu = mfma_bf16_16x16x32(fp8_widen8(now.u[i][0], now.u[i][1]), b0, pu);
             pg = mfma_bf16_16x16x32(fp8_widen8(now.g[i][2], now.g[i][3]), b1, pg);
@@ -430,7 +494,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
                 g += red[turn][w][0][src][c & 3];
                 u += red[turn][w][1][src][c & 3];
             }
-            if (p.m0 + m < p.count) {
+            if (m < kTokens && p.m0 + m < p.count) {
                 const float h = g / (1.0f + expf(-g)) * u;
                 const uint32_t hi = f32_to_bf16_bits(h);
                 const size_t at = (size_t)pair_of(table.pair[p.from + p.m0 + m]) * I + p.i0 + c;
@@ -448,49 +512,20 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     enter(at);
     ahead = at;
     Step ring[kUpRing];
-    uint32_t xrow = 0;
+    auto slots_at = [&](int n) -> uint8_t * { return n == 0 ? slots0 : n == 1 ? slots1 : slots2; };
 #pragma unroll
-    for (int n = 0; n < kUpRing; ++n) load(ring[n], ahead, xrow);
+    for (int n = 0; n < kUpRing; ++n) load(ring[n], slots_at(n), ahead);
     while (at.item < items) {
 #pragma unroll
         for (int n = 0; n < kUpRing; ++n) {
             if (at.item >= items) break;
-            compute(ring[n], at);
-            load(ring[n], ahead, xrow);
+            compute(ring[n], slots_at(n), at);
+            load(ring[n], slots_at(n), ahead);
             if (at.step == steps - 1) finish(at);
             advance(at);
         }
     }
 }
-
-// ---- rows of activations through LDS -----------------------------------------------
-
-// The activations of a few tokens reach the MFMA through LDS: 4 tokens' 128
-// features are one 1 KB load (a slot), where loads straight into the operand
-// registers take four, mostly of lanes without a token. (Per load the address
-// unit spends 16 cycles whatever its lanes hold: with 4 tokens per expert the
-// straight loads cost the down projection as much as its weights.) Lane l
-// brings the 16-byte chunk c of token l / 16 to chunk position c ^ 4 (l / 16),
-// so that the four tokens' equal chunks are on different banks.
-typedef __attribute__((address_space(3))) void moe_lds_void;
-constexpr int kSlot = 1024;
-
-__device__ __forceinline__ uint32_t slot_chunk(int lane) { return ((lane & 15) ^ (4 * (lane >> 4))) * 16; }
-
-__device__ __forceinline__ void load_slot(__amdgpu_buffer_rsrc_t r, uint8_t *slot, uint32_t row, int k, int K,
-                                          uint32_t chunk) {
-    const int at = 2 * k + (int)chunk;  // bytes into the row; zeros past its end
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (moe_lds_void *)slot, 16, at < 2 * K ? row + (uint32_t)at : kMoeOob, 0,
-                                             0, 0);
-}
-
-// Chunk c (of 16) of the lane's token (slots one after another, 4 tokens each).
-__device__ __forceinline__ bf16x8 slot_read(const uint8_t *slots, int token, int c) {
-    return *reinterpret_cast<const bf16x8 *>(slots + token * 256 + ((c ^ (4 * (token & 3))) * 16));
-}
-
-// Slots per group for at most 8 tokens.
-__device__ __forceinline__ int slots_of(int tokens) { return tokens <= 4 ? 1 : 2; }
 
 // ---- down projection and weighted sum ----------------------------------------
 
@@ -691,18 +726,26 @@ hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const dim3 up((unsigned)std::min<int64_t>((int64_t)most * (I / 16), kUpBlocks));
+    const auto launch_up = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, up, dim3(kUpThreads), 0, stream, X, w13, s13, logits, idx, gate, T, H, I, E, top_k,
+                           renorm ? 1 : 0, h_hi, h_lo, table);
+        return hipGetLastError();
+    };
     if (T * E <= kRouteInUp) {
-        hipLaunchKernelGGL(moe_up_kernel<true>, up, dim3(kUpThreads), 0, stream, X, w13, s13, logits, idx, gate, T, H,
-                           I, E, top_k, renorm ? 1 : 0, h_hi, h_lo, table);
+        err = T <= 4 ? launch_up(moe_up_kernel<true, 1>) : launch_up(moe_up_kernel<true, 0>);
     } else {
         hipLaunchKernelGGL(moe_route_kernel, dim3(T), dim3(kRouteThreads), 0, stream, logits, E, top_k,
                            renorm ? 1 : 0, idx, gate);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
-        hipLaunchKernelGGL(moe_up_kernel<false>, up, dim3(kUpThreads), 0, stream, X, w13, s13, logits, idx, gate, T,
-                           H, I, E, top_k, renorm ? 1 : 0, h_hi, h_lo, table);
+        // slots for as many tokens as an expert mostly has, as with more than they
+        // hold its weights are read again. Layer, H 4096, I 1408, slots / straight,
+        // at tokens x choices per expert: 4 (64 x 8 of 128) 446 / 451 us, 6 (48 x 8
+        // of 64) 265 / 261, 8 317 / 294.
+        err = T <= 4             ? launch_up(moe_up_kernel<false, 1>)
+              : pairs <= 4 * E ? launch_up(moe_up_kernel<false, 2>)
+                                 : launch_up(moe_up_kernel<false, 0>);
     }
-    err = hipGetLastError();
     if (err != hipSuccess) return err;
     // as many shares of I as give every wave a unit, at most one per group and
     // what 32 KB of LDS hold

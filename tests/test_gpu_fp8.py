@@ -245,9 +245,10 @@ def test_moe(T, H_, I, E, k, renorm):  # noqa: E741
     assert np.array_equal(H.host(Y), H.host(Y2)) and np.all(idx == -3) and np.all(gate == -3.0)
 
 
-def test_moe_all_tokens_on_the_same_experts():
-    # every token is the same, so one expert gets all 64
-    T, H_, I, E, k = 64, 256, 160, 12, 3  # noqa: E741
+@pytest.mark.parametrize("T,E", [(64, 12), (20, 64), (3, 64)])
+def test_moe_all_tokens_on_the_same_experts(T, E):
+    # every token is the same, so one expert gets them all
+    H_, I, k = 256, 160, 3  # noqa: E741
     bits = np.repeat(wl.random_bf16(9, (1, H_))["bits"], T, 0)
     wr, *w = experts(E, H_, I, 9)
     Y, idx, gate = run_moe(bits, wr["bits"], w, k)
