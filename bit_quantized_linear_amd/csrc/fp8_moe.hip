@@ -12,10 +12,10 @@
 // expert and 16 intermediate columns; the down projection with the weighted
 // sum, one block per 16 output columns. Each reached expert's weights are read
 // once, so the layer is bound by HBM: 64 tokens of 128 experts (H 4096, I 1408, 8
-// choices) take 447 us, 4.9 TB/s over all launches; for few bytes by the chain of
+// choices) take 439 us, 5.0 TB/s over all launches; for few bytes by the chain of
 // dependent loads: a token's logits, its choice, the experts' weights, then h and
 // again weights, in three launches about 1.1 us apart (1 token, H 2048, I 768, 8 of
-// 64 experts: 22 us, of which the weights alone would take 7.5).
+// 64 experts: 20.5 us, of which the weights alone would take 7.5).
 
 #include <hip/hip_runtime.h>
 
@@ -206,10 +206,11 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const double *
 }
 
 // Up to this many (token, expert) pairs the up kernel's blocks make the choices
-// themselves (a layer for one token of 64 experts: 22.8 us in three launches,
-// 26.5 in four; for 23 of 40: 35.3 and 31.6, as every block does all the
-// comparisons).
-constexpr int kRouteInUp = 128;
+// themselves. A layer, H 2048, I 768, with the choice in the up kernel / by
+// itself: 1 token of 64 experts 20.9 / 22.8 us, 16 of 16 29.9 / 30.5, 4 of 64 46.2
+// / 47.7; 4 of 128 52.1 / 50.7 and 64 of 8 39.3 / 37.9, as every block does all
+// the comparisons.
+constexpr int kRouteInUp = 256;
 
 // ---- the reached experts ---------------------------------------------------------
 
@@ -539,8 +540,8 @@ constexpr int kDownTokens = 8;  // of an expert at a time
 // weighted sum over its token's pairs in order, so the result does not depend on
 // which wave came first. 16 waves of 4 groups' weights each are the loads under
 // way; the rows of h come through LDS (above), filling kDownSlots slots at a time,
-// each a wait for memory: 4 slots where the sums leave them room (8 tokens of 64
-// experts 33 us, with 2 slots 34). HBM-bound: 64 tokens, H 4096, I 1408, 128
+// each a wait for memory: 4 slots where the sums leave them room (a layer for 8
+// tokens of 64 experts 98.7 us, with 2 slots 99.4). HBM-bound: 64 tokens, H 4096, I 1408, 128
 // experts 158 us (0.74 GB, 4.7 TB/s).
 template <int kDownSlots>
 __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
@@ -718,7 +719,7 @@ hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *
     if (!gate) gate = reinterpret_cast<float *>(ws + at.gate);
 
     const int eb = (E + kLogitExperts - 1) / kLogitExperts;
-    if (T == 1)
+    if (T == 1)  // one token of 64 experts: 20.9 us, 21.6 with the other
         hipLaunchKernelGGL(moe_logits_kernel<1>, dim3(eb), dim3(64 * kLogitWaves), 0, stream, X, wr, T, H, E, logits);
     else
         hipLaunchKernelGGL(moe_logits_kernel<4>, dim3(eb, (T + 3) / 4), dim3(64 * kLogitWaves), 0, stream, X, wr, T, H,
