@@ -166,7 +166,8 @@ def test_a_token_with_nan_or_inf_stays_alone(M):
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("M,N", [(5, 136), (40, 136), (300, 264), (700, 2056), (1800, 2056), (2100, 2056), (4100, 2056)])
+@pytest.mark.parametrize("M,N", [(5, 136), (40, 136), (300, 264), (700, 2056), (1800, 2056), (2100, 2056),
+                                 (4100, 2056)])
 def test_scales_past_the_largest_number_give_infinities(M, N, out):
     # one and three groups of 128: stages and waves without a group add nothing, not infinity times zero
     t = H.torch()
@@ -228,7 +229,8 @@ def check_moe(y, idx, gate, ref, rows=slice(None)):
     assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4])
 
 
-MOE = [(1, 16, 16, 1, 1), (1, 128, 64, 4, 2), (1, 2048, 768, 64, 8), (2, 144, 80, 5, 5), (3, 1040, 144, 33, 3),
+MOE = [(1, 16, 16, 1, 1), (1, 128, 32, 256, 16), (1, 128, 64, 4, 2), (1, 2048, 768, 64, 8), (2, 144, 80, 5, 5),
+       (3, 1040, 144, 33, 3),
        (5, 272, 400, 256, 16), (8, 512, 256, 8, 4), (17, 656, 48, 3, 1), (23, 1072, 400, 40, 3), (33, 256, 272, 6, 2),
        (64, 384, 128, 2, 2), (64, 512, 144, 100, 8), (64, 128, 64, 70, 16)]
 
@@ -267,7 +269,8 @@ def test_moe_ties_go_to_the_lowest_expert():
     assert np.array_equal(idx, np.repeat(np.arange(4)[None], T, 0)) and np.all(gate == 0.25)
     rows[40], rows[66] = wr["bits"][1], wr["bits"][1]  # two alike, apart from the rest
     Y, idx, gate = run_moe(bits, rows, w, k, renorm=False)
-    check_moe(y_of(Y, T, "bf16"), idx, gate, o8.moe(wl.f32_from_bf16_bits(bits), wl.f32_from_bf16_bits(rows), *w, k, False))
+    ref = o8.moe(wl.f32_from_bf16_bits(bits), wl.f32_from_bf16_bits(rows), *w, k, False)
+    check_moe(y_of(Y, T, "bf16"), idx, gate, ref)
 
 
 def test_moe_not_finite_tokens_and_experts_stay_alone():
