@@ -74,10 +74,8 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
 
 constexpr uint32_t kF8Oob = 0x80000000u;
 constexpr int kF8Cus = 256;  // compute units
-constexpr int kF8SkinnyWaves = 8;
 // one MFMA tile: with two, 20 x 5120 x 5120 took 14.6 us, in tiles of 64 it takes 10.8
 constexpr int kF8SkinnyTokens = 16;
-constexpr size_t kF8FusedLds = 40 << 10;  // the linear in one launch: LDS for its codes and scales
 
 typedef __attribute__((address_space(3))) void f8_lds_void;
 
@@ -455,25 +453,25 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 
 // ---- the product, few tokens -----------------------------------------------
 
-// One block computes 16 output columns of at most 16 tokens; its 8 waves take
-// the groups of K in turn (wave w groups w, w + 8, ...), `Ahead` of them in
-// flight, straight from global memory into the operands of the 16x16x128 MFMA
-// (weights as A: row = output column; tokens as B), and add their sums in LDS
-// in a fixed order. The weight is read once: bound by HBM, and at these sizes by
-// the way to the first of it (a launch, a load's latency, the sums): 13 x 2048 x
-// 12288 takes 8.2 us (25 MB, 3.1 TB/s), 1 x 5120 x 5120 in one launch 8.9 (26 MB,
-// 2.9 TB/s). More groups in flight than 2 or 3 cost more by the waves that their
-// registers keep out than they hide.
+// One block computes 16 output columns of at most 16 tokens; its W waves take
+// the groups of K in turn (wave w groups w, w + W, ...), straight from global
+// memory into the operands of the 16x16x128 MFMA (weights as A: row = output
+// column; tokens as B), and add their sums in LDS in a fixed order. The weight
+// is read once: bound by HBM, and at these sizes by the way to the first of it (a
+// launch, a load's latency, the sums): 13 x 2048 x 12288 (M x K x N) takes 8 us
+// (25 MB, 3.1 TB/s), 1 x 5120 x 5120 in one launch 8 (26 MB, 3.3 TB/s). Waves, 32
+// per compute unit, hide a load's latency better than loads ahead, whose
+// registers keep waves out: 1, 2, 3 and 4 groups in flight per wave take 8.5, 9.6,
+// 9.3 and 10.5 us for 1 x 5120 x 5120, 13.4, 14.6, 14.5 and 16.2 for 8 x 5120 x 12288.
 // kFused: from bf16 activations. While its first weights are on their way, each
 // block quantizes all tokens' features into LDS, exactly as the activation pass
 // does, which saves that launch; dynamic LDS: the codes [M][K rounded up to
 // groups], then the scales [G][M].
-template <int Ahead, bool kWide, bool kFused>
-__global__ __launch_bounds__(64 * kF8SkinnyWaves) void fp8_skinny_kernel(
+template <int W, bool kWide, bool kFused>
+__global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint16_t *__restrict__ X,
     const uint8_t *__restrict__ qw, const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N,
     int K, void *__restrict__ Y) {
-    constexpr int W = kF8SkinnyWaves;
     __shared__ f32x4 red[W][64];
     extern __shared__ __align__(16) uint8_t codes_s[];
     const int n0 = blockIdx.x * 16;
@@ -501,9 +499,7 @@ __global__ __launch_bounds__(64 * kF8SkinnyWaves) void fp8_skinny_kernel(
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     const int mrow = min(r16, M - 1);
 
-    i32x8 a[Ahead];
-#pragma unroll
-    for (int u = 0; u < Ahead; ++u) a[u] = operand(rw, r16, wave + W * u);  // past K: zeros
+    i32x8 a = operand(rw, r16, wave);  // past K: zeros
     if constexpr (kFused) {
         // 16 threads per token and group, 8 features each
         const int part = threadIdx.x & 15;
@@ -517,38 +513,22 @@ __global__ __launch_bounds__(64 * kF8SkinnyWaves) void fp8_skinny_kernel(
         }
         __syncthreads();
     }
-    for (int g0 = wave; g0 < G; g0 += W * Ahead) {
-        if (g0 != wave) {
-#pragma unroll
-            for (int u = 0; u < Ahead; ++u) a[u] = operand(rw, r16, g0 + W * u);
+    for (int g = wave; g < G; g += W) {
+        if (g != wave) a = operand(rw, r16, g);
+        i32x8 b;
+        float s;
+        if constexpr (kFused) {
+            const uint8_t *at = codes_s + ((size_t)mrow * G + g) * kF8Block + 16 * q4;
+            b = join(*reinterpret_cast<const u32x4 *>(at), *reinterpret_cast<const u32x4 *>(at + 64));
+            s = scales_s[g * M + mrow] * swr[g];
+        } else {
+            b = operand(rx, mrow, g);
+            s = sx[(size_t)g * M + mrow] * swr[g];
         }
-        i32x8 b[Ahead];
-        float s[Ahead];
-        if constexpr (!kFused) {
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        const f32x4 p = kWide ? mfma_wide_16x16x128(a, b, zero) : mfma_fp8_16x16x128(a, b, zero);
 #pragma unroll
-            for (int u = 0; u < Ahead; ++u) {
-                const int g = g0 + W * u;
-                b[u] = operand(rx, mrow, g);
-                s[u] = sx[(size_t)min(g, G - 1) * M + mrow] * swr[min(g, G - 1)];
-            }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // all of them under way before the first is used
-        // groups past K: zero weights and a zero scale add nothing, so no branch
-        // waits on them
-#pragma unroll
-        for (int u = 0; u < Ahead; ++u) {
-            const int g = min(g0 + W * u, G - 1);
-            if constexpr (kFused) {
-                const uint8_t *at = codes_s + ((size_t)mrow * G + g) * kF8Block + 16 * q4;
-                b[u] = join(*reinterpret_cast<const u32x4 *>(at), *reinterpret_cast<const u32x4 *>(at + 64));
-                s[u] = scales_s[g * M + mrow] * swr[g];
-            }
-            const float scale = fp8_scale_within(s[u], g0 + W * u, G);
-            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            const f32x4 p = kWide ? mfma_wide_16x16x128(a[u], b[u], zero) : mfma_fp8_16x16x128(a[u], b[u], zero);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(scale, p[e], acc[e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(s, p[e], acc[e]);
     }
     red[wave][lane] = acc;
     __syncthreads();
@@ -589,13 +569,29 @@ static hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t 
     return hipGetLastError();
 }
 
+// 16 waves per block where the blocks are all on the chip at once (two on a
+// compute unit), 8 where more of them take turns. Times in us in one launch, 16 / 8
+// waves: 1 x 5120 x 5120 (M x K x N) 7.9 / 8.4, 8 x 2048 x 2048 4.9 / 5.9, 2 x 8192 x
+// 8192 14.6 / 16.4; 3 x 5120 x 12288 15.0 / 13.5; of codes, 13 x 2048 x 12288 8.2 / 7.4.
+template <bool kWide, bool kFused>
+static hipError_t launch_skinny(const uint8_t *qx, const float *sx, const uint16_t *X, const uint8_t *qw,
+                                const float *sw, const uint16_t *bias, int M, int N, int K, void *Y, size_t lds,
+                                hipStream_t stream) {
+    const int tiles = (N + 15) / 16;
+    if (tiles <= 2 * kF8Cus)
+        hipLaunchKernelGGL((fp8_skinny_kernel<16, kWide, kFused>), dim3(tiles), dim3(1024), lds, stream, qx, sx, X, qw,
+                           sw, bias, M, N, K, Y);
+    else
+        hipLaunchKernelGGL((fp8_skinny_kernel<8, kWide, kFused>), dim3(tiles), dim3(512), lds, stream, qx, sx, X, qw,
+                           sw, bias, M, N, K, Y);
+    return hipGetLastError();
+}
+
 template <bool kWide>
 static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                               const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
     if (M <= kF8SkinnyTokens) {
-        hipLaunchKernelGGL((fp8_skinny_kernel<2, kWide, false>), dim3((N + 15) / 16), dim3(512), 0, stream, qx, sx,
-                           nullptr, qw, sw, bias, M, N, K, Y);
-        return hipGetLastError();
+        return launch_skinny<kWide, false>(qx, sx, nullptr, qw, sw, bias, M, N, K, Y, 0, stream);
     }
     // Tiles of t x t: the larger, the less each operand is read; the smaller,
     // the more compute units have one. Times in us for bf16, M x 5120 x 5120, by
@@ -632,20 +628,21 @@ template <bool kWide>
 static hipError_t launch_few(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias, int M, int N,
                              int K, void *Y, hipStream_t stream) {
     const size_t lds = (size_t)M * fp8_blocks(K) * (kF8Block + sizeof(float));
-    hipLaunchKernelGGL((fp8_skinny_kernel<3, kWide, true>), dim3((N + 15) / 16), dim3(512), lds, stream, nullptr,
-                       nullptr, X, qw, sw, bias, M, N, K, Y);
-    return hipGetLastError();
+    return launch_skinny<kWide, true>(nullptr, nullptr, X, qw, sw, bias, M, N, K, Y, lds, stream);
 }
 
-// Every block quantizes all tokens anew, so one launch pays where a compute unit
-// does not do it for too many token groups. Times of a call in us, in one / two
-// launches: 4 x 5120 x 5120 (200 groups a unit) 11.5 / 12.8, 2 x 12288 x 5120
-// (240) 13.0 / 15.5, 8 x 2048 x 2048 (128) 5.6 / 7.9, 16 x 1024 x 12288 (384)
-// 9.5 / 9.1, 8 x 5120 x 5120 (400) 15.4 / 13.4.
+// Every block quantizes all tokens anew: one launch pays where a compute unit does
+// not do it for too many groups (a token's 128 features) in all its blocks, or
+// where they are about one round of a block's threads. Times of a call in us, in
+// one / two launches: 1 x 5120 x 5120 (M x K x N, 50 groups a unit) 8.6 / 11.5, 2 x
+// 8192 x 8192 (256) 14.6 / 17.2, 3 x 5120 x 12288 (360) 13.1 / 15.1, 6 x 5120 x 5120
+// (300) 11.9 / 12.5, 16 x 2048 x 2048 (256) 7.2 / 8.1, 8 x 2048 x 12288 (384) 10.2 /
+// 10.2; 8 x 5120 x 5120 (400) 13.9 / 13.2, 8 x 4096 x 8192 (512) 15.6 / 12.8, 10 x 2048
+// x 12288 (480) 11.4 / 10.5. One round: 1 x 5120 x 65536 56.6 / 59.6, 1 x 2048 x 151936
+// 47.7 / 50.8. LDS for at most 384 groups: 51 KB.
 bool fp8_linear_in_one(int M, int N, int K) {
-    const int64_t groups = (int64_t)M * fp8_blocks(K);
-    return M <= kF8SkinnyTokens && groups * std::max(N, 16 * kF8Cus) <= (int64_t)256 * 16 * kF8Cus &&
-           groups * (kF8Block + sizeof(float)) <= kF8FusedLds;
+    const int64_t groups = (int64_t)M * fp8_blocks(K), tiles = ((int64_t)N + 15) / 16;
+    return M <= kF8SkinnyTokens && (groups <= 40 || groups * std::max<int64_t>(tiles, kF8Cus) <= 384 * kF8Cus);
 }
 
 hipError_t launch_fp8_linear_in_one(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias,
