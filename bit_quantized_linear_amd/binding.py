@@ -134,7 +134,10 @@ def _current_device():
     if _device_of is None:
         import torch
 
-        _device_of = torch.cuda.current_device
+        device = torch.cuda.current_device()  # starts torch's side of the device, too
+        # once that is up, the number without the check for it (0.2 us a call)
+        _device_of = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        return device
     return _device_of()
 
 
@@ -166,7 +169,8 @@ def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None):
 def _shape2(t, name):
     if t is None or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D tensor")
-    return int(t.shape[0]), int(t.shape[1])
+    rows, columns = t.shape
+    return int(rows), int(columns)
 
 
 _raw_stream = None
@@ -181,8 +185,8 @@ def _stream(stream):
 
         # the current stream's handle, where torch has it without a Stream
         # object (3 us a call)
-        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
-        _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = (lambda: raw(_current_device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
     return _raw_stream()
 
 
