@@ -453,33 +453,33 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 
 // ---- the product, few tokens -----------------------------------------------
 
-// One block computes 16 output columns of at most 16 tokens; its W waves take
+// One block computes 16 NT output columns of at most 16 tokens; its W waves take
 // the groups of K in turn (wave w groups w, w + W, ...), straight from global
 // memory into the operands of the 16x16x128 MFMA (weights as A: row = output
-// column; tokens as B), and add their sums in LDS in a fixed order. The weight
-// is read once: bound by HBM, and at these sizes by the way to the first of it (a
-// launch, a load's latency, the sums): 13 x 2048 x 12288 (M x K x N) takes 8 us
-// (25 MB, 3.1 TB/s), 1 x 5120 x 5120 in one launch 8 (26 MB, 3.3 TB/s). Waves, 32
-// per compute unit, hide a load's latency better than loads ahead, whose
+// column; tokens as B, for all NT tiles of columns), and add their sums in LDS in
+// a fixed order. The weight is read once: bound by HBM, and at these sizes by the
+// way to the first of it (a launch, a load's latency, the sums): 13 x 2048 x 12288
+// (M x K x N) takes 7.8 us (25 MB, 3.2 TB/s), 1 x 5120 x 5120 in one launch 8.4 (26
+// MB, 3.1 TB/s). Waves hide a load's latency better than loads ahead, whose
 // registers keep waves out: 1, 2, 3 and 4 groups in flight per wave take 8.5, 9.6,
 // 9.3 and 10.5 us for 1 x 5120 x 5120, 13.4, 14.6, 14.5 and 16.2 for 8 x 5120 x 12288.
 // kFused: from bf16 activations. While its first weights are on their way, each
 // block quantizes all tokens' features into LDS, exactly as the activation pass
 // does, which saves that launch; dynamic LDS: the codes [M][K rounded up to
 // groups], then the scales [G][M].
-template <int W, bool kWide, bool kFused>
+template <int W, int NT, bool kWide, bool kFused>
 __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint16_t *__restrict__ X,
     const uint8_t *__restrict__ qw, const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N,
     int K, void *__restrict__ Y) {
-    __shared__ f32x4 red[W][64];
+    __shared__ f32x4 red[W][NT][64];
     extern __shared__ __align__(16) uint8_t codes_s[];
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x * 16 * NT;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q4 = lane >> 4;
     const int G = (K + kF8Block - 1) / kF8Block;
-    const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(16, N - n0) * (uint32_t)K);
+    const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(qw + (size_t)n0 * K, (uint32_t)min(16 * NT, N - n0) * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(qx, kFused ? 0u : (uint32_t)M * (uint32_t)K);
     const float *swr = sw + (size_t)(n0 / kF8Block) * G;
     float *scales_s = reinterpret_cast<float *>(codes_s + (size_t)M * G * kF8Block);
@@ -496,10 +496,19 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
             __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k + 64 < K ? off + 64 : kF8Oob, 0, 0)));
     };
 
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int mrow = min(r16, M - 1);
 
-    i32x8 a = operand(rw, r16, wave);  // past K: zeros
+    // Where rows are a multiple of 4 KB apart, the same group of all rows lies on a
+    // few memory channels, so each block starts at another group (16 x 8192 x 8192:
+    // 13.6 us, 19.7 without; elsewhere it costs: 1 x 2048 x 151936 57, 49 without).
+    const int first = K % 4096 ? 0 : (int)blockIdx.x & ((1 << (31 - __builtin_clz(G))) - 1);
+    auto turned = [&](int i) __attribute__((always_inline)) { return i + first < G ? i + first : i + first - G; };
+    i32x8 a[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) a[t] = operand(rw, 16 * t + r16, turned(wave));
     if constexpr (kFused) {
         // 16 threads per token and group, 8 features each
         const int part = threadIdx.x & 15;
@@ -513,8 +522,12 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
         }
         __syncthreads();
     }
-    for (int g = wave; g < G; g += W) {
-        if (g != wave) a = operand(rw, r16, g);
+    for (int i = wave; i < G; i += W) {
+        const int g = turned(i);
+        if (i != wave) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) a[t] = operand(rw, 16 * t + r16, g);
+        }
         i32x8 b;
         float s;
         if constexpr (kFused) {
@@ -526,20 +539,24 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
             s = sx[(size_t)g * M + mrow] * swr[g];
         }
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        const f32x4 p = kWide ? mfma_wide_16x16x128(a, b, zero) : mfma_fp8_16x16x128(a, b, zero);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(s, p[e], acc[e]);
+        for (int t = 0; t < NT; ++t) {
+            const f32x4 p = kWide ? mfma_wide_16x16x128(a[t], b, zero) : mfma_fp8_16x16x128(a[t], b, zero);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(s, p[e], acc[t][e]);
+        }
     }
-    red[wave][lane] = acc;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) red[wave][t][lane] = acc[t];
     __syncthreads();
-    if (threadIdx.x < 256) {
-        const int m = threadIdx.x >> 4, c = threadIdx.x & 15;  // consecutive threads: consecutive columns of a token
-        const int src = 16 * (c >> 2) + m;
+    for (int i = threadIdx.x; i < 256 * NT; i += 64 * W) {
+        const int m = i / (16 * NT), c = i % (16 * NT);  // consecutive threads: consecutive columns of a token
+        const int src = 16 * ((c >> 2) & 3) + m;
         const int n = n0 + c;
         if (m < M && n < N) {
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) v += red[w][src][c & 3];
+            for (int w = 0; w < W; ++w) v += red[w][c >> 4][src][c & 3];
             if (bias) v += bf16_bits_to_f32(bias[n]);
             if constexpr (kWide)
                 static_cast<float *>(Y)[(size_t)m * N + n] = v;
@@ -569,22 +586,29 @@ static hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t 
     return hipGetLastError();
 }
 
-// 16 waves per block where the blocks are all on the chip at once (two on a
-// compute unit), 8 where more of them take turns. Times in us in one launch, 16 / 8
-// waves: 1 x 5120 x 5120 (M x K x N) 7.9 / 8.4, 8 x 2048 x 2048 4.9 / 5.9, 2 x 8192 x
-// 8192 14.6 / 16.4; 3 x 5120 x 12288 15.0 / 13.5; of codes, 13 x 2048 x 12288 8.2 / 7.4.
+// As many columns per block as leave one block for each compute unit, up to 64:
+// the tokens are read, and with kFused quantized, once per block. Beyond that,
+// 32. Times in us of codes, 1 token / 16 tokens: N = 2560, K = 5120, 16 columns 5.3 /
+// 7.5, 32 columns 7.5 / 9.6; 5120 x 5120 16 columns 8.4 / 12.0, 32 7.6 / 9.6, 64 11.8 /
+// 14.4; N = 16384, K = 4096 32 columns 13.8 / 15.0, 64 11.7 / 12.8; N = 20480, K = 2048
+// 32 9.1 / 11.4, 64 11.2 / 12.6. 16 waves for 16 columns, and for 32 where they
+// share the quantization and have a group of K each (8 tokens, 5120 x 5120: 11.8,
+// with 8 waves 14.3; of codes 9.2 and 8.6).
 template <bool kWide, bool kFused>
 static hipError_t launch_skinny(const uint8_t *qx, const float *sx, const uint16_t *X, const uint8_t *qw,
                                 const float *sw, const uint16_t *bias, int M, int N, int K, void *Y, size_t lds,
                                 hipStream_t stream) {
     const int tiles = (N + 15) / 16;
-    if (tiles <= 2 * kF8Cus)
-        hipLaunchKernelGGL((fp8_skinny_kernel<16, kWide, kFused>), dim3(tiles), dim3(1024), lds, stream, qx, sx, X, qw,
-                           sw, bias, M, N, K, Y);
-    else
-        hipLaunchKernelGGL((fp8_skinny_kernel<8, kWide, kFused>), dim3(tiles), dim3(512), lds, stream, qx, sx, X, qw,
-                           sw, bias, M, N, K, Y);
-    return hipGetLastError();
+    const auto launch = [&](auto kernel, int columns, int waves) {
+        hipLaunchKernelGGL(kernel, dim3((N + columns - 1) / columns), dim3(64 * waves), lds, stream, qx, sx, X, qw, sw,
+                           bias, M, N, K, Y);
+        return hipGetLastError();
+    };
+    if (tiles <= kF8Cus) return launch(fp8_skinny_kernel<16, 1, kWide, kFused>, 16, 16);
+    if (tiles > 2 * kF8Cus && tiles <= 4 * kF8Cus) return launch(fp8_skinny_kernel<8, 4, kWide, kFused>, 64, 8);
+    if constexpr (kFused)
+        if (fp8_blocks(K) > 8) return launch(fp8_skinny_kernel<16, 2, kWide, true>, 32, 16);
+    return launch(fp8_skinny_kernel<8, 2, kWide, kFused>, 32, 8);
 }
 
 template <bool kWide>
@@ -631,18 +655,17 @@ static hipError_t launch_few(const uint16_t *X, const uint8_t *qw, const float *
     return launch_skinny<kWide, true>(nullptr, nullptr, X, qw, sw, bias, M, N, K, Y, lds, stream);
 }
 
-// Every block quantizes all tokens anew: one launch pays where a compute unit does
-// not do it for too many groups (a token's 128 features) in all its blocks, or
-// where they are about one round of a block's threads. Times of a call in us, in
-// one / two launches: 1 x 5120 x 5120 (M x K x N, 50 groups a unit) 8.6 / 11.5, 2 x
-// 8192 x 8192 (256) 14.6 / 17.2, 3 x 5120 x 12288 (360) 13.1 / 15.1, 6 x 5120 x 5120
-// (300) 11.9 / 12.5, 16 x 2048 x 2048 (256) 7.2 / 8.1, 8 x 2048 x 12288 (384) 10.2 /
-// 10.2; 8 x 5120 x 5120 (400) 13.9 / 13.2, 8 x 4096 x 8192 (512) 15.6 / 12.8, 10 x 2048
-// x 12288 (480) 11.4 / 10.5. One round: 1 x 5120 x 65536 56.6 / 59.6, 1 x 2048 x 151936
-// 47.7 / 50.8. LDS for at most 384 groups: 51 KB.
+// Every block quantizes all tokens anew: one launch pays where a block does not do
+// it for too many groups (a token's 128 features; its threads do 32 or 64 at a
+// time), nor a compute unit in all its blocks. Times of a call in us, in one / two
+// launches: 1 x 5120 x 5120 (M x K x N) 8.2 / 11.0, 6 x 5120 x 5120 10.5 / 11.8, 16
+// x 2048 x 2048 6.8 / 8.5, 8 x 4096 x 4096 8.8 / 9.2, 2 x 8192 x 8192 14.9 / 16.8, 8 x
+// 2048 x 12288 9.9 / 10.2, 1 x 5120 x 30720 29.3 / 32.4, 4 x 2048 x 151936 54 / 58; 8 x
+// 5120 x 5120 11.9 / 11.8, 12 x 4096 x 4096 11.8 / 10.5, 13 x 2048 x 12288 11.4 / 10.7.
+// At most 256 groups: 34 KB of LDS.
 bool fp8_linear_in_one(int M, int N, int K) {
-    const int64_t groups = (int64_t)M * fp8_blocks(K), tiles = ((int64_t)N + 15) / 16;
-    return M <= kF8SkinnyTokens && (groups <= 40 || groups * std::max<int64_t>(tiles, kF8Cus) <= 384 * kF8Cus);
+    const int64_t groups = (int64_t)M * fp8_blocks(K), rounds = ((int64_t)N + 32 * kF8Cus - 1) / (32 * kF8Cus);
+    return M <= kF8SkinnyTokens && (groups <= 64 || groups * rounds <= 256);
 }
 
 hipError_t launch_fp8_linear_in_one(const uint16_t *X, const uint8_t *qw, const float *sw, const uint16_t *bias,
