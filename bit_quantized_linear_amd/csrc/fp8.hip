@@ -454,10 +454,11 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 // ---- the product, few tokens -----------------------------------------------
 
 // One block computes 16 NT output columns of at most 16 tokens; its W waves take
-// the groups of K in turn (wave w groups w, w + W, ...), straight from global
-// memory into the operands of the 16x16x128 MFMA (weights as A: row = output
-// column; tokens as B, for all NT tiles of columns), and add their sums in LDS in
-// a fixed order. The weight is read once: bound by HBM, and at these sizes by the
+// the groups of K in turn (part p of 16 has groups p, p + 16, ...; wave w of 8 the
+// parts w and w + 8, so that the order of a sum is the same with 16 waves and
+// with 8; of 64 columns, where there are always 8 waves, 8 parts), straight from global memory into the operands of the 16x16x128 MFMA
+// (weights as A: row = output column; tokens as B, for all NT tiles of columns),
+// and add the parts in LDS in order. The weight is read once: bound by HBM, and at these sizes by the
 // way to the first of it (a launch, a load's latency, the sums): 13 x 2048 x 12288
 // (M x K x N) takes 7.8 us (25 MB, 3.2 TB/s), 1 x 5120 x 5120 in one launch 8.4 (26
 // MB, 3.1 TB/s). Waves hide a load's latency better than loads ahead, whose
@@ -472,7 +473,8 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint16_t *__restrict__ X,
     const uint8_t *__restrict__ qw, const float *__restrict__ sw, const uint16_t *__restrict__ bias, int M, int N,
     int K, void *__restrict__ Y) {
-    __shared__ f32x4 red[W][NT][64];
+    constexpr int kSums = NT == 4 ? 8 : 16, kParts = kSums / W;  // parts of K, and how many a wave has
+    __shared__ f32x4 red[kSums][NT][64];
     extern __shared__ __align__(16) uint8_t codes_s[];
     const int n0 = blockIdx.x * 16 * NT;
     const int lane = threadIdx.x & 63;
@@ -496,9 +498,11 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
             __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, k + 64 < K ? off + 64 : kF8Oob, 0, 0)));
     };
 
-    f32x4 acc[NT];
+    f32x4 acc[kParts][NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < kParts; ++x)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[x][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int mrow = min(r16, M - 1);
 
     // Where rows are a multiple of 4 KB apart, the same group of all rows lies on a
@@ -522,7 +526,7 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
         }
         __syncthreads();
     }
-    for (int i = wave; i < G; i += W) {
+    auto group = [&](int i, f32x4(&to)[NT]) __attribute__((always_inline)) {
         const int g = turned(i);
         if (i != wave) {
 #pragma unroll
@@ -543,11 +547,18 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
         for (int t = 0; t < NT; ++t) {
             const f32x4 p = kWide ? mfma_wide_16x16x128(a[t], b, zero) : mfma_fp8_16x16x128(a[t], b, zero);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(s, p[e], acc[t][e]);
+            for (int e = 0; e < 4; ++e) to[t][e] = __builtin_fmaf(s, p[e], to[t][e]);
         }
+    };
+    for (int i = wave; i < G; i += kSums) {
+        group(i, acc[0]);
+        if constexpr (kParts == 2)
+            if (i + W < G) group(i + W, acc[1]);
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) red[wave][t][lane] = acc[t];
+    for (int x = 0; x < kParts; ++x)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) red[x * W + wave][t][lane] = acc[x][t];
     __syncthreads();
     for (int i = threadIdx.x; i < 256 * NT; i += 64 * W) {
         const int m = i / (16 * NT), c = i % (16 * NT);  // consecutive threads: consecutive columns of a token
@@ -556,7 +567,7 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
         if (m < M && n < N) {
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) v += red[w][c >> 4][src][c & 3];
+            for (int w = 0; w < kSums; ++w) v += red[w][c >> 4][src][c & 3];
             if (bias) v += bf16_bits_to_f32(bias[n]);
             if constexpr (kWide)
                 static_cast<float *>(Y)[(size_t)m * N + n] = v;

@@ -124,8 +124,13 @@ SHAPES = [(1, 16, 8), (1, 128, 16), (1, 144, 136), (2, 5120, 24), (7, 656, 1000)
           (65, 144, 136), (100, 1936, 1000), (128, 128, 128), (129, 656, 264), (257, 1024, 72), (500, 2064, 520)]
 
 
+# few tokens and many columns: 16, 32 and 64 columns per block, K in rows 4 KB apart, one launch and two
+WIDE = [(1, 400, 4096), (16, 1040, 4104), (3, 2000, 4104), (12, 4096, 4104), (16, 528, 8192), (2, 4096, 8200),
+        (13, 1152, 8200), (5, 144, 16384), (1, 2064, 16392), (4, 640, 16392), (16, 1040, 16392)]
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("M,K,N", SHAPES)
+@pytest.mark.parametrize("M,K,N", SHAPES + WIDE)
 def test_linear(M, K, N, out):
     bits = activations(M, K, M + N)
     qw, sw = weight(K, N, K + N)
