@@ -387,6 +387,15 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
         p.from = __builtin_amdgcn_readfirstlane(table.from[a]);
         p.count = __builtin_amdgcn_readfirstlane(table.from[a + 1]) - p.from;
     };
+    // Where rows are a multiple of 4 KB apart, the same group of all rows lies on a
+    // few memory channels, so each tile starts at another group (G is then a multiple
+    // of 32, and of a step). A layer for 64 tokens, H 4096, I 2048, 4 of 64 experts:
+    // 314 us, 330 without.
+    const int spread = H % 4096 ? 0 : (1 << (31 - __builtin_clz(G))) - 1;
+    auto group_of = [&](const Place &p) __attribute__((always_inline)) {
+        const int g = p.step * kUpWaves + wave, turned = g + ((p.i0 >> 4) & spread);
+        return spread && turned >= G ? turned - G : turned;
+    };
     auto advance = [&](Place &p) __attribute__((always_inline)) {
         if (++p.step < steps) return;
         p.step = 0;
@@ -421,11 +430,11 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
         }
         if constexpr (kSlots > 0) {
             __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what the slots held has been read
-            const int kx = p.item < items ? (p.step * kUpWaves + wave) * kF8Block : H;
+            const int kx = p.item < items ? group_of(p) * kF8Block : H;
 #pragma unroll
             for (int q = 0; q < kSlots; ++q) load_slot(rx, slots + (wave * kSlots + q) * kSlot, xrow[q], kx, H, chunk);
         }
-        const int k0 = (p.step * kUpWaves + wave) * kF8Block + 16 * q4;
+        const int k0 = group_of(p) * kF8Block + 16 * q4;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int k = k0 + 64 * i;
@@ -453,7 +462,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
             __builtin_amdgcn_s_waitcnt(0x0F70 | kLater);  // vmcnt(kLater)
             __builtin_amdgcn_sched_barrier(0);
         }
-        const int g = p.step * kUpWaves + wave;
+        const int g = group_of(p);
         const size_t block = ((size_t)p.e * 2 * gi + p.i0 / kF8Block) * G + min(g, G - 1);
         const float wg = fp8_scale_within(s13[block], g, G), wu = fp8_scale_within(s13[block + (size_t)gi * G], g, G);
         f32x4 pg = {0.f, 0.f, 0.f, 0.f}, pu = pg;
