@@ -425,8 +425,8 @@ __global__ __launch_bounds__(64 * WN * WM * KW, 1) void fp8_gemm_kernel(
 // blocks share each of the others (128 of its tokens each). 8 waves, one block
 // per compute unit: 130 KB of LDS hold two stages, and a stage's operands feed
 // 4 times the MFMAs that they take LDS reads for. Bound by the matrix cores: they
-// are busy 61 % of the time, at the clock that their power leaves (32760 x 5120 x
-// 5120: 690 to 725 us, 2.37 to 2.5 PFLOP/s; the library's product of the same
+// are busy 63 % of the time, at the clock that their power leaves (32760 x 5120 x
+// 5120: 690 to 740 us, 2.3 to 2.5 PFLOP/s; the library's product of the same
 // codes with one scale for all, 650 us). The rest is the epilogue, which nothing
 // overlaps (one tile's output is 128 KB), and the fill of each tile's first stage.
 __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
@@ -460,8 +460,8 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 // (weights as A: row = output column; tokens as B, for all NT tiles of columns),
 // and add the parts in LDS in order. The weight is read once: bound by HBM, and at these sizes by the
 // way to the first of it (a launch, a load's latency, the sums): 13 x 2048 x 12288
-// (M x K x N) takes 7.8 us (25 MB, 3.2 TB/s), 1 x 5120 x 5120 in one launch 8.4 (26
-// MB, 3.1 TB/s). Waves hide a load's latency better than loads ahead, whose
+// (M x K x N) takes 8.0 us (25 MB, 3.1 TB/s), 1 x 5120 x 5120 in one launch 8.6 (26
+// MB, 3.0 TB/s). Waves hide a load's latency better than loads ahead, whose
 // registers keep waves out: 1, 2, 3 and 4 groups in flight per wave take 8.5, 9.6,
 // 9.3 and 10.5 us for 1 x 5120 x 5120, 13.4, 14.6, 14.5 and 16.2 for 8 x 5120 x 12288.
 // kFused: from bf16 activations. While its first weights are on their way, each

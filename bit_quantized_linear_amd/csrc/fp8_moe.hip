@@ -336,8 +336,8 @@ constexpr int kUpRing = 3;      // steps under way per wave
 // significant bits), so that its rounding stays far below that of Y. kRoute:
 // every block also makes the choices, which saves a launch. Block 0 writes the
 // table down for the down projection. HBM-bound: 64 tokens, H 4096, I 1408, 128
-// experts 274 us (1.48 GB, 5.4 TB/s). The address and data units are busy 80 and
-// 90 % of that; with 4 steps ahead 271 us, but 14.4 instead of 13.8 for 23 tokens.
+// experts 265 us (1.48 GB, 5.6 TB/s). The address and data units are busy 73 and
+// 90 % of that; 4 steps ahead gain 1 % there and lose 4 % for 23 tokens.
 template <bool kRoute, int kSlots>
 __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
     const uint16_t *__restrict__ X, const uint8_t *__restrict__ w13, const float *__restrict__ s13,
