@@ -456,9 +456,10 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 // One block computes 16 NT output columns of at most 16 tokens; its W waves take
 // the groups of K in turn (part p of 16 has groups p, p + 16, ...; wave w of 8 the
 // parts w and w + 8, so that the order of a sum is the same with 16 waves and
-// with 8; of 64 columns, where there are always 8 waves, 8 parts), straight from global memory into the operands of the 16x16x128 MFMA
-// (weights as A: row = output column; tokens as B, for all NT tiles of columns),
-// and add the parts in LDS in order. The weight is read once: bound by HBM, and at these sizes by the
+// with 8; of 64 columns, where there are always 8 waves, 8 parts), straight from
+// global memory into the operands of the 16x16x128 MFMA (weights as A: row =
+// output column; tokens as B, for all NT tiles of columns), and add the parts in
+// LDS in order. The weight is read once: bound by HBM, and at these sizes by the
 // way to the first of it (a launch, a load's latency, the sums): 13 x 2048 x 12288
 // (M x K x N) takes 8.0 us (25 MB, 3.1 TB/s), 1 x 5120 x 5120 in one launch 8.6 (26
 // MB, 3.0 TB/s). Waves hide a load's latency better than loads ahead, whose

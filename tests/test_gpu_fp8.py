@@ -126,7 +126,8 @@ SHAPES = [(1, 16, 8), (1, 128, 16), (1, 144, 136), (2, 5120, 24), (7, 656, 1000)
 
 # few tokens and many columns: 16, 32 and 64 columns per block, K in rows 4 KB apart, one launch and two
 WIDE = [(1, 400, 4096), (16, 1040, 4104), (3, 2000, 4104), (12, 4096, 4104), (16, 528, 8192), (2, 4096, 8200),
-        (13, 1152, 8200), (5, 144, 16384), (1, 2064, 16392), (4, 640, 16392), (16, 1040, 16392)]
+        (13, 1152, 8200), (5, 144, 16384), (1, 2064, 16392), (4, 640, 16392), (16, 1040, 16392),
+        (16, 2048, 4200)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
