@@ -129,8 +129,8 @@ struct F8Wide {
 // added (4 FMAs a lane) while the next row tile's MFMAs run: the 16 x 16 x 128
 // MFMA and not the 32 x 32 x 64 one, whose results take two per group and four
 // times the registers (2150 against 2550 TFLOP/s at 32768 x 5120 x 5120).
-// NS stages take turns, loads NS - 1 ahead. KW = 2: two halves of the block
-// share K and add their sums at the end, for grids too small to fill the chip.
+// NS stages take turns, loads NS - 1 ahead. KW parts of the block share K and add
+// their sums at the end, for grids too small to fill the chip.
 // kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
 template <int WN, int WM, int TN, int TM, int NS, int KW, bool kWide, class Stage>
 __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, float *bias_s,
@@ -281,9 +281,11 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, flo
     // load unit has taken them all: 5 % slower at 32760 x 5120 x 5120). Two
     // stages run in pairs without a branch (a stage past K loads zeros and adds
     // none): with one the compiler spills.
-    static_assert(2 * TN >= kLoads, "the loads of a stage fit between its MFMAs");
+    constexpr int kTogether = (kLoads + 2 * TN - 1) / (2 * TN);  // loads at a time
     auto load_before = [&](Stage &nxt, int u) __attribute__((always_inline)) {
-        if (u % (TM / 2) == 0 && u / (TM / 2) < kLoads) issue(nxt, u / (TM / 2));
+        if (u % (TM / 2) == 0)
+#pragma unroll
+            for (int i = u / (TM / 2) * kTogether; i < min((u / (TM / 2) + 1) * kTogether, kLoads); ++i) issue(nxt, i);
     };
     auto run_stage = [&](int s, const Stage &cur, Stage &nxt) __attribute__((always_inline)) {
         next_stage();
@@ -340,18 +342,22 @@ __device__ __forceinline__ void fp8_tile(Stage &st0, Stage &st1, Stage &st2, flo
     for (int t = TN * TM - kDelay; t < TN * TM; ++t) add(t);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    // the waves of one part of K give their sums to those of the first
+    // the waves of the upper parts of K give their sums to those of the lower, in halves
     if constexpr (KW > 1) {
-        static_assert(KW == 2 && sizeof(Stage) >= sizeof(f32x4) * TN * TM * 64 * NW, "two parts, through one stage");
-        f32x4 *sums = reinterpret_cast<f32x4 *>(&st0) + wave * TN * TM * 64 + lane;
-        if (kw)
+        static_assert(sizeof(Stage) >= sizeof(f32x4) * TN * TM * 64 * NW * (KW / 2),
+                      "half the parts, through one stage");
 #pragma unroll
-            for (int t = 0; t < TN * TM; ++t) sums[t * 64] = acc[t / TM][t % TM];
-        __syncthreads();
-        if (!kw)
+        for (int half = KW / 2; half > 0; half /= 2) {
+            f32x4 *sums = reinterpret_cast<f32x4 *>(&st0) + ((kw % half) * NW + wave) * TN * TM * 64 + lane;
+            if (kw >= half && kw < 2 * half)
 #pragma unroll
-            for (int t = 0; t < TN * TM; ++t) acc[t / TM][t % TM] += sums[t * 64];
-        __syncthreads();
+                for (int t = 0; t < TN * TM; ++t) sums[t * 64] = acc[t / TM][t % TM];
+            __syncthreads();
+            if (kw < half)
+#pragma unroll
+                for (int t = 0; t < TN * TM; ++t) acc[t / TM][t % TM] += sums[t * 64];
+            __syncthreads();
+        }
     }
 
     // Output: 32 tokens x BN columns at a time through LDS (the waves of one
@@ -626,22 +632,32 @@ static hipError_t launch_skinny(const uint8_t *qx, const float *sx, const uint16
 template <bool kWide>
 static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                               const uint16_t *bias, int M, int N, int K, void *Y, hipStream_t stream) {
-    if (M <= kF8SkinnyTokens) {
-        return launch_skinny<kWide, false>(qx, sx, nullptr, qw, sw, bias, M, N, K, Y, 0, stream);
-    }
-    // Tiles of t x t: the larger, the less each operand is read; the smaller,
-    // the more compute units have one. Times in us for bf16, M x 5120 x 5120, by
-    // the rule / by the next smaller or larger tile: M = 17 10.8 / 14.1, 192 12.7
-    // / 15.7 (64, K in halves / not), 256 19.3 / 22.9, 384 22.1 / 24.9 (64 / K in
-    // halves, 128), 512 24.4 / 28.5, 768 27.2 / 39.4 (128, three stages / 64), 1024
-    // 38.0 / 48.9, 1536 44.3 / 46.6 (128, two stages / three, 256), 2048 57 / 75
-    // (256 / 128), 4096 108 / 123 (the last round's tiles shared / not).
     const auto tiles = [&](int64_t tn, int64_t tm) { return ((N + tn - 1) / tn) * ((M + tm - 1) / tm); };
+    // Up to 16 tokens: where the linear is one launch by the kernel for few tokens,
+    // its product alone gives the same bits. Elsewhere bf16 of more than 8 tokens is
+    // faster in tiles, which read them once for 32 or 64 columns: 8 tokens, 5120 x
+    // 5120 (K x N) 8.5 / 7.6 us, 4096 x 8192 7.8 / 8.2, 12288 x 1024 11.6 / 12.2; 16 tokens
+    // 9.7 / 7.8, 8.8 / 8.4, 13.7 / 12.2; fp32 9.8 / 10.0, 8.9 / 9.2, 13.7 / 18.0.
+    const bool few = M <= (kWide ? kF8SkinnyTokens : 8) ||
+                     (M <= kF8SkinnyTokens && (fp8_linear_in_one(M, N, K) || tiles(64, 32) > kF8Cus));
+    if (few) return launch_skinny<kWide, false>(qx, sx, nullptr, qw, sw, bias, M, N, K, Y, 0, stream);
+    // Tiles, the smallest of which no compute unit has more than one, up to 64 x 64:
+    // the larger, the less each operand is read; the smaller, the more compute units
+    // have one, and the more parts of K fit into LDS (4, 4 and 2). Times in us of M
+    // x 5120 x 5120, bf16 / fp32: M = 32 in tiles of 32 x 32 8.0 / 9.9, of 64 columns x
+    // 32 tokens 10.1 / 11.4, of 64 x 64 11.0 / 17.4; M = 96 13.5 / 18.1, 10.0 / 11.8,
+    // 11.6 / 17.9; M = 160 26 / 34, 20 / 22, 11.7 / 18.1.
     const int64_t small = tiles(64, 64);
+    if (tiles(32, 32) <= kF8Cus) return launch_tile<1, 1, 2, 2, 3, 4, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+    if (tiles(64, 32) <= kF8Cus) return launch_tile<2, 1, 2, 2, 3, 4, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     if (small <= kF8Cus) return launch_tile<2, 2, 2, 2, 3, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+    // Beyond: by the rule / by the next smaller or larger tile, bf16: M = 256 19.3 /
+    // 22.9, 384 22.1 / 24.9 (64 / K in halves, 128), 512 24.4 / 28.5, 768 27.2 / 39.4 (128,
+    // three stages / 64), 1024 38.0 / 48.9, 1536 44.3 / 46.6 (128, two stages / three,
+    // 256), 2048 57 / 75 (256 / 128), 4096 108 / 123 (the last round's tiles shared / not).
     if constexpr (kWide) {
-        // fp32: M = 128 19.1 / 26.4 (K in halves / not), 256 32.1 / 35.7, 1024 68.9 /
-        // 75.1 (64 / K in halves, 128), 1280 75.1 / 89.7, 4608 232 / 292 (128 / 64)
+        // fp32: M = 256 32.1 / 35.7, 1024 68.9 / 75.1 (64 / K in halves, 128), 1280 75.1 /
+        // 89.7, 4608 232 / 292 (128 / 64)
         if (small <= 6 * kF8Cus) return launch_tile<2, 2, 2, 2, 3, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
         return launch_tile<2, 2, 4, 4, 2, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     } else {

@@ -121,7 +121,8 @@ def run_linear(bits, qw, sw, bias, out, ws=None):
 
 SHAPES = [(1, 16, 8), (1, 128, 16), (1, 144, 136), (2, 5120, 24), (7, 656, 1000), (15, 1152, 64), (16, 2048, 40),
           (17, 400, 128), (31, 1936, 48), (33, 384, 264), (48, 272, 8), (63, 1040, 136), (64, 640, 128), (65, 16, 8),
-          (65, 144, 136), (100, 1936, 1000), (128, 128, 128), (129, 656, 264), (257, 1024, 72), (500, 2064, 520)]
+          (65, 144, 136), (100, 1936, 1000), (128, 128, 128), (129, 656, 264), (257, 1024, 72), (500, 2064, 520),
+          (11, 5136, 520), (16, 4112, 4104), (300, 400, 1032), (400, 400, 2056), (700, 400, 2056)]
 
 
 # few tokens and many columns: 16, 32 and 64 columns per block, K in rows 4 KB apart, one launch and two
