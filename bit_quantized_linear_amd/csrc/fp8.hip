@@ -641,31 +641,31 @@ static hipError_t launch_gemm(const uint8_t *qx, const float *sx, const uint8_t 
     const bool few = M <= (kWide ? kF8SkinnyTokens : 8) ||
                      (M <= kF8SkinnyTokens && (fp8_linear_in_one(M, N, K) || tiles(64, 32) > kF8Cus));
     if (few) return launch_skinny<kWide, false>(qx, sx, nullptr, qw, sw, bias, M, N, K, Y, 0, stream);
-    // Tiles, the smallest of which no compute unit has more than one, up to 64 x 64:
-    // the larger, the less each operand is read; the smaller, the more compute units
-    // have one, and the more parts of K fit into LDS (4, 4 and 2). Times in us of M
-    // x 5120 x 5120, bf16 / fp32: M = 32 in tiles of 32 x 32 8.0 / 9.9, of 64 columns x
-    // 32 tokens 10.1 / 11.4, of 64 x 64 11.0 / 17.4; M = 96 13.5 / 18.1, 10.0 / 11.8,
-    // 11.6 / 17.9; M = 160 26 / 34, 20 / 22, 11.7 / 18.1.
-    const int64_t small = tiles(64, 64);
+    // The smallest tile of which no compute unit has more than one: the larger, the
+    // less each operand is read; the smaller, the more compute units have one, and
+    // the more parts of K fit into LDS (4, 4, 2, 2 and, of 128 x 128, 1 for bf16 and 2
+    // for fp32, whose sums are slower). Times in us of M x 5120 x 5120, bf16 / fp32:
+    // M = 32 in tiles of 32 x 32 8.0 / 9.9, of 64 columns x 32 tokens 10.1 / 11.4, of
+    // 64 x 64 11.0 / 17.4; M = 96 13.5 / 18.1, 10.0 / 11.8, 11.6 / 17.9; M = 160 26 / 34, 20
+    // / 22, 11.7 / 18.1; M = 256 in 64 x 64 22.4 / 34.3, 64 columns x 128 tokens 16.9 /
+    // 28.6, 128 x 128 22.7 / 40.8; M = 512 33.3 / 51.3, 31.8 / 51.8, 22.9 / 41.2.
+    const int64_t small = tiles(64, 64), medium = tiles(128, 128);
     if (tiles(32, 32) <= kF8Cus) return launch_tile<1, 1, 2, 2, 3, 4, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     if (tiles(64, 32) <= kF8Cus) return launch_tile<2, 1, 2, 2, 3, 4, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     if (small <= kF8Cus) return launch_tile<2, 2, 2, 2, 3, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
-    // Beyond: by the rule / by the next smaller or larger tile, bf16: M = 256 19.3 /
-    // 22.9, 384 22.1 / 24.9 (64 / K in halves, 128), 512 24.4 / 28.5, 768 27.2 / 39.4 (128,
-    // three stages / 64), 1024 38.0 / 48.9, 1536 44.3 / 46.6 (128, two stages / three,
-    // 256), 2048 57 / 75 (256 / 128), 4096 108 / 123 (the last round's tiles shared / not).
+    if (tiles(64, 128) <= kF8Cus) return launch_tile<2, 2, 2, 4, 3, 2, kWide>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     if constexpr (kWide) {
-        // fp32: M = 256 32.1 / 35.7, 1024 68.9 / 75.1 (64 / K in halves, 128), 1280 75.1 /
-        // 89.7, 4608 232 / 292 (128 / 64)
+        // beyond, several small blocks on a compute unit, or two of 128 x 128: M = 1024
+        // 65.8 / 74.4, 1280 89.7 / 75.1, 4608 292 / 232
+        if (medium <= kF8Cus) return launch_tile<2, 2, 4, 4, 2, 2, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
         if (small <= 6 * kF8Cus) return launch_tile<2, 2, 2, 2, 3, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
         return launch_tile<2, 2, 4, 4, 2, 1, true>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
     } else {
-        const int64_t medium = tiles(128, 128), big = tiles(256, 256);
-        if (medium < kF8Cus / 2) return launch_tile<2, 2, 2, 2, 3, 1, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
-        // three stages of a 128 x 128 tile fill a compute unit's LDS, of two
-        // stages two blocks share it
-        if (medium <= kF8Cus) return launch_tile<2, 2, 4, 4, 3, 1, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
+        // 8 waves and three stages of a 128 x 128 tile, 4 waves and two where two
+        // blocks share a compute unit (M = 768 25.4, 1024 45.1 / 35.0, 37.9); 256 x 256
+        // from half a round of them on (M = 1536 46.6, with 128 42.2; 2048 57, with 128 73)
+        const int64_t big = tiles(256, 256);
+        if (medium <= kF8Cus) return launch_tile<2, 4, 4, 2, 3, 1, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
         if (big < kF8Cus / 2) return launch_tile<2, 2, 4, 4, 2, 1, false>(qx, sx, qw, sw, bias, M, N, K, Y, stream);
         // the tiles of a last round that would leave half the compute units
         // idle are shared by two blocks each

@@ -151,7 +151,10 @@ def test_linear(M, K, N, out):
     assert np.array_equal(H.host(Y).view(np.uint8), H.host(Y2).view(np.uint8))
 
 
-@pytest.mark.parametrize("M,K,N,out", [(4100, 400, 2056, "bf16"), (2300, 1936, 4360, "f32"), (6000, 128, 2048, "bf16")])
+@pytest.mark.parametrize("M,K,N,out", [(4100, 400, 2056, "bf16"), (2300, 1936, 4360, "f32"), (6000, 128, 2048, "bf16"),
+                                         (1700, 400, 2056, "bf16"), (1700, 400, 2056, "f32"), (2100, 272, 2056, "f32"),
+                                         (2100, 272, 2056, "bf16"), (900, 1040, 1544, "bf16"),
+                                         (900, 1040, 1544, "f32")])
 def test_linear_many_tokens(M, K, N, out):
     bits = activations(M, K, M)
     qw, sw = weight(K, N, N)
