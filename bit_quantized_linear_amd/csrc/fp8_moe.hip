@@ -540,32 +540,38 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
 // ---- down projection and weighted sum ----------------------------------------
 
 constexpr int kDownAhead = 4;  // groups of weights per set; two sets take turns
-constexpr int kDownTokens = 8;  // of an expert at a time
 
-// One block: 16 output columns of every token. A wave takes one reached expert
+// One block: kCols output columns of every token. A wave takes one reached expert
 // and one of 2^shift shares of I at a time (a unit; all of a wave's are the same
-// share), reads its 16 weight rows once, a batch of groups ahead of their use,
-// and leaves each pair's 16 sums in LDS at its own place; then each output is the
+// share), reads its weight rows once, a batch of groups ahead of their use,
+// and leaves each pair's sums in LDS at their own place; then each output is the
 // weighted sum over its token's pairs in order, so the result does not depend on
 // which wave came first. 16 waves of 4 groups' weights each are the loads under
 // way; the rows of h come through LDS (above), filling kDownSlots slots at a time,
 // each a wait for memory: 4 slots where the sums leave them room (a layer for 8
-// tokens of 64 experts 98.7 us, with 2 slots 99.4). HBM-bound: 64 tokens, H 4096, I 1408, 128
-// experts 158 us (0.74 GB, 4.7 TB/s).
-template <int kDownSlots>
+// tokens of 64 experts 98.7 us, with 2 slots 99.4). HBM-bound: 64 tokens, H 4096,
+// I 1408, 128 experts 158 us (0.74 GB, 4.7 TB/s).
+// kCols 8: the MFMA's rows 8 .. 15 are the same columns in the unit's next group,
+// and its columns 8 .. 15 the tokens there, so that two quadrants of the result
+// hold the sums of a group each.
+template <int kDownSlots, int kCols>
 __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     const uint8_t *__restrict__ w2, const float *__restrict__ s2, const uint16_t *__restrict__ h_hi,
     const uint16_t *__restrict__ h_lo, const float *__restrict__ gate, const MoeTable *__restrict__ table_in, int T,
     int H, int I, int top_k, int shift, uint16_t *__restrict__ Y) {
     __shared__ MoeTable table;
     __shared__ float gate_s[kMaxPairs];
-    extern __shared__ __align__(16) uint8_t smem[];  // slots [waves][2][kDownSlots], then sums [splits][T top_k][16]
+    extern __shared__ __align__(16) uint8_t smem[];  // slots [waves][2][kDownSlots], then sums [splits][T top_k][kCols]
     float *out = reinterpret_cast<float *>(smem + kDownWaves * 2 * kDownSlots * kSlot);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint8_t *slots = smem + wave * 2 * kDownSlots * kSlot;
     const int r16 = lane & 15, q4 = lane >> 4;
-    const int n0 = blockIdx.x * 16;
+    constexpr int kHalves = 16 / kCols;           // groups per step
+    constexpr int kTokens = kHalves == 1 ? 8 : 4;  // of an expert at a time
+    const int half = r16 / kCols, col = r16 % kCols;  // of the operands
+    const int half_out = 4 * q4 / kCols;              // of the result's rows 4 q4 ...
+    const int n0 = blockIdx.x * kCols;
     const int pairs = T * top_k;
     const int G = (I + kF8Block - 1) / kF8Block, gh = (H + kF8Block - 1) / kF8Block;
     const __amdgpu_buffer_rsrc_t rh = fp8_rsrc(h_hi, (uint32_t)pairs * (uint32_t)I * 2u);
@@ -581,7 +587,7 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
     __syncthreads();
     const int splits = 1 << shift, s = wave & (splits - 1);
     const int reached = __builtin_amdgcn_readfirstlane(table.reached);
-    const int all = (G - s + splits - 1) >> shift;  // groups of a unit
+    const int groups = (G - s + splits - 1) >> shift, all = (groups + kHalves - 1) / kHalves;  // and steps of a unit
 
     // where a wave is (a: the reached expert's number): batch `first` (of the unit's groups) for tokens m0 ...
     struct Place {
@@ -599,26 +605,26 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
         p.first += kDownAhead;
         if (p.first < all) return;
         p.first = 0;
-        p.m0 += kDownTokens;
+        p.m0 += kTokens;
         if (p.m0 < p.count) return;
         p.a += kDownWaves >> shift;
         enter(p);
     };
     auto load_weights = [&](u32x4(&to)[kDownAhead][2], const Place &p) __attribute__((always_inline)) {
-        const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(w2 + ((size_t)p.e * H + n0) * I, 16u * (uint32_t)I);
+        const __amdgpu_buffer_rsrc_t rw = fp8_rsrc(w2 + ((size_t)p.e * H + n0) * I, (uint32_t)kCols * (uint32_t)I);
 #pragma unroll
         for (int n = 0; n < kDownAhead; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int k = (s + ((p.first + n) << shift)) * kF8Block + 64 * i + 16 * q4;
-                to[n][i] = load16(rw, k < I ? (uint32_t)r16 * (uint32_t)I + (uint32_t)k : kMoeOob);  // zeros past I
+                const int k = (s + (((p.first + n) * kHalves + half) << shift)) * kF8Block + 64 * i + 16 * q4;
+                to[n][i] = load16(rw, k < I ? (uint32_t)col * (uint32_t)I + (uint32_t)k : kMoeOob);  // zeros past I
             }
     };
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     // one batch from `now`, the next one's weights to `next`
     auto batch = [&](Place &p, const u32x4(&now)[kDownAhead][2], u32x4(&next)[kDownAhead][2])
                      __attribute__((always_inline)) {
-        const int here = min(kDownTokens, p.count - p.m0), per = slots_of(here);
+        const int here = min(kTokens, p.count - p.m0), per = kHalves == 1 ? slots_of(here) : 1;
         const Place at = p;
         uint32_t row[2];
 #pragma unroll
@@ -629,11 +635,11 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
         advance(p);
 #pragma unroll
         for (int n = 0; n < kDownAhead; ++n) {
-            if (n * per % kDownSlots == 0) {  // the slots are empty: fill them, lo behind hi
+            if (n * kHalves * per % kDownSlots == 0) {  // the slots are empty: fill them, lo behind hi
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what they held has been read
 #pragma unroll
                 for (int q = 0; q < kDownSlots; ++q) {
-                    const int k = (s + ((at.first + n + (per == 1 ? q : q / 2)) << shift)) * kF8Block;
+                    const int k = (s + (((at.first + n) * kHalves + (per == 1 ? q : q / 2)) << shift)) * kF8Block;
                     load_slot(rh, slots + q * kSlot, (q & 1) && per > 1 ? row[1] : row[0], k, I, chunk);
                     load_slot(rl, slots + (kDownSlots + q) * kSlot, (q & 1) && per > 1 ? row[1] : row[0], k, I, chunk);
                 }
@@ -649,7 +655,7 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (at.first + n >= all) break;
-            const uint8_t *hi = slots + n * per % kDownSlots * kSlot, *lo = hi + kDownSlots * kSlot;
+            const uint8_t *hi = slots + (n * kHalves * per % kDownSlots + half) * kSlot, *lo = hi + kDownSlots * kSlot;
             const int token = r16 & (4 * per - 1);
             f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -661,13 +667,23 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
                 sum = mfma_bf16_16x16x32(a0, slot_read(hi, token, c), sum);
                 sum = mfma_bf16_16x16x32(a1, slot_read(hi, token, c + 1), sum);
             }
-            const float w = sw[s + ((at.first + n) << shift)];
+            const int group = (at.first + n) * kHalves;
+            float w = sw[s + (group << shift)];
+            if constexpr (kHalves == 2) {  // the second half may be past the last group
+                const float w1 = fp8_scale_within(sw[s + (min(group + 1, groups - 1) << shift)], group, groups - 1);
+                w = half_out ? w1 : w;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w, sum[i], acc[i]);
         }
-        if (at.first + kDownAhead >= all && r16 < here) {
-            const uint32_t pair = pair_of(table.pair[at.from + at.m0 + r16]);
-            *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + pair) * 16 + 4 * q4) = acc;
+        if (at.first + kDownAhead >= all) {
+            if constexpr (kHalves == 2)  // rows 0 .. 7 of columns 0 .. 7, and rows 8 .. 15 of columns 8 .. 15
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor(acc[i], 40);
+            if (r16 < here && half_out == 0) {
+                const uint32_t pair = pair_of(table.pair[at.from + at.m0 + r16]);
+                *reinterpret_cast<f32x4 *>(out + ((size_t)s * pairs + pair) * kCols + 4 * q4) = acc;
+            }
         }
     };
     Place p;
@@ -681,12 +697,12 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(
         batch(p, c1, c0);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < T * 16; i += kDownThreads) {
-        const int t = i >> 4, c = i & 15;
+    for (int i = threadIdx.x; i < T * kCols; i += kDownThreads) {
+        const int t = i / kCols, c = i % kCols;
         float y = 0.0f;
         for (int j = 0; j < top_k; ++j) {
             float o = 0.0f;
-            for (int s = 0; s < splits; ++s) o += out[((size_t)s * pairs + t * top_k + j) * 16 + c];
+            for (int s = 0; s < splits; ++s) o += out[((size_t)s * pairs + t * top_k + j) * kCols + c];
             y = __builtin_fmaf(gate_s[t * top_k + j], o, y);
         }
         Y[(size_t)t * H + n0 + c] = (uint16_t)f32_to_bf16_bits(y);
@@ -757,16 +773,24 @@ hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *
                                  : launch_up(moe_up_kernel<false, 0>);
     }
     if (err != hipSuccess) return err;
-    // as many shares of I as give every wave a unit, at most one per group and
-    // what 32 KB of LDS hold
+    // 8 columns per block where 16 would leave half the compute units without one:
+    // twice the blocks, if an expert has few tokens (4 at a time instead of 8) and the
+    // groups of I fill the steps of two. A layer with 16 / 8 columns: H 2048, I 768, 32
+    // x 4 of 64 experts 80.8 / 73.0 us, 64 x 6 of 64 110.7 / 105.6, H 448, I 720, 37 x 6 of 60
+    // 56.3 / 52.5; 17 x 6 of 6 31.8 / 32.7; I 336, H 768, 53 x 3 of 118 47.0 / 49.9; H 4096, I
+    // 1408, 8 x 4 of 64 97 / 109. As many shares of I as give every wave a unit, at most
+    // one per step and what 32 KB of LDS hold.
     const int G = fp8_blocks(I);
+    const int cols = H / 16 <= kUpBlocks / 2 && G > 4 && pairs <= 8 * E ? 8 : 16;
+    const int steps = (G * cols + 15) / 16;
     int shift = 0;
-    while (most << shift < kDownWaves && 2 << shift <= G && (2 << shift) * pairs * 64 <= (32 << 10)) ++shift;
-    const size_t sums = (size_t)pairs * 64 << shift;
+    while (most << shift < kDownWaves && 2 << shift <= steps && (2 << shift) * pairs * cols * 4 <= (32 << 10)) ++shift;
+    const size_t sums = (size_t)pairs * cols * 4 << shift;
     const int slots = sums <= (24 << 10) ? 4 : 2;  // in 160 KB, 7 of them the table and weights
     const size_t lds = (size_t)kDownWaves * 2 * slots * kSlot + sums;
-    const auto down = slots == 4 ? moe_down_kernel<4> : moe_down_kernel<2>;
-    hipLaunchKernelGGL(down, dim3(H / 16), dim3(kDownThreads), lds, stream, w2, s2, h_hi, h_lo, gate, table,
+    const auto down = cols == 8 ? slots == 4 ? moe_down_kernel<4, 8> : moe_down_kernel<2, 8>
+                                : slots == 4 ? moe_down_kernel<4, 16> : moe_down_kernel<2, 16>;
+    hipLaunchKernelGGL(down, dim3(H / cols), dim3(kDownThreads), lds, stream, w2, s2, h_hi, h_lo, gate, table,
                        T, H, I, top_k, shift, Y);
     return hipGetLastError();
 }

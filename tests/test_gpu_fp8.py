@@ -243,7 +243,8 @@ MOE = [(1, 16, 16, 1, 1), (1, 128, 32, 256, 16), (1, 128, 64, 4, 2), (1, 2048, 7
        (3, 1040, 144, 33, 3),
        (5, 272, 400, 256, 16), (8, 512, 256, 8, 4), (17, 656, 48, 3, 1), (23, 1072, 400, 40, 3), (33, 256, 272, 6, 2),
        (64, 384, 128, 2, 2), (64, 512, 144, 100, 8), (64, 128, 64, 70, 16),
-       (1, 4096, 32, 40, 2), (30, 4096, 48, 9, 2)]
+       (1, 4096, 32, 40, 2), (30, 4096, 48, 9, 2), (40, 464, 656, 60, 6), (3, 144, 784, 20, 2), (64, 272, 1040, 64, 7),
+       (64, 144, 656, 128, 16)]
 
 
 @pytest.mark.parametrize("renorm", [True, False])
