@@ -155,12 +155,13 @@ def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None):
         raise TypeError(f"{name}: device entry points take GPU tensors")
     if not t.is_contiguous():
         raise TypeError(f"{name}: tensors must be contiguous")
-    if itemsize is not None and t.element_size() != itemsize:
-        raise TypeError(f"{name}: expected {itemsize}-byte elements, got {t.element_size()}")
+    size = t.element_size()
+    if itemsize is not None and size != itemsize:
+        raise TypeError(f"{name}: expected {itemsize}-byte elements, got {size}")
     dev = _current_device() if device is None else device
     if t.device.index != dev:
         raise TypeError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{dev}")
-    have = t.numel() * t.element_size()
+    have = t.numel() * size
     if have < nbytes:
         raise ValueError(f"{name}: {have} bytes, the call needs at least {nbytes}")
     return t.data_ptr()
@@ -551,14 +552,16 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
     E, Hr = _shape2(wr, "wr")
     if w13 is None or w13.dim() != 4 or w2 is None or w2.dim() != 3:
         raise TypeError("w13 must be a 4-D and w2 a 3-D tensor")
-    I = int(w13.shape[2])  # noqa: E741
-    if Hr != H or tuple(w13.shape) != (E, 2, I, H) or tuple(w2.shape) != (E, H, I):
-        raise ValueError(f"X [{T}, {H}], wr [{E}, {Hr}], w13 {list(w13.shape)} and w2 {list(w2.shape)} do not fit")
+    shape13, shape2 = w13.shape, w2.shape
+    I = int(shape13[2])  # noqa: E741
+    if Hr != H or shape13 != (E, 2, I, H) or shape2 != (E, H, I):
+        raise ValueError(f"X [{T}, {H}], wr [{E}, {Hr}], w13 {list(shape13)} and w2 {list(shape2)} do not fit")
     for name, t in (("idx", idx), ("gate", gate)):
         if t is not None:
             rows, k = _shape2(t, name)
-            top_k = k if top_k is None else top_k
-            if (rows, k) != (T, top_k):
+            if top_k is None:
+                top_k = k
+            if rows != T or k != top_k:
                 raise ValueError(f"{name} is [{rows}, {k}], the call writes [{T}, {top_k}]")
     if top_k is None:
         raise ValueError("top_k is needed where neither idx nor gate is given")
