@@ -548,8 +548,8 @@ size_t svdq_fp8_moe_workspace_bytes(int T, int I, int E, int top_k);
  *      H % 16 == 0, I % 16 == 0, 1 <= E <= SVDQ_FP8_MOE_MAX_EXPERTS,
  *      1 <= top_k <= min(E, SVDQ_FP8_MOE_MAX_TOP_K), H < 2^22, I < 2^22,
  *      T * top_k * I < 2^30.
- * The weights of the experts that some token chose are read once (w13 of an
- * expert with more than 16 tokens once per 16, w2 with more than 8 once per 8).
+ * The weights of the experts that some token chose are read once for 8 or 16
+ * (w13; 4 in a call of up to 4 tokens) and 4 or 8 (w2) of the expert's tokens.
  * Deterministic; a token's outputs depend on its own row of X only. A token
  * with logits that are not finite has a full choice of experts all the same;
  * its weights and outputs may be NaN.
