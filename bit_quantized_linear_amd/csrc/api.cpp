@@ -84,11 +84,11 @@ svdq_status check_w4a4_shape(int M, int K, int rank, int group) {
 }
 
 // Block-scaled FP8: a tile's rows are addressed with 32-bit offsets (256 rows
-// of K bytes); columns rounded up to a tile stay below 2^31; a launch has fewer
-// than 2^32 threads along its grid's first dimension, 16 per token at the most.
+// of K bytes); a launch has fewer than 2^32 threads along its grid's first
+// dimension, 16 per token or 32 per column at the most.
 constexpr int kFp8MaxK = 1 << 22;
 constexpr int kFp8MaxTokens = (1 << 28) - 16;
-constexpr int kFp8MaxColumns = 0x7FFFFFFF - 511;
+constexpr int kFp8MaxColumns = (1 << 27) - 32;
 
 svdq_status check_fp8_linear_shape(int M, int N, int K, int y_dtype) {
     if (M < 0 || N <= 0 || K <= 0) return SVDQ_ERR_INVALID_ARGUMENT;

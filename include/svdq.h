@@ -500,7 +500,7 @@ svdq_status svdq_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, 
  * In:  qx, sx (svdq_fp8_quantize_act); qw, sw (svdq_fp8_prepare_weights);
  *      bias [N] bf16 or NULL; y_dtype SVDQ_BF16 or SVDQ_F32.
  * Out: Y [M, N]. Shapes: M >= 0 (M == 0 launches nothing), K % 16 == 0,
- *      N % 8 == 0, K < 2^22, M <= 2^28 - 16, N < 2^31 - 511. Deterministic.
+ *      N % 8 == 0, K < 2^22, M <= 2^28 - 16, N <= 2^27 - 32. Deterministic.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
  *      HIP. */
 svdq_status svdq_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,

@@ -36,6 +36,7 @@ def moe(X=FAKE, wr=FAKE, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, T=2, H=64, I=32, 
     (gemm, {"M": -1}, INVALID), (gemm, {"N": 0}, INVALID), (gemm, {"K": 72}, SHAPE), (gemm, {"N": 60}, SHAPE),
     (gemm, {"K": 1 << 22}, SHAPE), (gemm, {"M": 2147483647, "N": 8}, SHAPE), (gemm, {"M": 1, "N": 2147483640}, SHAPE),
     (quantize, {"M": 2147483647}, SHAPE), (quantize, {"M": (1 << 28) - 15}, SHAPE),
+    (gemm, {"M": 1, "N": 1 << 27}, SHAPE), (linear, {"M": 1, "N": (1 << 27) - 24, "K": 16}, SHAPE),
     (gemm, {"M": (1 << 28) - 15, "N": 8}, SHAPE), (linear, {"M": (1 << 28) - 15, "N": 8}, SHAPE),
     (gemm, {"M": 2147483647, "N": 2147483640}, SHAPE), (gemm, {"dt": 2}, INVALID),
     (gemm, {"qw": None}, INVALID), (gemm, {"sx": None}, INVALID), (gemm, {"Y": None}, INVALID),
