@@ -31,11 +31,14 @@ __device__ __forceinline__ void fp8_barrier() {
 
 // E4M3 x E4M3 with fp32 accumulation, unscaled. A lane's operand is 32 codes
 // of one row (A) or column (B). The matrix core adds the 8 products of a lane's 8 consecutive
-// codes aligned to the largest of them and cuts what lies 14 or more bits
-// below its leading one (measured: 2^16 + 2^3 is exact, 2^16 + 7.5 gives
-// 2^16); everything else is summed as in fp32. That is a relative error of
-// about 2e-5 of a sum of random products: a hundredth of bf16's rounding, but
-// two hundred times that of fp32, so outputs in fp32 take the bf16 MFMA
+// codes after cutting each, toward zero, to a multiple of 2^(e - 13), e the
+// largest sum of two codes' exponents among the products that are not 0 (a code
+// below 2^-6 counts as 2^-6); everything else is summed as in fp32. (Measured: 2^16 +
+// 2^3 is exact, 2^16 + 7.5 gives 2^16, and a model by this rule has the same bits
+// on random codes.) A run of codes from 2^-6 up loses less than 7 * 2^-13 of its
+// largest product. Of a sum of random products that is about 1e-5: three hundredths
+// of bf16's rounding's 2^-9, but a hundred times that of fp32, and of a sum
+// that cancels it can be any part. So outputs in fp32 take the bf16 MFMA
 // (mfma_wide_*), whose operands hold E4M3 values exactly and whose sums keep
 // 24 bits.
 __device__ __forceinline__ f32x4 mfma_fp8_16x16x128(i32x8 a, i32x8 b, f32x4 c) {

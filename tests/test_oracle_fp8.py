@@ -95,3 +95,27 @@ def test_prepare_weights_zero_and_refusals():
     with pytest.raises(b.SvdqError) as e:
         b.svdq_fp8_prepare_weights(bad)
     assert e.value.status == b.SVDQ_ERR_NUMERICAL
+
+
+def test_cut_sums_by_hand_and_by_loops():
+    x, w = np.zeros((1, 144)), np.zeros((2, 144))
+    x[0, :3], w[0, :3] = [256.0, 2.0, 2.5], [256.0, 4.0, 3.0]  # 2^16, 8 and 7.5 in one run: 7.5 goes
+    x[0, 130:132], w[1, 130:132] = [2.0 ** -9, 2.0 ** -9], [256.0, 2.0 ** -3]  # a subnormal counts as 2^-6
+    s = o8.cut_sums(o8.e4m3_encode(x), o8.e4m3_encode(w))
+    assert s.shape == (2, 1, 2) and s[0, 0, 0] == 2.0 ** 16 + 8 and s[0, 0, 1] == 0
+    assert s[1, 0, 1] == 0.5 and s[1, 0, 0] == 0
+    rng = np.random.default_rng(5)
+    qx, qw = (rng.integers(0, 127, (n, 32)).astype(np.uint8) | (rng.integers(0, 2, (n, 32)) << 7).astype(np.uint8)
+              for n in (3, 4))
+    s, vx, vw = o8.cut_sums(qx, qw), o8.e4m3_decode(qx), o8.e4m3_decode(qw)
+    expo = lambda v: max(int(np.floor(np.log2(abs(v)))), -6)  # noqa: E731
+    for m in range(3):
+        for n in range(4):
+            total = 0.0
+            for k in range(0, 32, 8):
+                pairs = [(a, c) for a, c in zip(vx[m, k: k + 8], vw[n, k: k + 8]) if a * c]
+                unit = 2.0 ** (max(expo(a) + expo(c) for a, c in pairs) - 13)
+                total += sum(np.sign(a * c) * np.floor(abs(a * c) / unit) * unit for a, c in pairs)
+            assert s[0, m, n] == total
+    sx, sw = np.full((1, 3), 2.0, np.float32), np.full((1, 1), 0.5, np.float32)
+    assert np.array_equal(o8.forward_cut(qx, sx, qw, sw, [1.0, 2.0, 3.0, 4.0]), s[0] + [[1.0, 2.0, 3.0, 4.0]])
