@@ -191,6 +191,16 @@ def _stream(stream):
     return _raw_stream()
 
 
+def _forget_device():
+    global _device_of, _raw_stream
+    _device_of = _raw_stream = None
+
+
+# a forked child cannot use its parent's GPU: it asks torch anew, whose own
+# check says so
+os.register_at_fork(after_in_child=_forget_device)
+
+
 # ------------------------------------------------------------------ info --
 
 def svdq_version() -> int:
