@@ -515,17 +515,23 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _fp8_out(Y, M, N, dev):
+    """Pointer and type code of the output Y [M, N], whose element size says which type it is."""
+    if Y is None:
+        raise TypeError("Y: a tensor is needed, its element size gives the output's type")
+    wide = Y.element_size()
+    return _dev_ptr(Y, 4 if wide == 4 else 2, M * N * wide, "Y", dev), SVDQ_F32 if wide == 4 else SVDQ_BF16
+
+
 def svdq_fp8_gemm(qx, sx, qw, sw, bias, Y, stream=None):
     """Y [M, N] (bf16 or fp32, by its element size) of quantized activations
     qx [M, K], sx and the block-scaled weight qw [N, K], sw."""
     M, K = _shape2(qx, "qx")
     dev = _current_device()
     N, qwp, swp = _fp8_weight(qw, sw, K, dev)
-    wide = Y.element_size()
+    Yp, out = _fp8_out(Y, M, N, dev)
     st = lib().svdq_fp8_gemm(_dev_ptr(qx, 1, M * K, "qx", dev), _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev),
-                             qwp, swp, _dev_ptr(bias, 2, N * 2, "bias", dev), M, N, K,
-                             _dev_ptr(Y, 4 if wide == 4 else 2, M * N * wide, "Y", dev),
-                             SVDQ_F32 if wide == 4 else SVDQ_BF16, _stream(stream))
+                             qwp, swp, _dev_ptr(bias, 2, N * 2, "bias", dev), M, N, K, Yp, out, _stream(stream))
     _check("svdq_fp8_gemm", st)
 
 
@@ -539,12 +545,11 @@ def svdq_fp8_linear(X, qw, sw, bias, workspace, Y, stream=None):
     M, K = _shape2(X, "X")
     dev = _current_device()
     N, qwp, swp = _fp8_weight(qw, sw, K, dev)
-    wide = Y.element_size()
+    Yp, out = _fp8_out(Y, M, N, dev)
     ws_need = svdq_fp8_workspace_bytes(M, K)
     st = lib().svdq_fp8_linear(_dev_ptr(X, 2, M * K * 2, "X", dev), qwp, swp, _dev_ptr(bias, 2, N * 2, "bias", dev),
-                               M, N, K, _dev_ptr(workspace, None, ws_need, "workspace", dev), _nbytes(workspace),
-                               _dev_ptr(Y, 4 if wide == 4 else 2, M * N * wide, "Y", dev),
-                               SVDQ_F32 if wide == 4 else SVDQ_BF16, _stream(stream))
+                               M, N, K, _dev_ptr(workspace, None, ws_need, "workspace", dev), _nbytes(workspace), Yp,
+                               out, _stream(stream))
     _check("svdq_fp8_linear", st)
 
 

@@ -135,3 +135,12 @@ def test_moe_shapes_that_do_not_fit(guarded, monkeypatch):  # noqa: F811
             call({**t, arg: Dev(shape, t[arg].element_size())})
     with pytest.raises(ValueError):
         b.svdq_fp8_moe_layer(t["X"], t["wr"], t["w13"], t["s13"], t["w2"], t["s2"], t["Y"], None, None, t["ws"])
+
+
+@pytest.mark.parametrize("name", ["gemm", "linear"])
+def test_an_output_is_needed_for_its_type(name, guarded, monkeypatch):  # noqa: F811
+    sized = SizeQueries(guarded)
+    monkeypatch.setattr(b, "lib", lambda: sized)
+    call, t = _case(name)
+    with pytest.raises(TypeError, match="Y"):
+        call({**t, "Y": None})
