@@ -141,14 +141,15 @@ def _current_device():
     return _device_of()
 
 
-def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None):
+def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None, formats=None):
     """Device pointer of a torch tensor (None -> NULL).
 
     The library receives raw pointers and sizes, so the extent a call will
     touch is checked here, before anything is launched: the tensor must be a
     contiguous GPU tensor on the current device (`device`, looked up when not
-    given) holding at least `nbytes` bytes. A violation raises TypeError
-    (kind, layout, element size, device) or ValueError (too small)."""
+    given) holding at least `nbytes` bytes, of one of the types `formats` where
+    they are given. A violation raises TypeError (kind, layout, element size,
+    type, device) or ValueError (too small)."""
     if t is None:
         return None
     if not t.is_cuda:
@@ -158,6 +159,10 @@ def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None):
     size = t.element_size()
     if itemsize is not None and size != itemsize:
         raise TypeError(f"{name}: expected {itemsize}-byte elements, got {size}")
+    if formats is not None:
+        dtype = getattr(t, "dtype", None)
+        if dtype is not None and dtype not in formats:
+            raise TypeError(f"{name}: {dtype}, the call takes {', '.join(sorted(map(str, formats)))}")
     dev = _current_device() if device is None else device
     if t.device.index != dev:
         raise TypeError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{dev}")
@@ -495,12 +500,31 @@ def w4a16_linear(X, packed, bias, Y, N, group=GROUP, stream=None):
     _check("w4a16_linear", st)
 
 
+_fp8_types = None
+
+
+def _fp8_formats():
+    """The torch types of E4M3 codes, bf16, fp32 and int32 numbers at the
+    block-scaled FP8 entry points. Integers of the width hold the bits, as
+    elsewhere; another format of the same width (float16, e4m3fnuz, e5m2) would
+    be read as something else."""
+    global _fp8_types
+    if _fp8_types is None:
+        import torch as t
+
+        _fp8_types = (frozenset((t.float8_e4m3fn, t.uint8, t.int8)), frozenset((t.bfloat16, t.int16, t.uint16)),
+                      frozenset((t.float32,)), frozenset((t.int32, t.uint32)))
+    return _fp8_types
+
+
 def svdq_fp8_quantize_act(X, qx, sx, stream=None):
     """E4M3 codes qx [M, K] (1-byte elements) and scales sx [ceil(K/128), M] of X [M, K] bf16."""
     M, K = _shape2(X, "X")
     dev = _current_device()
-    st = lib().svdq_fp8_quantize_act(_dev_ptr(X, 2, M * K * 2, "X", dev), M, K, _dev_ptr(qx, 1, M * K, "qx", dev),
-                                     _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev), _stream(stream))
+    e4m3, bf16, f32, _ = _fp8_formats()
+    st = lib().svdq_fp8_quantize_act(_dev_ptr(X, 2, M * K * 2, "X", dev, bf16), M, K,
+                                     _dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
+                                     _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev, f32), _stream(stream))
     _check("svdq_fp8_quantize_act", st)
 
 
@@ -508,7 +532,9 @@ def _fp8_weight(qw, sw, K, dev):
     N, Kw = _shape2(qw, "qw")
     if Kw != K:
         raise ValueError(f"qw has {Kw} columns, X has K = {K}")
-    return N, _dev_ptr(qw, 1, N * K, "qw", dev), _dev_ptr(sw, 4, fp8_blocks(N) * fp8_blocks(K) * 4, "sw", dev)
+    e4m3, _, f32, _ = _fp8_formats()
+    swp = _dev_ptr(sw, 4, fp8_blocks(N) * fp8_blocks(K) * 4, "sw", dev, f32)
+    return N, _dev_ptr(qw, 1, N * K, "qw", dev, e4m3), swp
 
 
 def _nbytes(t):
@@ -519,8 +545,10 @@ def _fp8_out(Y, M, N, dev):
     """Pointer and type code of the output Y [M, N], whose element size says which type it is."""
     if Y is None:
         raise TypeError("Y: a tensor is needed, its element size gives the output's type")
-    wide = Y.element_size()
-    return _dev_ptr(Y, 4 if wide == 4 else 2, M * N * wide, "Y", dev), SVDQ_F32 if wide == 4 else SVDQ_BF16
+    _, bf16, f32, _ = _fp8_formats()
+    if Y.element_size() == 4:
+        return _dev_ptr(Y, 4, M * N * 4, "Y", dev, f32), SVDQ_F32
+    return _dev_ptr(Y, 2, M * N * 2, "Y", dev, bf16), SVDQ_BF16
 
 
 def svdq_fp8_gemm(qx, sx, qw, sw, bias, Y, stream=None):
@@ -530,8 +558,10 @@ def svdq_fp8_gemm(qx, sx, qw, sw, bias, Y, stream=None):
     dev = _current_device()
     N, qwp, swp = _fp8_weight(qw, sw, K, dev)
     Yp, out = _fp8_out(Y, M, N, dev)
-    st = lib().svdq_fp8_gemm(_dev_ptr(qx, 1, M * K, "qx", dev), _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev),
-                             qwp, swp, _dev_ptr(bias, 2, N * 2, "bias", dev), M, N, K, Yp, out, _stream(stream))
+    e4m3, bf16, f32, _ = _fp8_formats()
+    st = lib().svdq_fp8_gemm(_dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
+                             _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev, f32), qwp, swp,
+                             _dev_ptr(bias, 2, N * 2, "bias", dev, bf16), M, N, K, Yp, out, _stream(stream))
     _check("svdq_fp8_gemm", st)
 
 
@@ -547,9 +577,11 @@ def svdq_fp8_linear(X, qw, sw, bias, workspace, Y, stream=None):
     N, qwp, swp = _fp8_weight(qw, sw, K, dev)
     Yp, out = _fp8_out(Y, M, N, dev)
     ws_need = svdq_fp8_workspace_bytes(M, K)
-    st = lib().svdq_fp8_linear(_dev_ptr(X, 2, M * K * 2, "X", dev), qwp, swp, _dev_ptr(bias, 2, N * 2, "bias", dev),
-                               M, N, K, _dev_ptr(workspace, None, ws_need, "workspace", dev), _nbytes(workspace), Yp,
-                               out, _stream(stream))
+    _, bf16, _, _ = _fp8_formats()
+    st = lib().svdq_fp8_linear(_dev_ptr(X, 2, M * K * 2, "X", dev, bf16), qwp, swp,
+                               _dev_ptr(bias, 2, N * 2, "bias", dev, bf16), M, N, K,
+                               _dev_ptr(workspace, None, ws_need, "workspace", dev), _nbytes(workspace), Yp, out,
+                               _stream(stream))
     _check("svdq_fp8_linear", st)
 
 
@@ -583,13 +615,14 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
     dev = _current_device()
     gi, gh = fp8_blocks(I), fp8_blocks(H)
     need = svdq_fp8_moe_workspace_bytes(T, I, E, top_k)
+    e4m3, bf16, f32, i32 = _fp8_formats()
     st = lib().svdq_fp8_moe_layer(
-        _dev_ptr(X, 2, T * H * 2, "X", dev), _dev_ptr(wr, 2, E * H * 2, "wr", dev),
-        _dev_ptr(w13, 1, E * 2 * I * H, "w13", dev), _dev_ptr(s13, 4, E * 2 * gi * gh * 4, "s13", dev),
-        _dev_ptr(w2, 1, E * H * I, "w2", dev), _dev_ptr(s2, 4, E * gh * gi * 4, "s2", dev), T, H, I, E, top_k,
-        1 if renormalize else 0, _dev_ptr(idx, 4, T * top_k * 4, "idx", dev),
-        _dev_ptr(gate, 4, T * top_k * 4, "gate", dev), _dev_ptr(workspace, None, need, "workspace", dev),
-        _nbytes(workspace), _dev_ptr(Y, 2, T * H * 2, "Y", dev), _stream(stream))
+        _dev_ptr(X, 2, T * H * 2, "X", dev, bf16), _dev_ptr(wr, 2, E * H * 2, "wr", dev, bf16),
+        _dev_ptr(w13, 1, E * 2 * I * H, "w13", dev, e4m3), _dev_ptr(s13, 4, E * 2 * gi * gh * 4, "s13", dev, f32),
+        _dev_ptr(w2, 1, E * H * I, "w2", dev, e4m3), _dev_ptr(s2, 4, E * gh * gi * 4, "s2", dev, f32), T, H, I, E,
+        top_k, 1 if renormalize else 0, _dev_ptr(idx, 4, T * top_k * 4, "idx", dev, i32),
+        _dev_ptr(gate, 4, T * top_k * 4, "gate", dev, f32), _dev_ptr(workspace, None, need, "workspace", dev),
+        _nbytes(workspace), _dev_ptr(Y, 2, T * H * 2, "Y", dev, bf16), _stream(stream))
     _check("svdq_fp8_moe_layer", st)
 
 

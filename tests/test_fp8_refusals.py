@@ -144,3 +144,35 @@ def test_an_output_is_needed_for_its_type(name, guarded, monkeypatch):  # noqa: 
     call, t = _case(name)
     with pytest.raises(TypeError, match="Y"):
         call({**t, "Y": None})
+
+
+# of every tensor: the types a call takes (integers of the width hold the bits), and some of the same width that are
+# another format or another kind of number
+E4M3 = (["float8_e4m3fn", "uint8", "int8"],
+        ["float8_e4m3fnuz", "float8_e5m2", "float8_e5m2fnuz", "float8_e8m0fnu", "bool"])
+BF16 = (["bfloat16", "int16", "uint16"], ["float16"])
+F32 = (["float32"], ["int32"])
+I32 = (["int32", "uint32"], ["float32"])
+FORMATS = {
+    "quantize": {"X": BF16, "qx": E4M3, "sx": F32},
+    "gemm": {"qx": E4M3, "sx": F32, "qw": E4M3, "sw": F32, "bias": BF16, "Y": BF16},
+    "linear": {"X": BF16, "qw": E4M3, "sw": F32, "bias": BF16, "Y": F32},
+    "moe": {"X": BF16, "wr": BF16, "w13": E4M3, "s13": F32, "w2": E4M3, "s2": F32, "Y": BF16, "idx": I32, "gate": F32},
+}
+
+
+@pytest.mark.parametrize("name", list(FORMATS))
+def test_tensors_of_another_format_are_refused(name, guarded, monkeypatch):  # noqa: F811
+    import torch
+
+    sized = SizeQueries(guarded)
+    monkeypatch.setattr(b, "lib", lambda: sized)
+    call, tensors = _case(name)
+    assert set(FORMATS[name]) == set(tensors) - {"ws"}
+    for arg, (taken, refused) in FORMATS[name].items():
+        for dtype in taken + refused:
+            t = Dev(tensors[arg].shape, tensors[arg].element_size())
+            t.dtype = getattr(torch, dtype)
+            assert t.dtype.itemsize == t.element_size()
+            with pytest.raises(Reached if dtype in taken else TypeError, match=None if dtype in taken else arg):
+                call({**tensors, arg: t})
