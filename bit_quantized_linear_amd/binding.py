@@ -9,6 +9,7 @@ linear; if the library is missing every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 
 import numpy as np
@@ -517,14 +518,22 @@ def _fp8_formats():
     return _fp8_types
 
 
+def _fp8_scales(t, shape, name, dev):
+    """Pointer of fp32 scales: a tensor with as many dimensions as `shape` has its
+    rows, too (the same bytes in another order would pass by their number)."""
+    if t is not None and t.shape != shape and t.dim() == len(shape) and tuple(t.shape[1:]) != shape[1:]:
+        raise ValueError(f"{name} is {list(t.shape)}, the call takes {list(shape)}")
+    return _dev_ptr(t, 4, 4 * math.prod(shape), name, dev, _fp8_formats()[2])
+
+
 def svdq_fp8_quantize_act(X, qx, sx, stream=None):
     """E4M3 codes qx [M, K] (1-byte elements) and scales sx [ceil(K/128), M] of X [M, K] bf16."""
     M, K = _shape2(X, "X")
     dev = _current_device()
-    e4m3, bf16, f32, _ = _fp8_formats()
+    e4m3, bf16, _, _ = _fp8_formats()
     st = lib().svdq_fp8_quantize_act(_dev_ptr(X, 2, M * K * 2, "X", dev, bf16), M, K,
                                      _dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
-                                     _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev, f32), _stream(stream))
+                                     _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev), _stream(stream))
     _check("svdq_fp8_quantize_act", st)
 
 
@@ -532,9 +541,8 @@ def _fp8_weight(qw, sw, K, dev):
     N, Kw = _shape2(qw, "qw")
     if Kw != K:
         raise ValueError(f"qw has {Kw} columns, X has K = {K}")
-    e4m3, _, f32, _ = _fp8_formats()
-    swp = _dev_ptr(sw, 4, fp8_blocks(N) * fp8_blocks(K) * 4, "sw", dev, f32)
-    return N, _dev_ptr(qw, 1, N * K, "qw", dev, e4m3), swp
+    qwp = _dev_ptr(qw, 1, N * K, "qw", dev, _fp8_formats()[0])
+    return N, qwp, _fp8_scales(sw, (fp8_blocks(N), fp8_blocks(K)), "sw", dev)
 
 
 def _nbytes(t):
@@ -558,9 +566,9 @@ def svdq_fp8_gemm(qx, sx, qw, sw, bias, Y, stream=None):
     dev = _current_device()
     N, qwp, swp = _fp8_weight(qw, sw, K, dev)
     Yp, out = _fp8_out(Y, M, N, dev)
-    e4m3, bf16, f32, _ = _fp8_formats()
+    e4m3, bf16, _, _ = _fp8_formats()
     st = lib().svdq_fp8_gemm(_dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
-                             _dev_ptr(sx, 4, fp8_blocks(K) * M * 4, "sx", dev, f32), qwp, swp,
+                             _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev), qwp, swp,
                              _dev_ptr(bias, 2, N * 2, "bias", dev, bf16), M, N, K, Yp, out, _stream(stream))
     _check("svdq_fp8_gemm", st)
 
@@ -618,8 +626,8 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
     e4m3, bf16, f32, i32 = _fp8_formats()
     st = lib().svdq_fp8_moe_layer(
         _dev_ptr(X, 2, T * H * 2, "X", dev, bf16), _dev_ptr(wr, 2, E * H * 2, "wr", dev, bf16),
-        _dev_ptr(w13, 1, E * 2 * I * H, "w13", dev, e4m3), _dev_ptr(s13, 4, E * 2 * gi * gh * 4, "s13", dev, f32),
-        _dev_ptr(w2, 1, E * H * I, "w2", dev, e4m3), _dev_ptr(s2, 4, E * gh * gi * 4, "s2", dev, f32), T, H, I, E,
+        _dev_ptr(w13, 1, E * 2 * I * H, "w13", dev, e4m3), _fp8_scales(s13, (E, 2, gi, gh), "s13", dev),
+        _dev_ptr(w2, 1, E * H * I, "w2", dev, e4m3), _fp8_scales(s2, (E, gh, gi), "s2", dev), T, H, I, E,
         top_k, 1 if renormalize else 0, _dev_ptr(idx, 4, T * top_k * 4, "idx", dev, i32),
         _dev_ptr(gate, 4, T * top_k * 4, "gate", dev, f32), _dev_ptr(workspace, None, need, "workspace", dev),
         _nbytes(workspace), _dev_ptr(Y, 2, T * H * 2, "Y", dev, bf16), _stream(stream))

@@ -176,3 +176,19 @@ def test_tensors_of_another_format_are_refused(name, guarded, monkeypatch):  # n
             assert t.dtype.itemsize == t.element_size()
             with pytest.raises(Reached if dtype in taken else TypeError, match=None if dtype in taken else arg):
                 call({**tensors, arg: t})
+
+
+# scales in another order have the same bytes; a flat buffer is taken by its size
+@pytest.mark.parametrize("name,arg,wrong,flat", [
+    ("quantize", "sx", (40, 2), (2 * 40 + 5,)), ("gemm", "sx", (40, 2), (2 * 40,)), ("gemm", "sw", (1, 4), (4,)),
+    ("linear", "sw", (1, 4), (5,)), ("moe", "s13", (5, 2, 2, 1), (20,)), ("moe", "s13", (5, 1, 2, 2), (20,)),
+    ("moe", "s2", (5, 1, 2), (10,)),
+])
+def test_scales_in_another_order_are_refused(name, arg, wrong, flat, guarded, monkeypatch):  # noqa: F811
+    sized = SizeQueries(guarded)
+    monkeypatch.setattr(b, "lib", lambda: sized)
+    call, tensors = _case(name)
+    right = tensors[arg].shape
+    for shape, what in ((wrong, ValueError), (flat, Reached), ((right[0] + 1,) + right[1:], Reached)):
+        with pytest.raises(what, match=arg if what is ValueError else None):
+            call({**tensors, arg: Dev(shape, 4)})
