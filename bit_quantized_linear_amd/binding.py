@@ -157,13 +157,15 @@ def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None, formats=Non
         raise TypeError(f"{name}: device entry points take GPU tensors")
     if not t.is_contiguous():
         raise TypeError(f"{name}: tensors must be contiguous")
-    size = t.element_size()
-    if itemsize is not None and size != itemsize:
-        raise TypeError(f"{name}: expected {itemsize}-byte elements, got {size}")
-    if formats is not None:
-        dtype = getattr(t, "dtype", None)
-        if dtype is not None and dtype not in formats:
+    dtype = None if formats is None else getattr(t, "dtype", None)
+    if dtype is not None:  # one of `formats`, each of `itemsize` bytes
+        if dtype not in formats:
             raise TypeError(f"{name}: {dtype}, the call takes {', '.join(sorted(map(str, formats)))}")
+        size = itemsize
+    else:
+        size = t.element_size()
+        if itemsize is not None and size != itemsize:
+            raise TypeError(f"{name}: expected {itemsize}-byte elements, got {size}")
     dev = _current_device() if device is None else device
     if t.device.index != dev:
         raise TypeError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{dev}")
@@ -518,42 +520,44 @@ def _fp8_formats():
     return _fp8_types
 
 
-def _fp8_scales(t, shape, name, dev):
+def _fp8_scales(t, shape, name, dev, f32):
     """Pointer of fp32 scales: a tensor with as many dimensions as `shape` has its
     rows, too (the same bytes in another order would pass by their number)."""
-    if t is not None and t.shape != shape and t.dim() == len(shape) and tuple(t.shape[1:]) != shape[1:]:
-        raise ValueError(f"{name} is {list(t.shape)}, the call takes {list(shape)}")
-    return _dev_ptr(t, 4, 4 * math.prod(shape), name, dev, _fp8_formats()[2])
+    nbytes = 0
+    if t is not None and t.shape != shape:
+        if t.dim() == len(shape) and tuple(t.shape[1:]) != shape[1:]:
+            raise ValueError(f"{name} is {list(t.shape)}, the call takes {list(shape)}")
+        nbytes = 4 * math.prod(shape)
+    return _dev_ptr(t, 4, nbytes, name, dev, f32)
 
 
 def svdq_fp8_quantize_act(X, qx, sx, stream=None):
     """E4M3 codes qx [M, K] (1-byte elements) and scales sx [ceil(K/128), M] of X [M, K] bf16."""
     M, K = _shape2(X, "X")
     dev = _current_device()
-    e4m3, bf16, _, _ = _fp8_formats()
+    e4m3, bf16, f32, _ = _fp8_formats()
     st = lib().svdq_fp8_quantize_act(_dev_ptr(X, 2, M * K * 2, "X", dev, bf16), M, K,
                                      _dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
-                                     _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev), _stream(stream))
+                                     _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev, f32), _stream(stream))
     _check("svdq_fp8_quantize_act", st)
 
 
-def _fp8_weight(qw, sw, K, dev):
+def _fp8_weight(qw, sw, K, dev, e4m3, f32):
     N, Kw = _shape2(qw, "qw")
     if Kw != K:
         raise ValueError(f"qw has {Kw} columns, X has K = {K}")
-    qwp = _dev_ptr(qw, 1, N * K, "qw", dev, _fp8_formats()[0])
-    return N, qwp, _fp8_scales(sw, (fp8_blocks(N), fp8_blocks(K)), "sw", dev)
+    qwp = _dev_ptr(qw, 1, N * K, "qw", dev, e4m3)
+    return N, qwp, _fp8_scales(sw, (fp8_blocks(N), fp8_blocks(K)), "sw", dev, f32)
 
 
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _fp8_out(Y, M, N, dev):
+def _fp8_out(Y, M, N, dev, bf16, f32):
     """Pointer and type code of the output Y [M, N], whose element size says which type it is."""
     if Y is None:
         raise TypeError("Y: a tensor is needed, its element size gives the output's type")
-    _, bf16, f32, _ = _fp8_formats()
     if Y.element_size() == 4:
         return _dev_ptr(Y, 4, M * N * 4, "Y", dev, f32), SVDQ_F32
     return _dev_ptr(Y, 2, M * N * 2, "Y", dev, bf16), SVDQ_BF16
@@ -564,11 +568,11 @@ def svdq_fp8_gemm(qx, sx, qw, sw, bias, Y, stream=None):
     qx [M, K], sx and the block-scaled weight qw [N, K], sw."""
     M, K = _shape2(qx, "qx")
     dev = _current_device()
-    N, qwp, swp = _fp8_weight(qw, sw, K, dev)
-    Yp, out = _fp8_out(Y, M, N, dev)
-    e4m3, bf16, _, _ = _fp8_formats()
+    e4m3, bf16, f32, _ = _fp8_formats()
+    N, qwp, swp = _fp8_weight(qw, sw, K, dev, e4m3, f32)
+    Yp, out = _fp8_out(Y, M, N, dev, bf16, f32)
     st = lib().svdq_fp8_gemm(_dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
-                             _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev), qwp, swp,
+                             _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev, f32), qwp, swp,
                              _dev_ptr(bias, 2, N * 2, "bias", dev, bf16), M, N, K, Yp, out, _stream(stream))
     _check("svdq_fp8_gemm", st)
 
@@ -582,10 +586,10 @@ def svdq_fp8_linear(X, qw, sw, bias, workspace, Y, stream=None):
     on the way, times the block-scaled weight qw [N, K], sw, plus bias."""
     M, K = _shape2(X, "X")
     dev = _current_device()
-    N, qwp, swp = _fp8_weight(qw, sw, K, dev)
-    Yp, out = _fp8_out(Y, M, N, dev)
+    e4m3, bf16, f32, _ = _fp8_formats()
+    N, qwp, swp = _fp8_weight(qw, sw, K, dev, e4m3, f32)
+    Yp, out = _fp8_out(Y, M, N, dev, bf16, f32)
     ws_need = svdq_fp8_workspace_bytes(M, K)
-    _, bf16, _, _ = _fp8_formats()
     st = lib().svdq_fp8_linear(_dev_ptr(X, 2, M * K * 2, "X", dev, bf16), qwp, swp,
                                _dev_ptr(bias, 2, N * 2, "bias", dev, bf16), M, N, K,
                                _dev_ptr(workspace, None, ws_need, "workspace", dev), _nbytes(workspace), Yp, out,
@@ -626,8 +630,8 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
     e4m3, bf16, f32, i32 = _fp8_formats()
     st = lib().svdq_fp8_moe_layer(
         _dev_ptr(X, 2, T * H * 2, "X", dev, bf16), _dev_ptr(wr, 2, E * H * 2, "wr", dev, bf16),
-        _dev_ptr(w13, 1, E * 2 * I * H, "w13", dev, e4m3), _fp8_scales(s13, (E, 2, gi, gh), "s13", dev),
-        _dev_ptr(w2, 1, E * H * I, "w2", dev, e4m3), _fp8_scales(s2, (E, gh, gi), "s2", dev), T, H, I, E,
+        _dev_ptr(w13, 1, E * 2 * I * H, "w13", dev, e4m3), _fp8_scales(s13, (E, 2, gi, gh), "s13", dev, f32),
+        _dev_ptr(w2, 1, E * H * I, "w2", dev, e4m3), _fp8_scales(s2, (E, gh, gi), "s2", dev, f32), T, H, I, E,
         top_k, 1 if renormalize else 0, _dev_ptr(idx, 4, T * top_k * 4, "idx", dev, i32),
         _dev_ptr(gate, 4, T * top_k * 4, "gate", dev, f32), _dev_ptr(workspace, None, need, "workspace", dev),
         _nbytes(workspace), _dev_ptr(Y, 2, T * H * 2, "Y", dev, bf16), _stream(stream))
