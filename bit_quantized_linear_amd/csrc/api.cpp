@@ -511,7 +511,7 @@ svdq_status svdq_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw,
 }
 
 size_t svdq_fp8_workspace_bytes(int M, int K) {
-    if (M < 0 || K <= 0 || K % 16) return 0;
+    if (M < 0 || K <= 0 || K % 16 || K >= kFp8MaxK || M > kFp8MaxTokens) return 0;
     return svdq::fp8_workspace_scales(M, K) + (size_t)svdq::fp8_blocks(K) * (size_t)M * sizeof(float);
 }
 

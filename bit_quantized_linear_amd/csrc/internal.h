@@ -100,7 +100,7 @@ hipError_t launch_w4a16_linear(const uint16_t *X, const uint8_t *packed, const u
                                int N, int K, uint16_t *Y, hipStream_t stream);
 
 // block-scaled FP8 (fp8.hip, fp8_moe.hip)
-inline int fp8_blocks(int n) { return (n + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK; }
+inline int fp8_blocks(int n) { return n / SVDQ_FP8_BLOCK + (n % SVDQ_FP8_BLOCK != 0); }
 // byte offset of the scales behind the codes of X in svdq_fp8_linear's workspace
 inline size_t fp8_workspace_scales(int M, int K) { return ((size_t)M * (size_t)K + 255) / 256 * 256; }
 hipError_t launch_fp8_quantize_act(const uint16_t *X, int M, int K, uint8_t *qx, float *sx, hipStream_t stream);

@@ -499,9 +499,9 @@ svdq_status fp8_prepare_impl(const uint16_t *W, int K, int N, uint8_t *qw, float
     const int G = fp8_blocks(K), B = fp8_blocks(N);
     parallel_for(0, B, [&](int64_t b0, int64_t b1) {
         for (int64_t b = b0; b < b1; ++b) {
-            const int n0 = (int)b * SVDQ_FP8_BLOCK, n1 = std::min(N, n0 + SVDQ_FP8_BLOCK);
+            const int n0 = (int)b * SVDQ_FP8_BLOCK, n1 = n0 + std::min(N - n0, SVDQ_FP8_BLOCK);
             for (int g = 0; g < G; ++g) {
-                const int k0 = g * SVDQ_FP8_BLOCK, k1 = std::min(K, k0 + SVDQ_FP8_BLOCK);
+                const int k0 = g * SVDQ_FP8_BLOCK, k1 = k0 + std::min(K - k0, SVDQ_FP8_BLOCK);
                 float amax = std::ldexp(1.0f, -100);
                 for (int k = k0; k < k1; ++k)
                     for (int n = n0; n < n1; ++n)

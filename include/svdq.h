@@ -512,7 +512,7 @@ svdq_status svdq_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw,
                           const uint16_t *bias, int M, int N, int K, void *Y, int y_dtype, void *stream);
 
 /* Bytes of device workspace svdq_fp8_linear needs for an [M, K] input (0 on a
- * bad argument): the codes and scales of X. */
+ * bad argument or a shape that it refuses): the codes and scales of X. */
 size_t svdq_fp8_workspace_bytes(int M, int K);
 
 /* The block-scaled FP8 linear from bf16 activations: svdq_fp8_quantize_act and

@@ -192,3 +192,14 @@ def test_scales_in_another_order_are_refused(name, arg, wrong, flat, guarded, mo
     for shape, what in ((wrong, ValueError), (flat, Reached), ((right[0] + 1,) + right[1:], Reached)):
         with pytest.raises(what, match=arg if what is ValueError else None):
             call({**tensors, arg: Dev(shape, 4)})
+
+
+def test_workspace_of_shapes_that_no_call_takes():
+    # K from 2^22, M past 2^28 - 16, and numbers whose blocks of 128 pass 31 bits
+    for M, K in ((1, 1 << 22), (1, 2147483632), (64, 2147483632), ((1 << 28) - 15, 16), (2147483647, 16),
+                 (2147483647, 2147483632)):
+        assert b.svdq_fp8_workspace_bytes(M, K) == 0
+        if M <= (1 << 28) - 16:
+            assert linear(M=M, K=K) == SHAPE
+    M, K = (1 << 28) - 16, (1 << 22) - 16
+    assert b.svdq_fp8_workspace_bytes(M, K) >= M * K + 4 * M * (1 << 15)
