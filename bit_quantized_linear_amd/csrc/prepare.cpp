@@ -25,6 +25,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <thread>
 #include <vector>
 
@@ -53,13 +54,19 @@ void parallel_for(int64_t begin, int64_t end, F &&fn) {
         fn(begin, end);
         return;
     }
+    const auto part = [&fn, begin, total, nt](int t) {
+        fn(begin + total * t / nt, begin + total * (t + 1) / nt);
+    };
     std::vector<std::thread> pool;
-    pool.reserve(nt);
-    for (int t = 0; t < nt; ++t) {
-        int64_t a = begin + total * t / nt;
-        int64_t b = begin + total * (t + 1) / nt;
-        pool.emplace_back([&fn, a, b] { fn(a, b); });
+    int t = 0;
+    try {
+        pool.reserve(nt);
+        for (; t < nt; ++t) pool.emplace_back(part, t);
+    } catch (const std::exception &) {
+        // no room for another thread: the parts from t on are this one's, as a C
+        // entry has no one to throw to
     }
+    for (; t < nt; ++t) part(t);
     for (auto &th : pool) th.join();
 }
 
