@@ -34,13 +34,20 @@ TINY = 2.0 ** -100
 F64 = np.float64
 
 
+def _value(b):
+    ex, man = (b >> 3) & 15, b & 7
+    if ex == 15 and man == 7:
+        return np.nan
+    mag = man * 2.0 ** -9 if ex == 0 else (1 + man / 8.0) * 2.0 ** (ex - 7)
+    return -mag if b & 0x80 else mag
+
+
+_BYTES = np.array([_value(b) for b in range(256)])
+
+
 def e4m3_decode(b):
     """Values of E4M3 bytes (NaN for 0x7F and 0xFF)."""
-    b = np.asarray(b, dtype=np.uint8).astype(np.int64)
-    ex, man = (b >> 3) & 15, b & 7
-    mag = np.where(ex == 0, man * 2.0 ** -9, (1 + man / 8.0) * np.exp2((ex - 7).astype(F64)))
-    mag = np.where((ex == 15) & (man == 7), np.nan, mag)
-    return np.where(b & 0x80, -mag, mag)
+    return _BYTES[np.asarray(b, dtype=np.uint8)]
 
 
 _VALUES = e4m3_decode(np.arange(127))  # ascending magnitudes of codes 0 .. 126
