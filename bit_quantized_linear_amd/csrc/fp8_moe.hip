@@ -506,7 +506,9 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(
             }
             if (m < kTokens && p.m0 + m < p.count) {
                 const float h = g / (1.0f + expf(-g)) * u;
-                const uint32_t hi = f32_to_bf16_bits(h);
+                uint32_t hi = f32_to_bf16_bits(h);
+                // a finite h past the largest bf16 number takes that one, and lo the rest
+                if ((hi & 0x7FFFu) == 0x7F80u && __builtin_isfinite(h)) --hi;
                 const size_t at = (size_t)pair_of(table.pair[p.from + p.m0 + m]) * I + p.i0 + c;
                 h_hi[at] = (uint16_t)hi;
                 // no remainder of an infinity or NaN

@@ -94,3 +94,19 @@ def test_experts_of_chosen_numbers_of_tokens(E, I):  # noqa: E741
     Y, idx, gate = g.run_moe(bits, wl.bf16_bits_from_f32(wr), w, 1)
     assert np.array_equal(idx[:, 0], owner)
     g.check_moe(g.y_of(Y, T, "bf16"), idx, gate, o8.moe(wl.f32_from_bf16_bits(bits), wr, *w, 1, True))
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_a_finite_intermediate_value_next_to_the_largest_number_stays_finite(sign):
+    # h = 2^64 (2 - 2^-10) 2^63 is finite in fp32 and past every bf16 number
+    H_, I = 32, 16  # noqa: E741
+    x = np.zeros((1, H_), np.float32)
+    x[0, 0] = 2.0 ** 60
+    w13, w2 = np.zeros((1, 2, I, H_), np.uint8), np.zeros((1, H_, I), np.uint8)
+    w13[0, :, 3, 0], w2[0, :, 3] = 0x38, 0x38  # 1.0
+    s13 = np.array([2.0 ** 4, sign * (2 - 2.0 ** -10) * 2.0 ** 3], np.float32).reshape(1, 2, 1, 1)
+    s2 = np.full((1, 1, 1), 2.0 ** -100, np.float32)
+    wr = np.zeros((1, H_), np.float32)
+    Y, idx, gate = g.run_moe(wl.bf16_bits_from_f32(x), wl.bf16_bits_from_f32(wr), (w13, s13, w2, s2), 1)
+    y = g.y_of(Y, 1, "bf16")
+    assert np.all(y == sign * 2.0 ** 28), y[0, :4]  # (2 - 2^-10) 2^27, rounded to bf16
