@@ -153,22 +153,24 @@ def _dev_ptr(t, itemsize=None, nbytes=0, name="tensor", device=None, formats=Non
     type, device) or ValueError (too small)."""
     if t is None:
         return None
-    if not t.is_cuda:
+    dtype = None if formats is None else getattr(t, "dtype", None)
+    # a tensor with a type to look at tells its device by number at half the cost
+    index = (t.device.index if t.is_cuda else -1) if dtype is None else t.get_device()
+    if index < 0:
         raise TypeError(f"{name}: device entry points take GPU tensors")
     if not t.is_contiguous():
         raise TypeError(f"{name}: tensors must be contiguous")
-    dtype = None if formats is None else getattr(t, "dtype", None)
-    if dtype is not None:  # one of `formats`, each of `itemsize` bytes
-        if dtype not in formats:
-            raise TypeError(f"{name}: {dtype}, the call takes {', '.join(sorted(map(str, formats)))}")
-        size = itemsize
-    else:
+    if dtype is None:
         size = t.element_size()
         if itemsize is not None and size != itemsize:
             raise TypeError(f"{name}: expected {itemsize}-byte elements, got {size}")
+    elif dtype in formats:  # each of `itemsize` bytes
+        size = itemsize
+    else:
+        raise TypeError(f"{name}: {dtype}, the call takes {', '.join(sorted(map(str, formats)))}")
     dev = _current_device() if device is None else device
-    if t.device.index != dev:
-        raise TypeError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{dev}")
+    if index != dev:
+        raise TypeError(f"{name} is on cuda:{index}, the current device is cuda:{dev}")
     have = t.numel() * size
     if have < nbytes:
         raise ValueError(f"{name}: {have} bytes, the call needs at least {nbytes}")
@@ -550,10 +552,6 @@ def _fp8_weight(qw, sw, K, dev, e4m3, f32):
     return N, qwp, _fp8_scales(sw, (fp8_blocks(N), fp8_blocks(K)), "sw", dev, f32)
 
 
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
-
-
 def _fp8_out(Y, M, N, dev, bf16, f32):
     """Pointer and type code of the output Y [M, N], whose element size says which type it is."""
     if Y is None:
@@ -592,8 +590,8 @@ def svdq_fp8_linear(X, qw, sw, bias, workspace, Y, stream=None):
     ws_need = svdq_fp8_workspace_bytes(M, K)
     st = lib().svdq_fp8_linear(_dev_ptr(X, 2, M * K * 2, "X", dev, bf16), qwp, swp,
                                _dev_ptr(bias, 2, N * 2, "bias", dev, bf16), M, N, K,
-                               _dev_ptr(workspace, None, ws_need, "workspace", dev), _nbytes(workspace), Yp, out,
-                               _stream(stream))
+                               _dev_ptr(workspace, None, ws_need, "workspace", dev),
+                               0 if workspace is None else ws_need, Yp, out, _stream(stream))
     _check("svdq_fp8_linear", st)
 
 
@@ -634,7 +632,7 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
         _dev_ptr(w2, 1, E * H * I, "w2", dev, e4m3), _fp8_scales(s2, (E, gh, gi), "s2", dev, f32), T, H, I, E,
         top_k, 1 if renormalize else 0, _dev_ptr(idx, 4, T * top_k * 4, "idx", dev, i32),
         _dev_ptr(gate, 4, T * top_k * 4, "gate", dev, f32), _dev_ptr(workspace, None, need, "workspace", dev),
-        _nbytes(workspace), _dev_ptr(Y, 2, T * H * 2, "Y", dev, bf16), _stream(stream))
+        0 if workspace is None else need, _dev_ptr(Y, 2, T * H * 2, "Y", dev, bf16), _stream(stream))
     _check("svdq_fp8_moe_layer", st)
 
 

@@ -172,7 +172,7 @@ def test_tensors_of_another_format_are_refused(name, guarded, monkeypatch):  # n
     for arg, (taken, refused) in FORMATS[name].items():
         for dtype in taken + refused:
             t = Dev(tensors[arg].shape, tensors[arg].element_size())
-            t.dtype = getattr(torch, dtype)
+            t.dtype, t.get_device = getattr(torch, dtype), lambda: 0
             assert t.dtype.itemsize == t.element_size()
             with pytest.raises(Reached if dtype in taken else TypeError, match=None if dtype in taken else arg):
                 call({**tensors, arg: t})
@@ -203,3 +203,17 @@ def test_workspace_of_shapes_that_no_call_takes():
             assert linear(M=M, K=K) == SHAPE
     M, K = (1 << 28) - 16, (1 << 22) - 16
     assert b.svdq_fp8_workspace_bytes(M, K) >= M * K + 4 * M * (1 << 15)
+
+
+def test_typed_tensors_elsewhere_are_refused(guarded, monkeypatch):  # noqa: F811
+    import torch
+
+    sized = SizeQueries(guarded)
+    monkeypatch.setattr(b, "lib", lambda: sized)
+    call, tensors = _case("gemm")
+    with pytest.raises(TypeError, match="sx: device entry points take GPU tensors"):
+        call({**tensors, "sx": torch.zeros((2, 40))})
+    other = Dev((2, 40), 4)
+    other.dtype, other.get_device = torch.float32, lambda: 1
+    with pytest.raises(TypeError, match="sx is on cuda:1, the current device is cuda:0"):
+        call({**tensors, "sx": other})
