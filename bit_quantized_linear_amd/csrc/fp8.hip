@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kF8QThreads) void fp8_quantize_kernel(const uint16_
 
 constexpr uint32_t kF8Oob = 0x80000000u;
 constexpr int kF8Cus = 256;  // compute units
-// one MFMA tile: with two, 20 x 5120 x 5120 took 14.6 us, in tiles of 64 it takes 10.8
+// one MFMA tile: with two, 20 x 5120 x 5120 took 14.6 us, in tiles of 32 x 32 it takes 8.5
 constexpr int kF8SkinnyTokens = 16;
 
 typedef __attribute__((address_space(3))) void f8_lds_void;
@@ -128,7 +128,7 @@ struct F8Wide {
 // One 16x16x128 MFMA is a whole group of a tile, so its result is scaled and
 // added (4 FMAs a lane) while the next row tile's MFMAs run: the 16 x 16 x 128
 // MFMA and not the 32 x 32 x 64 one, whose results take two per group and four
-// times the registers (2150 against 2550 TFLOP/s at 32768 x 5120 x 5120).
+// times the registers (1.19 times the time at 32768 x 5120 x 5120).
 // NS stages take turns, loads NS - 1 ahead. KW parts of the block share K and add
 // their sums at the end, for grids too small to fill the chip.
 // kWide: sums to fp32 precision on bf16 MFMAs, for fp32 outputs; otherwise bf16.
@@ -429,11 +429,11 @@ __global__ __launch_bounds__(64 * WN * WM * KW, 1) void fp8_gemm_kernel(
 
 // 256 x 256 tiles, of which the grid's first `whole` blocks take one each; two
 // blocks share each of the others (128 of its tokens each). 8 waves, one block
-// per compute unit: 130 KB of LDS hold two stages, and a stage's operands feed
+// per compute unit: 133 KB of LDS hold two stages, and a stage's operands feed
 // 4 times the MFMAs that they take LDS reads for. Bound by the matrix cores: they
 // are busy 63 % of the time, at the clock that their power leaves (32760 x 5120 x
-// 5120: 690 to 740 us, 2.3 to 2.5 PFLOP/s; the library's product of the same
-// codes with one scale for all, 650 us). The rest is the epilogue, which nothing
+// 5120: 690 to 720 us, 2.4 to 2.5 PFLOP/s; 4608 x 5120 x 12288: 250, 2.3; the
+// library's product of the same codes with one scale for all, 650 and 214). The rest is the epilogue, which nothing
 // overlaps (one tile's output is 128 KB), and the fill of each tile's first stage.
 __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
@@ -466,8 +466,8 @@ __global__ __launch_bounds__(512, 1) void fp8_gemm256_kernel(
 // global memory into the operands of the 16x16x128 MFMA (weights as A: row =
 // output column; tokens as B, for all NT tiles of columns), and add the parts in
 // LDS in order. The weight is read once: bound by HBM, and at these sizes by the
-// way to the first of it (a launch, a load's latency, the sums): 13 x 2048 x 12288
-// (M x K x N) takes 8.0 us (25 MB, 3.1 TB/s), 1 x 5120 x 5120 in one launch 8.6 (26
+// way to the first of it (a launch, a load's latency, the sums): 8 x 2048 x 12288
+// (M x K x N) takes 7.7 us (25 MB, 3.3 TB/s), 1 x 5120 x 5120 in one launch 8.6 (26
 // MB, 3.0 TB/s). Waves hide a load's latency better than loads ahead, whose
 // registers keep waves out: 1, 2, 3 and 4 groups in flight per wave take 8.5, 9.6,
 // 9.3 and 10.5 us for 1 x 5120 x 5120, 13.4, 14.6, 14.5 and 16.2 for 8 x 5120 x 12288.
@@ -513,8 +513,11 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(
     const int mrow = min(r16, M - 1);
 
     // Where rows are a multiple of 4 KB apart, the same group of all rows lies on a
-    // few memory channels, so each block starts at another group (16 x 8192 x 8192:
-    // 13.6 us, 19.7 without; elsewhere it costs: 1 x 2048 x 151936 57, 49 without).
+    // few memory channels, so each block starts at another group. Weights that the
+    // last-level cache holds gain by it, those from HBM little (us, with / without: 8 x
+    // 8192 x 8192 14.1 / 17.8, from HBM 18.0 / 18.0; 8 x 4096 x 16384 13.3 / 13.7 and
+    // 15.1 / 16.6; fp32 16 x 8192 x 8192 15.7 / 18.4 and 19.4 / 18.5); rows at other
+    // distances lose (1 x 2048 x 151936 57 / 49).
     const int first = K % 4096 ? 0 : (int)blockIdx.x & ((1 << (31 - __builtin_clz(G))) - 1);
     auto turned = [&](int i) __attribute__((always_inline)) { return i + first < G ? i + first : i + first - G; };
     i32x8 a[NT];

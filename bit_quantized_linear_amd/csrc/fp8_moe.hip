@@ -8,11 +8,12 @@
 //   Y[t]    = sum_j w[t, j] (h[t, j] Wd), rounded once to bf16
 //
 // Launches: the router's logits; the choices (where the up kernel's blocks do
-// not make them themselves); the gate and up projections, one block per reached
-// expert and 16 intermediate columns; the down projection with the weighted
-// sum, one block per 16 or 8 output columns. Each reached expert's weights are read
-// once, so the layer is bound by HBM: 64 tokens of 128 experts (H 4096, I 1408, 8
-// choices) take 439 us, 5.0 TB/s over all launches; for few bytes by the chain of
+// not make them themselves); the gate and up projections, at most 256 blocks that
+// take items of a reached expert and 16 intermediate columns in turn; the down
+// projection with the weighted sum, one block per 16 or 8 output columns. A reached
+// expert's weights are read once for 4 to 16 of its tokens, so with few tokens each
+// the layer is bound by HBM: 64 tokens of 128 experts (H 4096, I 1408, 8 choices)
+// take 440 us, 5.0 TB/s over all launches; for few bytes by the chain of
 // dependent loads: a token's logits, its choice, the experts' weights, then h and
 // again weights, in three launches about 1.1 us apart (1 token, H 2048, I 768, 8 of
 // 64 experts: 20.5 us, of which the weights alone would take 7.5).
@@ -550,9 +551,10 @@ constexpr int kDownAhead = 4;  // groups of weights per set; two sets take turns
 // weighted sum over its token's pairs in order, so the result does not depend on
 // which wave came first. 16 waves of 4 groups' weights each are the loads under
 // way; the rows of h come through LDS (above), filling kDownSlots slots at a time,
-// each a wait for memory: 4 slots where the sums leave them room (a layer for 8
-// tokens of 64 experts 98.7 us, with 2 slots 99.4). HBM-bound: 64 tokens, H 4096,
-// I 1408, 128 experts 158 us (0.74 GB, 4.7 TB/s).
+// each a wait for memory (a batch's first leaves the next batch's weights under
+// way, the others wait for those too): 4 slots where the sums leave them room (a
+// layer for 8 tokens of 64 experts 98.7 us, with 2 slots 99.4). HBM-bound: 64
+// tokens, H 4096, I 1408, 128 experts 158 us (0.74 GB, 4.7 TB/s).
 // kCols 8: the MFMA's rows 8 .. 15 are the same columns in the unit's next group,
 // and its columns 8 .. 15 the tokens there, so that two quadrants of the result
 // hold the sums of a group each.
