@@ -33,8 +33,11 @@ FP8_BLOCK = 128
 FP8_MOE_MAX_TOKENS = 64
 FP8_MOE_MAX_EXPERTS = 256
 FP8_MOE_MAX_TOP_K = 16
+ROPE_MAX_AXES = 4
+ROPE_MAX_PAIRS = 256
+KV8_PAGE = 64
 
-_vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_vp, _i, _f, _sz, _ll = C.c_void_p, C.c_int, C.c_float, C.c_size_t, C.c_int64
 
 # name -> (restype, argtypes), mirroring include/svdq.h
 SIGNATURES = {
@@ -71,6 +74,12 @@ SIGNATURES = {
     "svdq_fp8_linear": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp, _i, _vp]),
     "svdq_fp8_moe_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "svdq_fp8_moe_layer": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "svdq_fp8_norm_quantize": (_i, [_vp, _vp, _vp, _f, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "svdq_rope": (_i, [_vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _ll, _vp]),
+    "svdq_kv8_append": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "svdq_kv8_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "svdq_kv8_attention": (_i, [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i, _vp,
+                                _vp, _vp, _sz, _vp]),
     "svdq_debug_group_partials": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
     "w8a8_debug_acc": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp]),
     "svdq_debug_set_arch_override": (_i, [C.c_char_p]),
@@ -634,6 +643,140 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
         _dev_ptr(gate, 4, T * top_k * 4, "gate", dev, f32), _dev_ptr(workspace, None, need, "workspace", dev),
         0 if workspace is None else need, _dev_ptr(Y, 2, T * H * 2, "Y", dev, bf16), _stream(stream))
     _check("svdq_fp8_moe_layer", st)
+
+
+def svdq_fp8_norm_quantize(X, residual, weight, eps, total, Y, qx, sx, stream=None):
+    """Root-mean-square norm of X [M, K] (+ residual), bf16, with weights [K]:
+    total = the sum (bf16; may be residual or X itself), Y = the norm in bf16, qx
+    [M, K] and sx [ceil(K/128), M] = its E4M3 codes and scales, as
+    svdq_fp8_quantize_act writes them. residual, total, Y, and qx with sx may be
+    None, but not both Y and qx."""
+    M, K = _shape2(X, "X")
+    dev = _current_device()
+    e4m3, bf16, f32, _ = _fp8_formats()
+    n = M * K * 2
+    st = lib().svdq_fp8_norm_quantize(
+        _dev_ptr(X, 2, n, "X", dev, bf16), _dev_ptr(residual, 2, n, "residual", dev, bf16),
+        _dev_ptr(weight, 2, K * 2, "weight", dev, bf16), eps, M, K, _dev_ptr(total, 2, n, "total", dev, bf16),
+        _dev_ptr(Y, 2, n, "Y", dev, bf16), _dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
+        _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev, f32), _stream(stream))
+    _check("svdq_fp8_norm_quantize", st)
+
+
+def _dev_heads(t, name, dev, bf16):
+    """Pointer, stride between tokens and shape of heads [T, H, D] in bf16, whose
+    rows may be parts of wider ones (a projection's output)."""
+    if t is None or t.dim() != 3:
+        raise TypeError(f"{name} must be a 3-D tensor")
+    if t.dtype not in bf16:
+        raise TypeError(f"{name}: {t.dtype}, the call takes {', '.join(sorted(map(str, bf16)))}")
+    index = t.get_device()
+    if index < 0:
+        raise TypeError(f"{name}: device entry points take GPU tensors")
+    if index != dev:
+        raise TypeError(f"{name} is on cuda:{index}, the current device is cuda:{dev}")
+    T, H, D = t.shape
+    row, head, one = t.stride()
+    if T <= 1 or H * D == 0:  # there is no next row
+        row = max(H * D, -(-H * D // 8) * 8)
+    if (D > 1 and one != 1) or (H > 1 and head != D) or row < H * D:
+        raise TypeError(f"{name}: the heads of a token must be contiguous, and tokens apart")
+    return t.data_ptr(), row, T, H, D
+
+
+def svdq_rope(X, positions, freqs, sections, Y, interleaved=False, stream=None):
+    """Y = X [T, H, D] (bf16, rows may be parts of wider ones) turned by rotary
+    positions: positions [T, axes] int32, freqs [R / 2] fp64, sections: the pairs of
+    each axis, R / 2 in all. Y may be X."""
+    dev = _current_device()
+    _, bf16, _, i32 = _fp8_formats()
+    xp, xs, T, H, D = _dev_heads(X, "X", dev, bf16)
+    yp, ys, *shape = _dev_heads(Y, "Y", dev, bf16)
+    if shape != [T, H, D]:
+        raise ValueError(f"Y is {shape}, the call writes {[T, H, D]}")
+    axes = len(sections)
+    if positions is None or positions.dim() != 2 or tuple(positions.shape) != (T, axes):
+        raise ValueError(f"positions must be [{T}, {axes}]")
+    st = lib().svdq_rope(xp, xs, _dev_ptr(positions, 4, T * axes * 4, "positions", dev, i32),
+                         _dev_ptr(freqs, 8, 8 * sum(sections), "freqs", dev, _f64_format()), (_i * axes)(*sections),
+                         axes, 1 if interleaved else 0, T, H, D, yp, ys, _stream(stream))
+    _check("svdq_rope", st)
+
+
+_f64_types = None
+
+
+def _f64_format():
+    global _f64_types
+    if _f64_types is None:
+        import torch as t
+
+        _f64_types = frozenset((t.float64,))
+    return _f64_types
+
+
+def _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32):
+    """Checked pointers of the 8-bit cache, and its number of pages."""
+    if kc is None or kc.dim() != 4 or vc is None or vc.dim() != 4 or ks is None or vs is None:
+        raise TypeError("kc and vc must be 4-D tensors, ks and vs the scales")
+    P = int(kc.shape[0])
+    if tuple(kc.shape[1:]) != (Hk, KV8_PAGE, D) or tuple(vc.shape) != (P, Hk, D, KV8_PAGE):
+        raise ValueError(f"kc {list(kc.shape)} and vc {list(vc.shape)} do not fit {Hk} heads of {D}: "
+                         f"[pages, {Hk}, {KV8_PAGE}, {D}] and [pages, {Hk}, {D}, {KV8_PAGE}]")
+    n = P * Hk * KV8_PAGE * D
+    return P, (_dev_ptr(kc, 1, n, "kc", dev, e4m3), _fp8_scales(ks, (P, Hk), "ks", dev, f32),
+               _dev_ptr(vc, 1, n, "vc", dev, e4m3), _fp8_scales(vs, (P, Hk), "vs", dev, f32))
+
+
+def _kv8_batch(starts, lengths, table, dev, i32):
+    """Checked pointers of a batch, its sequences and the table's width."""
+    B, max_pages = _shape2(table, "table")
+    return B, max_pages, (_dev_ptr(starts, 4, 4 * (B + 1), "starts", dev, i32),
+                          _dev_ptr(lengths, 4, 4 * B, "lengths", dev, i32),
+                          _dev_ptr(table, 4, 4 * B * max_pages, "table", dev, i32))
+
+
+def svdq_kv8_append(K, V, starts, lengths, table, kc, ks, vc, vs, stream=None):
+    """New keys and values K, V [T, Hk, D] (bf16, rows may be parts of wider ones)
+    into the 8-bit cache kc [pages, Hk, 64, D], ks [pages, Hk], vc [pages, Hk, D, 64],
+    vs [pages, Hk]; starts [B + 1], lengths [B] and table [B, max_pages] int32 say
+    which rows are whose and where they go."""
+    dev = _current_device()
+    e4m3, bf16, f32, i32 = _fp8_formats()
+    kp, kst, T, Hk, D = _dev_heads(K, "K", dev, bf16)
+    vp, vst, *shape = _dev_heads(V, "V", dev, bf16)
+    if shape != [T, Hk, D]:
+        raise ValueError(f"V is {shape}, K {[T, Hk, D]}")
+    B, max_pages, batch = _kv8_batch(starts, lengths, table, dev, i32)
+    P, cache = _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32)
+    st = lib().svdq_kv8_append(kp, kst, vp, vst, *batch, T, B, max_pages, P, Hk, D, *cache, _stream(stream))
+    _check("svdq_kv8_append", st)
+
+
+def svdq_kv8_attention_workspace_bytes(T, B, max_pages, Hq, Hk, D) -> int:
+    return int(lib().svdq_kv8_attention_workspace_bytes(T, B, max_pages, Hq, Hk, D))
+
+
+def svdq_kv8_attention(Q, kc, ks, vc, vs, starts, lengths, table, scale, O, lse=None, workspace=None,  # noqa: E741
+                       causal=True, window=0, stream=None):
+    """O [T, Hq, D] bf16 = attention of the newest tokens' queries Q [T, Hq, D] (bf16,
+    rows may be parts of wider ones) over the 8-bit cache; lse [T, Hq] fp32 takes
+    the logarithms of the weights' sums. The rest as svdq_kv8_append."""
+    dev = _current_device()
+    e4m3, bf16, f32, i32 = _fp8_formats()
+    qp, qst, T, Hq, D = _dev_heads(Q, "Q", dev, bf16)
+    Hk = int(kc.shape[1]) if kc is not None and kc.dim() == 4 else 0
+    P, cache = _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32)
+    B, max_pages, batch = _kv8_batch(starts, lengths, table, dev, i32)
+    if lse is not None and tuple(lse.shape) != (T, Hq):
+        raise ValueError(f"lse is {list(lse.shape)}, the call writes {[T, Hq]}")
+    need = svdq_kv8_attention_workspace_bytes(T, B, max_pages, Hq, Hk, D)
+    st = lib().svdq_kv8_attention(qp, qst, *cache, *batch, T, B, max_pages, P, Hq, Hk, D, scale, 1 if causal else 0,
+                                  window, _dev_ptr(O, 2, T * Hq * D * 2, "O", dev, bf16),
+                                  _dev_ptr(lse, 4, T * Hq * 4, "lse", dev, f32),
+                                  _dev_ptr(workspace, None, need, "workspace", dev), 0 if workspace is None else need,
+                                  _stream(stream))
+    _check("svdq_kv8_attention", st)
 
 
 def svdq_debug_group_partials(qx, qw, P, M, N, K, group=GROUP, qfmt=QFMT_INT4, stream=None):

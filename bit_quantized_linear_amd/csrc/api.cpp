@@ -108,6 +108,30 @@ svdq_status check_fp8_moe_shape(int T, int H, int I, int E, int top_k) {
     return fits_buffer((int64_t)T * top_k, 2LL * I) ? SVDQ_OK : SVDQ_ERR_UNSUPPORTED_SHAPE;
 }
 
+// The 8-bit cache: a launch numbers the new tokens' pages and the queries' tiles
+// in its grid's first dimension, sequences and heads in the others.
+constexpr int kKvMaxTokens = 1 << 24;
+constexpr int kKvMaxBatch = 65536;
+constexpr int kKvMaxHeads = 1024;
+
+svdq_status check_kv8_shape(int T, int B, int max_pages, int num_pages, int Hk, int D) {
+    if (T < 0 || B < 0 || max_pages <= 0 || num_pages <= 0 || Hk <= 0 || D <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
+    if ((D != 64 && D != 128) || T >= kKvMaxTokens || B >= kKvMaxBatch || Hk > kKvMaxHeads || max_pages > 1 << 24)
+        return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    return SVDQ_OK;
+}
+
+svdq_status check_kv8_queries(int T, int Hq, int Hk) {
+    if (Hq <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
+    return Hq % Hk || Hq > 65535 || (int64_t)T * Hq >= 1 << 30 ? SVDQ_ERR_UNSUPPORTED_SHAPE : SVDQ_OK;
+}
+
+// Rows of heads: a stride between tokens that holds a row and keeps 16-byte pieces aligned.
+svdq_status check_rows(int64_t stride, int64_t width) {
+    if (stride < width) return SVDQ_ERR_INVALID_ARGUMENT;
+    return stride % 8 ? SVDQ_ERR_UNSUPPORTED_SHAPE : SVDQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -560,6 +584,95 @@ svdq_status svdq_fp8_moe_layer(const uint16_t *X, const uint16_t *wr, const uint
     if (T == 0) return SVDQ_OK;
     return launched(svdq::launch_fp8_moe(X, wr, w13, s13, w2, s2, T, H, I, E, top_k, renormalize != 0, idx, gate,
                                          workspace, Y, (hipStream_t)stream));
+}
+
+svdq_status svdq_fp8_norm_quantize(const uint16_t *X, const uint16_t *residual, const uint16_t *w, float eps, int M,
+                                   int K, uint16_t *sum, uint16_t *Y, uint8_t *qx, float *sx, void *stream) {
+    if (M < 0 || K <= 0 || !(eps >= 0.0f) || std::isinf(eps)) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (K % 16 || K >= kFp8MaxK || M >= 1 << 22) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (!w || (M > 0 && (!X || (!Y && !qx) || !qx != !sx))) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(X) || !aligned16(residual) || !aligned16(w) || !aligned16(sum) || !aligned16(Y) || !aligned16(qx) ||
+        !aligned16(sx))
+        return SVDQ_ERR_MISALIGNED;
+    const svdq_status st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (M == 0) return SVDQ_OK;
+    return launched(svdq::launch_fp8_norm(X, residual, w, eps, M, K, sum, Y, qx, sx, (hipStream_t)stream));
+}
+
+svdq_status svdq_rope(const uint16_t *X, int64_t x_stride, const int32_t *positions, const double *freqs,
+                      const int *sections, int axes, int interleaved, int T, int H, int D, uint16_t *Y,
+                      int64_t y_stride, void *stream) {
+    if (T < 0 || H <= 0 || D <= 0 || axes <= 0 || !sections || !freqs) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (axes > SVDQ_ROPE_MAX_AXES || D % 8 || T >= 1 << 24 || (int64_t)H * D >= 1 << 24) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    int64_t pairs = 0;
+    for (int i = 0; i < axes; ++i) {
+        if (sections[i] < 0) return SVDQ_ERR_INVALID_ARGUMENT;
+        pairs += sections[i];
+    }
+    if (pairs == 0) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (pairs % 8 || pairs > SVDQ_ROPE_MAX_PAIRS || 2 * pairs > D) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    svdq_status st = check_rows(x_stride, (int64_t)H * D);
+    if (st == SVDQ_OK) st = check_rows(y_stride, (int64_t)H * D);
+    if (st != SVDQ_OK) return st;
+    if (T > 0 && (!X || !Y || !positions)) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(X) || !aligned16(positions) || !aligned16(freqs) || !aligned16(Y)) return SVDQ_ERR_MISALIGNED;
+    if (X == Y && x_stride != y_stride && T > 1) return SVDQ_ERR_INVALID_ARGUMENT;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0) return SVDQ_OK;
+    return launched(svdq::launch_rope(X, x_stride, positions, freqs, sections, axes, interleaved != 0, T, H, D, Y,
+                                      y_stride, (hipStream_t)stream));
+}
+
+svdq_status svdq_kv8_append(const uint16_t *K, int64_t k_stride, const uint16_t *V, int64_t v_stride,
+                            const int32_t *starts, const int32_t *lengths, const int32_t *table, int T, int B,
+                            int max_pages, int num_pages, int Hk, int D, uint8_t *kc, float *ks, uint8_t *vc,
+                            float *vs, void *stream) {
+    svdq_status st = check_kv8_shape(T, B, max_pages, num_pages, Hk, D);
+    if (st == SVDQ_OK) st = check_rows(k_stride, (int64_t)Hk * D);
+    if (st == SVDQ_OK) st = check_rows(v_stride, (int64_t)Hk * D);
+    if (st != SVDQ_OK) return st;
+    if (!kc || !ks || !vc || !vs || (T > 0 && (!K || !V)) || !starts || (B > 0 && (!lengths || !table)))
+        return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(K) || !aligned16(V) || !aligned16(starts) || !aligned16(lengths) || !aligned16(table) ||
+        !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0 || B == 0) return SVDQ_OK;
+    const svdq::KvBatch kv{starts, lengths, table, T, B, max_pages, num_pages};
+    return launched(svdq::launch_kv8_append(kv, K, k_stride, V, v_stride, Hk, D, kc, ks, vc, vs, (hipStream_t)stream));
+}
+
+size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, int Hk, int D) {
+    if (check_kv8_shape(T, B, max_pages, 1, Hk, D) != SVDQ_OK || check_kv8_queries(T, Hq, Hk) != SVDQ_OK) return 0;
+    return svdq::kv8_attention_workspace(T, B, max_pages, Hq, Hk, D);
+}
+
+svdq_status svdq_kv8_attention(const uint16_t *Q, int64_t q_stride, const uint8_t *kc, const float *ks,
+                               const uint8_t *vc, const float *vs, const int32_t *starts, const int32_t *lengths,
+                               const int32_t *table, int T, int B, int max_pages, int num_pages, int Hq, int Hk, int D,
+                               float scale, int causal, int window, uint16_t *O, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    svdq_status st = check_kv8_shape(T, B, max_pages, num_pages, Hk, D);
+    if (st == SVDQ_OK) st = check_kv8_queries(T, Hq, Hk);
+    if (st == SVDQ_OK) st = check_rows(q_stride, (int64_t)Hq * D);
+    if (st != SVDQ_OK) return st;
+    if (!(scale > 0.0f) || std::isinf(scale) || window < 0 || (window > 0 && !causal)) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!kc || !ks || !vc || !vs || (T > 0 && (!Q || !O)) || !starts || (B > 0 && (!lengths || !table)))
+        return SVDQ_ERR_INVALID_ARGUMENT;
+    const size_t need = svdq::kv8_attention_workspace(T, B, max_pages, Hq, Hk, D);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SVDQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(Q) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) || !aligned16(starts) ||
+        !aligned16(lengths) || !aligned16(table) || !aligned16(O) || !aligned16(lse) || !aligned16(workspace))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0 || B == 0) return SVDQ_OK;
+    const svdq::KvBatch kv{starts, lengths, table, T, B, max_pages, num_pages};
+    return launched(svdq::launch_kv8_attention(kv, Q, q_stride, kc, ks, vc, vs, Hq, Hk, D, scale, causal != 0, window, O,
+                                               lse, workspace, (hipStream_t)stream));
 }
 
 svdq_status svdq_debug_group_partials(const uint8_t *qx, const uint8_t *qw,

@@ -33,7 +33,7 @@ svdq_status truncated_svd(const double *A, int K, int N, int rank, double *U,
 bool all_finite_bf16(const uint16_t *p, int64_t n);
 
 // ---- device launchers (act_quant.hip, w4a4_gemm.hip, w4a4_fp6_gemm.hip, w8a8.hip, w4a16.hip,
-//      mx_gemm.hip, fp8.hip, fp8_moe.hip) ----
+//      mx_gemm.hip, fp8.hip, fp8_moe.hip, fp8_norm.hip, rope.hip, kv8_append.hip, kv8_attention.hip) ----
 // Arguments are validated by the caller; launchers only pick a grid and launch.
 hipError_t launch_channel_absmax(const uint16_t *X, int M, int K, float *absmax,
                                  hipStream_t stream);
@@ -114,6 +114,24 @@ size_t fp8_moe_workspace_size(int T, int I, int E, int top_k);
 hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *w13, const float *s13,
                           const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k, bool renorm,
                           int32_t *idx, float *gate, void *workspace, uint16_t *Y, hipStream_t stream);
+
+// norm, rotary positions, 8-bit key and value cache (fp8_norm.hip, rope.hip, kv8_append.hip, kv8_attention.hip)
+hipError_t launch_fp8_norm(const uint16_t *X, const uint16_t *residual, const uint16_t *w, float eps, int M, int K,
+                           uint16_t *sum, uint16_t *Y, uint8_t *qx, float *sx, hipStream_t stream);
+hipError_t launch_rope(const uint16_t *X, int64_t x_stride, const int32_t *positions, const double *freqs,
+                       const int *sections, int axes, int interleaved, int T, int H, int D, uint16_t *Y,
+                       int64_t y_stride, hipStream_t stream);
+// a batch on the cache: device arrays starts [B + 1], lengths [B], table [B, max_pages]
+struct KvBatch {
+    const int32_t *starts, *lengths, *table;
+    int T, B, max_pages, num_pages;
+};
+hipError_t launch_kv8_append(const KvBatch &kv, const uint16_t *K, int64_t k_stride, const uint16_t *V, int64_t v_stride,
+                             int Hk, int D, uint8_t *kc, float *ks, uint8_t *vc, float *vs, hipStream_t stream);
+size_t kv8_attention_workspace(int T, int B, int max_pages, int Hq, int Hk, int D);
+hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_stride, const uint8_t *kc,
+                                const float *ks, const uint8_t *vc, const float *vs, int Hq, int Hk, int D, float scale,
+                                bool causal, int window, uint16_t *O, float *lse, void *workspace, hipStream_t stream);
 
 // matrix-core rate microbenchmark (peak.hip)
 int64_t mfma_rate_ops_per_wave_round(int kind);

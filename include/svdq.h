@@ -115,6 +115,10 @@ typedef enum svdq_qformat {
 #define SVDQ_FP8_MOE_MAX_TOKENS 64
 #define SVDQ_FP8_MOE_MAX_EXPERTS 256
 #define SVDQ_FP8_MOE_MAX_TOP_K 16
+#define SVDQ_ROPE_MAX_AXES 4
+#define SVDQ_ROPE_MAX_PAIRS 256
+#define SVDQ_KV8_PAGE 64
+#define SVDQ_KV8_MAX_SPLITS 128
 
 /* Text of a status code (static storage; never NULL). */
 const char *svdq_status_string(int status);
@@ -564,6 +568,126 @@ svdq_status svdq_fp8_moe_layer(const uint16_t *X, const uint16_t *wr, const uint
                                const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k,
                                int renormalize, int32_t *idx, float *gate, void *workspace,
                                size_t workspace_bytes, uint16_t *Y, void *stream);
+
+/* The residual's addition and root-mean-square norm before block-scaled FP8
+ * linears, with their codes and scales as the output (svdq_fp8_gemm takes them):
+ *   h[m, k] = X[m, k] + residual[m, k]                             (fp32)
+ *   y[m, k] = h[m, k] / sqrt(mean_k h[m, k]^2 + eps) * w[k]        (fp32)
+ *   per token m and block g of 128 features (the last holds what is left of
+ *   K): A = max(max |y|, 2^-100), sx[g, m] = fp32(A / 448),
+ *   qx = E4M3(fp32(y * fp32(448 / A))), round to nearest even.
+ *   The squares are summed in fp64; y goes to the codes without a rounding to
+ *   bf16. A token with a value that is not finite has NaN or 0 for its outputs'
+ *   values, other tokens are not affected.
+ * In:  X [M, K] bf16; residual [M, K] bf16 or NULL; w [K] bf16; eps >= 0.
+ * Out: sum [M, K] bf16: h rounded once, the next residual (NULL if not wanted;
+ *      may be residual or X itself); Y [M, K] bf16: y rounded once, for layers
+ *      that take bf16 (svdq_fp8_moe_layer); qx [M, K] E4M3 bytes and
+ *      sx [ceil(K/128), M] fp32. Y, or qx and sx, may be NULL, not both.
+ * Shapes: M >= 0 (M == 0 launches nothing), K % 16 == 0, K < 2^22, M < 2^22.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
+ *      HIP. */
+svdq_status svdq_fp8_norm_quantize(const uint16_t *X, const uint16_t *residual, const uint16_t *w, float eps, int M,
+                                   int K, uint16_t *sum, uint16_t *Y, uint8_t *qx, float *sx, void *stream);
+
+/* Rotary positions with one or several axes (a text's position; time, height and
+ * width of a video's token) on H heads of T tokens:
+ *   angle[t, j] = positions[t, axis of pair j] * freqs[j]          (fp64)
+ *   (a, b) -> (a cos - b sin, a sin + b cos)           (fp32, rounded once)
+ * for the R / 2 pairs of a head's first R features, R / 2 = the sum of sections:
+ * pair j is features (2j, 2j + 1) if interleaved != 0, otherwise (j, j + R / 2);
+ * axis a has sections[a] consecutive pairs. Features from R on are copied.
+ * Negative frequencies turn back.
+ * In:  X bf16, head h of token t at X + t x_stride + h D (strides in elements:
+ *      a projection's rows serve as they are, query and key heads in one call);
+ *      positions [T, axes] int32; freqs [R / 2] fp64; sections [axes] (host).
+ * Out: Y bf16, likewise with y_stride; Y may be X with the same stride, and must
+ *      not overlap it otherwise.
+ * Shapes: T >= 0 (T == 0 launches nothing) and T < 2^24, D % 8 == 0, R % 16 == 0,
+ *      0 < R <= D, R / 2 <= SVDQ_ROPE_MAX_PAIRS, axes <= SVDQ_ROPE_MAX_AXES,
+ *      strides % 8 == 0 and >= H D, H D < 2^24.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
+ *      HIP. */
+svdq_status svdq_rope(const uint16_t *X, int64_t x_stride, const int32_t *positions, const double *freqs,
+                      const int *sections, int axes, int interleaved, int T, int H, int D, uint16_t *Y,
+                      int64_t y_stride, void *stream);
+
+/* The 8-bit key and value cache. num_pages pages of SVDQ_KV8_PAGE = 64 tokens:
+ *   kc [num_pages, Hk, 64, D] E4M3 bytes (keys), ks [num_pages, Hk] fp32,
+ *   vc [num_pages, Hk, D, 64] E4M3 bytes (values, a feature's 64 tokens
+ *   together), vs [num_pages, Hk] fp32; value = code * the page's scale.
+ * A batch of B sequences in a call:
+ *   starts [B + 1] int32: rows starts[b] .. starts[b + 1] - 1 of the call's T
+ *      rows are the newest tokens of sequence b, in order;
+ *   lengths [B] int32: tokens of sequence b, the new ones among them;
+ *   table [B, max_pages] int32: token t of sequence b is token t % 64 of page
+ *      table[b, t / 64].
+ * All three are read on the device (a captured graph sees what they hold when it
+ * is replayed). Whatever they contain, no access leaves the buffers: starts are
+ * held to 0 .. T, lengths to 0 .. 64 max_pages, and tokens of a page number
+ * outside 0 .. num_pages - 1 are not written and not seen. Rows outside the
+ * sequences' are left as they are. */
+
+/* New keys and values into the cache, before or after svdq_rope as the model has
+ * it. Row starts[b] + i becomes token lengths[b] - n + i of sequence b, n its
+ * new tokens (those that would be before token 0 are left out).
+ *   per page, head, and keys and values: A = max(max |x| over the new tokens,
+ *   2^-100), need = the least power of two with A <= 448 need; s = need, or
+ *   max(need, the page's scale) where the page holds earlier tokens of the
+ *   sequence; code = E4M3(fp32(x / s)), and the earlier tokens' codes become
+ *   E4M3(fp32(code * (old scale / s))), both round to nearest even.
+ * Values that are not finite become the NaN code and do not count for A. What a
+ * page holds behind the sequence's last token is neither read nor written.
+ * In:  K, V bf16, head h of row t at K + t k_stride + h D (strides in elements).
+ * In/out: kc, ks, vc, vs. A page that a call writes belongs to one sequence of
+ *      the batch (a page shared as a prefix is copied before it is written).
+ * The same call again gives the same cache.
+ * Shapes: T >= 0, B >= 0 (either 0 launches nothing), T < 2^24, B < 65536,
+ *      D 64 or 128, 1 <= Hk <= 1024, strides % 8 == 0 and >= Hk D,
+ *      1 <= max_pages <= 2^24, num_pages >= 1.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
+ *      HIP. */
+svdq_status svdq_kv8_append(const uint16_t *K, int64_t k_stride, const uint16_t *V, int64_t v_stride,
+                            const int32_t *starts, const int32_t *lengths, const int32_t *table, int T, int B,
+                            int max_pages, int num_pages, int Hk, int D, uint8_t *kc, float *ks, uint8_t *vc,
+                            float *vs, void *stream);
+
+/* Bytes of device workspace of svdq_kv8_attention (0 if it needs none, or on a
+ * bad argument). */
+size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, int Hk, int D);
+
+/* Attention of a batch's newest tokens over the cache: prompts, parts of prompts,
+ * decoded and drafted tokens; the new tokens' keys and values have been appended.
+ *   o[q] = sum_t softmax_t(scale q . k_t) v_t     over the tokens t that q sees:
+ *   with causal != 0 token i of n new ones is at position p = lengths[b] - n + i
+ *   and sees the tokens up to p, with window > 0 only the last `window` of them
+ *   (itself among them); with causal == 0 (text or frames that a diffusion model
+ *   looks at) every token of its sequence.
+ *   A query that sees nothing has 0 for its output. Tokens that a query does not
+ *   see have no part in its output, NaN or infinities in their place or not.
+ * Head hq of a query uses the keys and values of head hq / (Hq / Hk).
+ * Scores, weights' sums and outputs are fp32 sums of products of bf16 numbers
+ * (the codes' values, exact; weights rounded to bf16); one rounding to bf16.
+ * In:  Q bf16, head h of row t at Q + t q_stride + h D (stride in elements);
+ *      scale finite and > 0.
+ * Out: O [T, Hq, D] bf16; lse [T, Hq] fp32 or NULL: the natural logarithm of the
+ *      sum of exp(scale q . k_t) over what is seen (-infinity for nothing), with
+ *      which outputs over parts of a context can be joined.
+ * Workspace: device memory of at least svdq_kv8_attention_workspace_bytes(T, B,
+ *      max_pages, Hq, Hk, D) bytes (NULL if that is 0), owned by the caller, not
+ *      read before it is written; calls that may overlap in time need one each.
+ * A batch with few queries per sequence on average (T Hq / Hk <= 16 B) shares a
+ * sequence's pages between blocks; other batches share the queries only, so
+ * decoded tokens are best kept in calls of their own.
+ * Shapes: as svdq_kv8_append, with Hq % Hk == 0, T Hq < 2^30, Hq <= 65535,
+ *      q_stride >= Hq D. Deterministic.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
+ *      HIP. */
+svdq_status svdq_kv8_attention(const uint16_t *Q, int64_t q_stride, const uint8_t *kc, const float *ks,
+                               const uint8_t *vc, const float *vs, const int32_t *starts, const int32_t *lengths,
+                               const int32_t *table, int T, int B, int max_pages, int num_pages, int Hq, int Hk, int D,
+                               float scale, int causal, int window, uint16_t *O, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------- TEST-ONLY (same kernels) --- */
 
