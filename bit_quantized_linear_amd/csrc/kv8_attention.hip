@@ -22,6 +22,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "fp8_common.h"
@@ -351,199 +352,462 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 
 // ---- many queries ----------------------------------------------------------
 
-constexpr int kPreRows = 128;
+// 8 codes as bf16 values times a page's scale, a power of two, which goes into the
+// conversion; and times another scale (of a cache filled elsewhere), for a rounding.
+__device__ __forceinline__ u32x4 widen_scaled(u32x2 v, float scale) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], scale, false));
+        w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], scale, true));
+    }
+    return w;
+}
 
-// A block takes 128 queries, 32 a wave, and walks the pages that they see: a page
-// goes to LDS as bf16, by all threads, into one of two buffers while the other is
-// read; its loads are under way a page earlier.
-template <int D>
-__global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(AttnArgs a) {
-    constexpr int KS = D / 16, DT = D / 32, KCH = D / 8, BPT = D / 4;  // BPT: bytes of a page per thread
-    struct Stage {
-        u32x4 k[kKvPage * KCH];
-        u32x4 v[D * 8];
-    };
-    __shared__ Stage stage[2];
-    __shared__ uint32_t nan_s[2][4];
+__device__ __forceinline__ u32x4 widen_rounded(u32x2 v, float scale) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = (int)v[i];
+        w[2 * i] = bf16x2_bits(__builtin_amdgcn_cvt_f32_fp8(x, 0) * scale, __builtin_amdgcn_cvt_f32_fp8(x, 1) * scale);
+        w[2 * i + 1] = bf16x2_bits(__builtin_amdgcn_cvt_f32_fp8(x, 2) * scale, __builtin_amdgcn_cvt_f32_fp8(x, 3) * scale);
+    }
+    return w;
+}
+
+__device__ __forceinline__ bool power_of_two(float x) { return !(__float_as_uint(x) & 0x807FFFFFu) && x > 0.0f && x < INFINITY; }
+
+// The larger of a lane's and the other half wave's value.
+__device__ __forceinline__ float max_of_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+constexpr float kRise = 6.0f;  // how far, in powers of two, a score may pass the base that weights are taken to
+
+constexpr int kPreInfo = 512;  // pages whose numbers and scales are in LDS at a time
+
+// A block takes 32 queries a wave and walks the pages that they see, or its part of
+// them, in steps of 32 tokens. A page goes to LDS as bf16, by all threads, a page
+// before it is read, its loads a page earlier; its number and scales are read for
+// 512 pages at once, so that no load waits for another in the loop.
+// Pages that every query of the block sees whole are pipelined: a step multiplies
+// the next step's scores and the last one's weights while it works out its own
+// weights, three things that do not wait for each other. The base of the weights
+// (m above) is a whole number and rises only where a score passes it by more than
+// kRise: weights are then below 2^kRise, and what is multiplied when it does rise
+// (O, l and the weights not yet multiplied) is multiplied exactly.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a, int tiles) {
+    constexpr int KS = D / 16, DT = D / 32, KCH = D / 8;
+    constexpr int PC = D / 8 / NW;  // pieces of 8 codes of a page's keys, and of its values, per thread
+    constexpr int kRows = 32 * NW;
+    constexpr int KP = KCH + 1, VP = 9;  // pieces of 16 bytes from row to row in LDS: 8 rows at a piece fall on distinct banks
+    __shared__ u32x4 k_s[2][kKvPage * KP];
+    __shared__ u32x4 v_s[3][D * VP];
+    __shared__ u32x4 info_s[kPreInfo];
+    __shared__ uint32_t nan_s[3][NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q32 = lane & 31, h = lane >> 5;
-    const int head = blockIdx.y;
-    int b, tile;
     const int group = a.group;
-    if (!kv_find(a.kv, blockIdx.x, b, tile, [=](const KvSeq &s) { return (s.rows * group + kPreRows - 1) / kPreRows; }))
-        return;
+    // Blocks are dealt to the 8 XCDs in turn: a head's tiles go to one of them, so
+    // that its pages are read once per L2; the heads left over go to all
+    int head, item;
+    const int split = blockIdx.y;
+    {
+        const int whole = a.Hk / 8 * 8, id = blockIdx.x;
+        if (id < whole * tiles) {
+            head = id / (8 * tiles) * 8 + id % 8;
+            item = id / 8 % tiles;
+        } else {
+            const int rest = a.Hk - whole, j = id - whole * tiles;
+            head = whole + j % rest;
+            item = j / rest;
+        }
+    }
+    int b, tile;
+    if (!kv_find(a.kv, item, b, tile, [=](const KvSeq &s) { return (s.rows * group + kRows - 1) / kRows; })) return;
     b = __builtin_amdgcn_readfirstlane(b);
     const KvSeq seq = kv_seq(a.kv, b);
     const int rows = seq.rows * group;
-    tile = (rows + kPreRows - 1) / kPreRows - 1 - __builtin_amdgcn_readfirstlane(tile);  // the longest first
-    const int r0 = tile * kPreRows, last = min(r0 + kPreRows, rows) - 1;
-    const int wr0 = min(r0 + 32 * wave, last), wlast = min(wr0 + 31, last);
-    const int r = min(wr0 + q32, last);
-    int low, high, low0, high0, low1, high1, wlow0, whigh0, wlow1, whigh1;
-    kv_seen(a, seq, r / group, low, high);
+    tile = (rows + kRows - 1) / kRows - 1 - __builtin_amdgcn_readfirstlane(tile);  // the longest first
+    const int r0 = tile * kRows, last = min(r0 + kRows, rows) - 1;
+    const int row = min(r0 + 32 * wave + q32, last);
+    int low, high, low0, high0, low1, high1;
+    kv_seen(a, seq, row / group, low, high);
     kv_seen(a, seq, r0 / group, low0, high0);
     kv_seen(a, seq, last / group, low1, high1);
-    kv_seen(a, seq, wr0 / group, wlow0, whigh0);
-    kv_seen(a, seq, wlast / group, wlow1, whigh1);
-    const int p0 = low0 / kKvPage, p1 = (high1 + kKvPage - 1) / kKvPage;
+    // pages p0 .. p1 - 1 are this block's, of them f0 .. f1 - 1 seen whole by every query
+    int p0 = low0 / kKvPage, p1 = (high1 + kKvPage - 1) / kKvPage;
+    {
+        const int per = (max(p1 - p0, 0) + a.splits - 1) / a.splits;
+        p0 += split * per;
+        p1 = min(p1, p0 + per);
+    }
+    const int f0 = (low1 + kKvPage - 1) / kKvPage, f1 = high0 / kKvPage;
 
     bf16x8 q[KS];
     {
-        const uint16_t *src = a.Q + (int64_t)(seq.row0 + r / group) * a.q_stride +
-                              (int64_t)(head * group + r % group) * D + 8 * h;
+        const uint16_t *src = a.Q + (int64_t)(seq.row0 + row / group) * a.q_stride +
+                              (int64_t)(head * group + row % group) * D + 8 * h;
 #pragma unroll
         for (int i = 0; i < KS; ++i) q[i] = bitcast<bf16x8>(src + 16 * i);
     }
-    float m = -INFINITY, l = 0.0f;
+    float base = -3.4028235e38f, l = 0.0f;
     f32x16 o[DT];
+    auto zero = [](f32x16 &x) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < DT; ++i)
+        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+    };
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+    for (int i = 0; i < DT; ++i) zero(o[i]);
 
-    // this thread's part of a page: BPT bytes of key tid / 4 and of a row of V^T
-    u32x4 kr[BPT / 16], vr[BPT / 16];
-    float ks = 0.0f, vs = 0.0f;
-    int page = -1;
-    auto fetch = [&](int p) __attribute__((always_inline)) {
-        page = p < p1 ? kv_page(a.kv, b, p) : -1;
-        if (page < 0) return;
-        const int64_t unit = (int64_t)page * a.Hk + head;
-        ks = a.ks[unit];
-        vs = a.vs[unit];
-        const uint8_t *kp = a.kc + unit * kKvPage * D + tid * BPT, *vp = a.vc + unit * kKvPage * D + tid * BPT;
-#pragma unroll
-        for (int i = 0; i < BPT / 16; ++i) {
-            kr[i] = bitcast<u32x4>(kp + 16 * i);
-            vr[i] = bitcast<u32x4>(vp + 16 * i);
+    // ---- pages to LDS ----
+    // info_s: page number (-1: not there), the factor of its scores, its value scale,
+    // and whether it is plain: there, seen whole by every query, its value scale a
+    // power of two. Plain pages are what the pipelined steps take
+    int info0 = 0;  // the page of info_s[0]
+    auto load_info = [&](int from, int to) __attribute__((always_inline)) {
+        info0 = from;
+        for (int i = tid; i < to - from; i += 64 * NW) {
+            const int p = from + i, page = kv_page(a.kv, b, p);
+            u32x4 x = {(uint32_t)page, 0u, 0u, 0u};
+            if (page >= 0) {
+                const int64_t unit = (int64_t)page * a.Hk + head;
+                const float ks = a.ks[unit], vs = a.vs[unit];
+                x[1] = __float_as_uint(fmaxf(ks * a.scale, 1.17549435e-38f));
+                x[2] = __float_as_uint(vs);
+                x[3] = p >= f0 && p < f1 && power_of_two(vs);
+            }
+            info_s[i] = x;
         }
     };
-    const int krow = tid / 4, kch = tid % 4 * (BPT / 8), vrow = tid * BPT / 64, vch = tid * BPT % 64 / 8;
-    // matrix-core row i of a tile of 32 keys is token 16 (i / 16) + 8 (i / 4 % 2) + 4 (i / 8 % 2) + i % 4
-    const int key = 16 * (q32 >> 4) + 8 * (q32 >> 2 & 1) + 4 * (q32 >> 3 & 1) + (q32 & 3);
-
-    fetch(p0);
-    int buf = 0;
-    for (int p = p0; p < p1; ++p) {
-        if (page < 0) {
-            fetch(p + 1);
-            continue;
+    // this thread's part of a page: PC pieces of a key and of a row of V^T
+    u32x2 kr[PC], vr[PC];
+    u32x4 held = {0u, 0u, 0u, 0u};  // info of the page in kr, vr
+    auto fetch = [&](u32x4 info) __attribute__((always_inline)) {
+        held = info;
+        const int page = max(__builtin_amdgcn_readfirstlane((int)info[0]), 0);
+        const int64_t unit = (int64_t)page * a.Hk + head;
+        const uint8_t *kp = a.kc + unit * kKvPage * D + tid * PC * 8, *vp = a.vc + unit * kKvPage * D + tid * PC * 8;
+        if constexpr (PC == 1) {
+            kr[0] = bitcast<u32x2>(kp);
+            vr[0] = bitcast<u32x2>(vp);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PC; i += 2) {
+                const u32x4 k = bitcast<u32x4>(kp + 8 * i), v = bitcast<u32x4>(vp + 8 * i);
+                kr[i] = u32x2{k[0], k[1]};
+                kr[i + 1] = u32x2{k[2], k[3]};
+                vr[i] = u32x2{v[0], v[1]};
+                vr[i + 1] = u32x2{v[2], v[3]};
+            }
         }
-        const int t0 = p * kKvPage;
-        Stage &st = stage[buf];
-        // a page that some query does not see whole (see the kernel above)
-        const bool cut = t0 < low1 || t0 + kKvPage > high0;
-        if (cut) {
+    };
+    auto held_plain = [&]() __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane((int)held[3]) != 0; };
+    // matrix-core row i of a tile of 32 keys is token 16 (i / 16) + 8 (i / 4 % 2) + 4 (i / 8 % 2) + i % 4, so that
+    // element e of a lane's scores is token 16 (e / 8) + 8 h + e % 8: keys lie in LDS in that order
+    const int token = tid * PC / KCH, krow = (token & 0x33) | (token & 8) >> 1 | (token & 4) << 1;
+    const int k_at = krow * KP + tid * PC % KCH, v_at = tid * PC / 8 * VP + tid * PC % 8;
+    // The page held to LDS, as page p.
+    // Of a page that some query does not see whole, values that none sees become 0 (a
+    // hidden token's weight is 0, but its value may be NaN), and it is noted whether
+    // one of the others is NaN
+    auto store = [&](int p, int ki, int vi) __attribute__((always_inline)) {
+        const bool there = (int)held[0] >= 0;
+        const float vs = __uint_as_float(held[2]);
+        if (!there) {
+#pragma unroll
+            for (int i = 0; i < PC; ++i) kr[i] = vr[i] = u32x2{0u, 0u};
+        }
+        if (p < f0 || p >= f1) {
             uint32_t nan = 0;
 #pragma unroll
-            for (int i = 0; i < BPT / 16; ++i)
+            for (int i = 0; i < PC; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    vr[i][j] &= byte_mask(t0 + 8 * vch + 16 * i + 4 * j, low0, high1);
+                for (int j = 0; j < 2; ++j) {
+                    vr[i][j] &= byte_mask(p * kKvPage + tid * PC % 8 * 8 + 8 * i + 4 * j, low0, high1);
                     nan |= nan_codes(vr[i][j]);
                 }
             const bool any = __any(nan != 0);
-            if (lane == 0) nan_s[buf][wave] = any;
+            if (lane == 0) nan_s[vi][wave] = any;
+        } else if (lane == 0) {
+            nan_s[vi][wave] = 0;
         }
+        const bool two = power_of_two(vs);
 #pragma unroll
-        for (int i = 0; i < BPT / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                st.k[krow * KCH + ((kch + 2 * i + j) ^ (krow & 7))] =
-                    __builtin_bit_cast(u32x4, fp8_widen8(kr[i][2 * j], kr[i][2 * j + 1]));
-                st.v[vrow * 8 + ((vch + 2 * i + j) ^ (vrow & 7))] =
-                    __builtin_bit_cast(u32x4, fp8_widen8(vr[i][2 * j], vr[i][2 * j + 1]));
-            }
-        const float c = ks * a.scale, vscale = vs;
+        for (int i = 0; i < PC; ++i) {
+            k_s[ki][k_at + i] = widen_scaled(kr[i], 1.0f);
+            v_s[vi][v_at + i] = two ? widen_scaled(vr[i], vs) : widen_rounded(vr[i], there ? vs : 1.0f);
+        }
+    };
+    // One of the 2 PC pieces of a plain page
+    auto store_piece = [&](int n, int ki, int vi) __attribute__((always_inline)) {
+        if (n < PC)
+            k_s[ki][k_at + n] = widen_scaled(kr[n], 1.0f);
+        else
+            v_s[vi][v_at + n - PC] = widen_scaled(vr[n - PC], __uint_as_float(held[2]));
+    };
+    auto meet = [&]() __attribute__((always_inline)) {  // what this wave wrote is in LDS, and everyone is here
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's part is in LDS
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         fp8_barrier();
-        fetch(p + 1);
-        const bool slow = cut && (nan_s[buf][0] | nan_s[buf][1] | nan_s[buf][2] | nan_s[buf][3]);
-        buf ^= 1;
-        if (t0 >= whigh1 || t0 + kKvPage <= wlow0) continue;  // none of this wave's queries sees it
+    };
 
-        f32x16 s[2];
+    // ---- a step of 32 tokens: half a page ----
+    auto key = [&](int ki, int half, int i) __attribute__((always_inline)) {  // 8 features from 16 i on of 32 tokens
+        return __builtin_bit_cast(bf16x8, k_s[ki][(32 * half + q32) * KP + 2 * i + h]);
+    };
+    auto value = [&](int vi, int half, int u, int i) __attribute__((always_inline)) {  // 8 tokens of 32 features
+        return __builtin_bit_cast(bf16x8, v_s[vi][(32 * i + q32) * VP + 4 * half + 2 * u + h]);
+    };
+    auto top_of = [&](const f32x16 &s) __attribute__((always_inline)) {
+        float m = fmaxf(s[0], s[1]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < KS; ++i)
-                s[t] = mfma_bf16_32x32x16(
-                    __builtin_bit_cast(bf16x8, st.k[(32 * t + key) * KCH + ((2 * i + h) ^ (key & 7))]), q[i], s[t]);
-        }
-        if (t0 < wlow1 || t0 + kKvPage > whigh0) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int at = t0 + 32 * t + 16 * (e >> 3) + 8 * h + (e & 7);
-                    s[t][e] = at >= low && at < high ? s[t][e] : -INFINITY;
-                }
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[t][e]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = fmaxf(m, top * c);
-        const float base = m_new == -INFINITY ? 0.0f : m_new;
-        const float alpha = exp2_of(m - base);
-        m = m_new;
-        l *= alpha;
-        bf16x8 w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = exp2_of(__builtin_fmaf(s[u >> 1][8 * (u & 1) + e], c, -base));
-                l += x[e];
-            }
-            w[u] = pack8(x, vscale);
-        }
+        for (int e = 2; e < 16; e += 2) m = fmaxf(fmaxf(m, s[e]), s[e + 1]);
+        return max_of_halves(m);
+    };
+    // The base raised to a step's largest score, what was taken to the old one
+    // multiplied with the factor that is returned
+    auto raise_to = [&](float top) __attribute__((always_inline)) {
+        const float to = top > base ? ceilf(top) : base;
+        const float f = exp2_of(base - to);
+        base = to;
+        l *= f;
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[i][e] *= alpha;
-        auto value = [&](int i, int u) __attribute__((always_inline)) {
-            const int d = 32 * i + q32;
-            return __builtin_bit_cast(bf16x8, st.v[d * 8 + ((2 * u + h) ^ (d & 7))]);
-        };
-        if (!slow) {
+            for (int e = 0; e < 16; ++e) o[i][e] *= f;
+        return f;
+    };
+    auto raise = [&](float top, bf16x8 (&pending)[2]) __attribute__((always_inline)) {
+        if (!__any(top > base + kRise)) return;
+        const float f = raise_to(top);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 2; ++u) {
+            u32x4 w = __builtin_bit_cast(u32x4, pending[u]);
 #pragma unroll
-                for (int i = 0; i < DT; ++i) o[i] = mfma_bf16_32x32x16(value(i, u), w[u], o[i]);
-        } else {
+            for (int i = 0; i < 4; ++i)
+                w[i] = bf16x2_bits(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+            pending[u] = __builtin_bit_cast(bf16x8, w);
+        }
+    };
+    // The pipelined step. It has KS + 2 DT parts, pinned in this order: each issues the
+    // matrix-core instruction of one operand from LDS, fetches the operand kAhead
+    // parts on, and does a share of everything else.
+    //   s: this step's scores, whose weights go to w; c their factor
+    //   sn, top: the next step's scores (keys kn, half hn) and their largest
+    //   wp: the last step's weights (values vp, half hp)
+    //   (ka, ha): the keys of the step after the next
+    // kStage: store the page held to (ki, vi), meet the other waves, fetch the page of info_s[next]
+    constexpr int kParts = KS + 2 * DT;
+    constexpr int kAhead = D == 64 ? 3 : 5, kRing = 8;
+    static_assert(kAhead <= 2 * DT && kParts % kRing == 0, "the page is stored before the waves meet");
+    bf16x8 operand[kRing];
+    auto step = [&](auto kStage, int ki, int vi, int next, const float (&s)[16], float c, bf16x8 (&w)[2], int kn, int hn,
+                    float (&sn)[16], float &top, int vp, int hp, const bf16x8 (&wp)[2], int ka,
+                    int ha) __attribute__((always_inline)) {
+        float sum[2] = {0.0f, 0.0f}, most = -INFINITY;
+        uint32_t packed[2][4];
+        f32x16 acc;
+        zero(acc);
+        u32x4 info = held;
+#pragma unroll
+        for (int n = 0; n < kParts; ++n) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (kStage && n == kParts - kAhead) meet();
+            const bf16x8 x = operand[n % kRing];
+            const int v = n - KS;
+            if (n < KS)
+                acc = mfma_bf16_32x32x16(x, q[n], acc);
+            else
+                o[v % DT] = mfma_bf16_32x32x16(x, wp[v / DT], o[v % DT]);
+            const int r = n + kAhead, rv = r - KS;
+            operand[r % kRing] = r < KS       ? key(kn, hn, r)
+                                 : r < kParts ? value(vp, hp, rv / DT, rv % DT)
+                                              : key(ka, ha, r - kParts);
+            if (kStage && n == 0) info = info_s[next];
+            if (kStage && n < KS) {
+#pragma unroll
+                for (int i = n * 2 * PC / KS; i < (n + 1) * 2 * PC / KS; ++i) store_piece(i, ki, vi);
+            }
+            if (kStage && n == KS) fetch(info);
+            // this part's share of the 8 pairs of weights
+#pragma unroll
+            for (int j = n * 8 / kParts; j < (n + 1) * 8 / kParts; ++j) {
+                const int e = 2 * j;
+                const float x0 = exp2_of(__builtin_fmaf(s[e], c, -base));
+                const float x1 = exp2_of(__builtin_fmaf(s[e + 1], c, -base));
+                sum[0] += x0;
+                sum[1] += x1;
+                packed[j / 4][j % 4] = bf16x2_bits(x0, x1);
+                asm volatile("" : "+v"(packed[j / 4][j % 4]), "+v"(sum[0]), "+v"(sum[1]));  // here, not later
+            }
+            // and, from the second part behind the scores on, of the largest scores
+            if (n > KS) {
+                constexpr int kTopParts = kParts - KS - 1;
+                const int at = n - KS - 1;
+#pragma unroll
+                for (int j = at * 8 / kTopParts; j < (at + 1) * 8 / kTopParts; ++j) {
+                    sn[2 * j] = acc[2 * j];
+                    sn[2 * j + 1] = acc[2 * j + 1];
+                    most = fmaxf(fmaxf(most, sn[2 * j]), sn[2 * j + 1]);
+                    asm volatile("" : "+v"(most));
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        l += sum[0] + sum[1];
+        top = max_of_halves(most);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            w[u] = __builtin_bit_cast(bf16x8, u32x4{packed[u][0], packed[u][1], packed[u][2], packed[u][3]});
+    };
+    // A page, one thing after the other, with its masks
+    auto cut_page = [&](int p, int ki, int vi, float c) __attribute__((always_inline)) {
+        uint32_t slow = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) slow |= nan_s[vi][i];
+        for (int half = 0; c > 0.0f && half < 2; ++half) {
+            // the tokens that the lane's query sees, counted as its elements are: count of them, from `from` on
+            const int at = p * kKvPage + 32 * half + 8 * h, from = low - at;
+            const uint32_t count = (uint32_t)max(high - low, 0);
+            auto sees = [&](int e) { return (uint32_t)(16 * (e >> 3) + (e & 7) - from) < count; };
+            f32x16 s;
+            zero(s);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) s = mfma_bf16_32x32x16(key(ki, half, i), q[i], s);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
+            const float top = top_of(s) * c;
+            if (__any(top > base + kRise)) raise_to(top);
+            bf16x8 w[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = exp2_of(__builtin_fmaf(s[8 * u + e], c, -base));
+                    l += x[e];
+                }
+                w[u] = pack8(x, 1.0f);
+            }
+            if (!slow) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < DT; ++i) o[i] = mfma_bf16_32x32x16(value(vi, half, u, i), w[u], o[i]);
+                continue;
+            }
+            // NaN reaches the queries that see its token, and no other
+            bf16x8 seen[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                u32x4 see;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    see[e] = (sees(8 * u + 2 * e) ? 0x3F80u : 0u) | (sees(8 * u + 2 * e + 1) ? 0x3F800000u : 0u);
+                seen[u] = __builtin_bit_cast(bf16x8, see);
+            }
 #pragma unroll
             for (int i = 0; i < DT; ++i) {
-                f32x16 count;
+                f32x16 nans;
+                zero(nans);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) count[e] = 0.0f;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int at = t0 + 16 * u + 8 * h;
-                    u32x4 see;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        see[e] = (at + 2 * e >= low && at + 2 * e < high ? 0x3F80u : 0u) |
-                                 (at + 2 * e + 1 >= low && at + 2 * e + 1 < high ? 0x3F800000u : 0u);
-                    bf16x8 v = value(i, u), nan;
+                for (int u = 0; u < 2; ++u) {
+                    bf16x8 v = value(vi, half, u, i), nan;
                     split_nan(v, nan);
-                    count = mfma_bf16_32x32x16(nan, __builtin_bit_cast(bf16x8, see), count);
+                    nans = mfma_bf16_32x32x16(nan, seen[u], nans);
                     o[i] = mfma_bf16_32x32x16(v, w[u], o[i]);
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[i][e] = count[e] > 0.0f ? NAN : o[i][e];
+                for (int e = 0; e < 16; ++e) o[i][e] = nans[e] > 0.0f ? NAN : o[i][e];
             }
         }
+    };
+
+    for (int s0 = p0; s0 < p1; s0 += kPreInfo) {
+        const int s1 = min(p1, s0 + kPreInfo);
+        if (s0 > p0) meet();  // the last run's pages have been read
+        load_info(s0, s1);
+        meet();
+        // Page p is in k_s[kc], v_s[vc], its factor is c and `plain` says what it is; page p + 1 is held
+        int kc = 0, vc = 0, vp = 2;
+        const auto after = [&](int v) { return v == 2 ? 0 : v + 1; };
+        const auto info_at = [&](int p) { return min(p, s1 - 1) - info0; };
+        fetch(info_s[0]);
+        float c = __uint_as_float(held[1]);
+        bool plain = held_plain();
+        store(s0, kc, vc);
+        fetch(info_s[info_at(s0 + 1)]);
+        meet();
+        for (int p = s0; p < s1; ++p) {
+            if (plain && p + 1 < s1 && held_plain()) {
+                float t0[16], t1[16], top0, top1;
+                bf16x8 w0[2], w1[2] = {};
+                {
+                    f32x16 x;
+                    zero(x);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) x = mfma_bf16_32x32x16(key(kc, 0, i), q[i], x);
+                    top0 = top_of(x);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) t0[e] = x[e];
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) operand[i] = key(kc, 1, i);
+                int vw = vc;  // the values of w1 (at first zeros: any page that all see)
+                do {
+                    const float cn = __uint_as_float(held[1]);
+                    const int vn = after(vc);
+                    raise(top0 * c, w1);
+                    step(std::true_type(), kc ^ 1, vn, info_at(p + 2), t0, c, w0, kc, 1, t1, top1, vw, 1, w1, kc ^ 1, 0);
+                    raise(top1 * c, w0);
+                    step(std::false_type(), 0, 0, 0, t1, c, w1, kc ^ 1, 0, t0, top0, vc, 0, w0, kc ^ 1, 1);
+                    vw = vc;
+                    vc = vn;
+                    kc ^= 1;
+                    c = cn;
+                    ++p;
+                } while (p + 1 < s1 && held_plain());
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < DT; ++i) o[i] = mfma_bf16_32x32x16(value(vw, 1, u, i), w1[u], o[i]);
+            }
+            const float cn = __uint_as_float(held[1]);
+            const int vn = after(vc);
+            plain = held_plain();
+            if (p + 1 < s1) {
+                store(p + 1, kc ^ 1, vn);
+                fetch(info_s[info_at(p + 2)]);
+            }
+            cut_page(p, kc, vc, c);
+            meet();
+            kc ^= 1;
+            vc = vn;
+            c = cn;
+        }
     }
+
     l += __shfl_xor(l, 32);
-    if (wr0 + q32 > wlast || r0 + 32 * wave > last) return;
-    const int64_t at = (int64_t)(seq.row0 + r / group) * a.Hq + head * group + r % group;
+    if (r0 + 32 * wave + q32 > last) return;
+    const int64_t at = (int64_t)(seq.row0 + row / group) * a.Hq + head * group + row % group;
+    if (a.splits > 1) {
+        float *dst = a.part + (at * a.splits + split) * D;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<f32x4 *>(dst + 32 * i + 8 * e + 4 * h) =
+                    f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+        if (h == 0) {
+            float *ml = a.part + (int64_t)a.kv.T * a.Hq * a.splits * D + (at * a.splits + split) * 2;
+            ml[0] = base;
+            ml[1] = l;
+        }
+        return;
+    }
     const float f = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < DT; ++i)
@@ -552,7 +816,7 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(AttnArgs a) {
             *reinterpret_cast<u32x2 *>(a.O + at * D + 32 * i + 8 * e + 4 * h) =
                 u32x2{bf16x2_bits(o[i][4 * e] * f, o[i][4 * e + 1] * f),
                       bf16x2_bits(o[i][4 * e + 2] * f, o[i][4 * e + 3] * f)};
-    if (a.lse && h == 0) a.lse[at] = (m + log2f(l)) * kLn2;
+    if (a.lse && h == 0) a.lse[at] = (base + log2f(l)) * kLn2;
 }
 
 // Few queries per sequence and key head on average: the kernel that splits pages.
@@ -590,9 +854,10 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
                            dim3(256), 0, stream, a);
         return hipGetLastError();
     }
-    const int64_t tiles = ((int64_t)kv.T * a.group + (int64_t)(kPreRows - 1) * kv.B) / kPreRows;
-    hipLaunchKernelGGL(D == 64 ? kv8_prompt_kernel<64> : kv8_prompt_kernel<128>, dim3((unsigned)tiles, (unsigned)Hk),
-                       dim3(256), 0, stream, a);
+    const auto tiles = [&](int rows) { return (int)(((int64_t)kv.T * a.group + (int64_t)(rows - 1) * kv.B) / rows); };
+    const int n = tiles(256);
+    hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 8> : kv8_prompt_kernel<128, 8>), dim3((unsigned)(n * Hk)),
+                       dim3(512), 0, stream, a, n);
     return hipGetLastError();
 }
 
