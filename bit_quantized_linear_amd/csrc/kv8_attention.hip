@@ -95,11 +95,13 @@ constexpr int kDecWaves = 4;
 constexpr int kDecRows = 16;
 
 // A block takes up to 16 queries at a time and a run of the sequence's pages, its
-// waves every fourth of them, straight into registers, the next page while this
-// one is computed; the waves' sums are joined in LDS and, where a sequence's pages
-// are split over blocks, by a second kernel.
+// waves every fourth of them, straight into registers: the next page's keys as soon
+// as this one's scores are there, its values as soon as this one's are multiplied.
+// The numbers and scales of a wave's next 64 pages are in its lanes. The waves' sums
+// are joined in LDS and, where a sequence's pages are split over blocks, by a second
+// kernel.
 template <int D>
-__global__ __launch_bounds__(64 * kDecWaves) void kv8_decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs a) {
     constexpr int KC = D / 64;  // 64-byte pieces of a key
     constexpr int DT = D / 16;  // 16-row tiles of V^T
     __shared__ __align__(16) float o_s[kDecWaves][kDecRows][D + 4];
@@ -136,35 +138,50 @@ __global__ __launch_bounds__(64 * kDecWaves) void kv8_decode_kernel(AttnArgs a) 
 #pragma unroll
         for (int i = 0; i < DT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-        u32x4 k[4][KC], v[DT];
-        float ks = 0.0f, vs = 0.0f;
-        int page = -1;
-        auto fetch = [&](int p) __attribute__((always_inline)) {
-            page = p < p1 ? kv_page(a.kv, b, p) : -1;
-            if (page < 0) return;
-            const int64_t unit = (int64_t)page * a.Hk + head;
-            const uint8_t *kp = a.kc + unit * kKvPage * D, *vp = a.vc + unit * kKvPage * D;
-            ks = a.ks[unit];
+        // lane i: page p0 + wave + 4 (first + i) of the sequence
+        int number = -1, first = 0;
+        float factor = 0.0f, vs = 0.0f;
+        auto look_up = [&](int from) __attribute__((always_inline)) {
+            first = from;
+            const int p = p0 + wave + kDecWaves * (from + lane);
+            number = p < p1 ? kv_page(a.kv, b, p) : -1;
+            const int64_t unit = (int64_t)max(number, 0) * a.Hk + head;
+            factor = a.ks[unit] * a.scale;
             vs = a.vs[unit];
+        };
+        u32x4 k[4][KC], v[DT];
+        auto unit_of = [&](int i) {
+            return (int64_t)max(__builtin_amdgcn_readlane(number, i - first), 0) * a.Hk + head;
+        };
+        auto load_keys = [&](int i) __attribute__((always_inline)) {
+            const uint8_t *kp = a.kc + unit_of(i) * kKvPage * D;
             // tile j's row i is token 16 (i / 4) + 4 j + i % 4
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < KC; ++i)
-                    k[j][i] = bitcast<u32x4>(kp + (16 * (q16 >> 2) + 4 * j + (q16 & 3)) * D + 64 * i + 16 * g4);
-#pragma unroll
-            for (int i = 0; i < DT; ++i) v[i] = bitcast<u32x4>(vp + (16 * i + q16) * kKvPage + 16 * g4);
+                for (int n = 0; n < KC; ++n)
+                    k[j][n] = bitcast<u32x4>(kp + (16 * (q16 >> 2) + 4 * j + (q16 & 3)) * D + 64 * n + 16 * g4);
         };
-        fetch(p0 + wave);
-        for (int p = p0 + wave; p < p1; p += kDecWaves) {
-            if (page < 0) {
-                fetch(p + kDecWaves);
-                continue;
-            }
-            const float c = ks * a.scale, vscale = vs;
+        auto load_values = [&](int i) __attribute__((always_inline)) {
+            const uint8_t *vp = a.vc + unit_of(i) * kKvPage * D;
+#pragma unroll
+            for (int n = 0; n < DT; ++n) v[n] = bitcast<u32x4>(vp + (16 * n + q16) * kKvPage + 16 * g4);
+        };
+        const int count = p1 > p0 + wave ? (p1 - p0 - wave + kDecWaves - 1) / kDecWaves : 0;
+        if (count > 0) {
+            look_up(0);
+            load_keys(0);
+            load_values(0);
+        }
+        for (int i = 0; i < count; ++i) {
+            const int p = p0 + wave + kDecWaves * i;
+            const bool there = __builtin_amdgcn_readlane(number, i - first) >= 0, more = i + 1 < count;
+            const float c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(factor), i - first));
+            const float vscale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), i - first));
             f32x4 s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                __builtin_amdgcn_sched_barrier(0);  // few converted operands at a time: registers
                 s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < KC; ++i) {
@@ -172,11 +189,15 @@ __global__ __launch_bounds__(64 * kDecWaves) void kv8_decode_kernel(AttnArgs a) 
                     s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][i][2], k[j][i][3]), q[2 * i + 1], s[j]);
                 }
             }
-            u32x4 vc[DT];
-#pragma unroll
-            for (int i = 0; i < DT; ++i) vc[i] = v[i];
             const int t0 = p * kKvPage;
-            fetch(p + kDecWaves);
+            if (more) {
+                if (i + 1 - first == 64) look_up(i + 1);
+                load_keys(i + 1);
+            }
+            if (!there) {
+                if (more) load_values(i + 1);
+                continue;
+            }
             // a page that some query does not see whole: hidden tokens' weights are
             // 0, and their values are not multiplied, as they may be NaN
             uint32_t nan = 0;
@@ -187,9 +208,9 @@ __global__ __launch_bounds__(64 * kDecWaves) void kv8_decode_kernel(AttnArgs a) 
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t mask = byte_mask(t0 + 16 * g4 + 4 * j, low0, high1);
 #pragma unroll
-                    for (int i = 0; i < DT; ++i) {
-                        vc[i][j] &= mask;
-                        nan |= nan_codes(vc[i][j]);
+                    for (int n = 0; n < DT; ++n) {
+                        v[n][j] &= mask;
+                        nan |= nan_codes(v[n][j]);
                     }
                     see[j] = byte_mask(t0 + 16 * g4 + 4 * j, low, high);
 #pragma unroll
@@ -199,9 +220,9 @@ __global__ __launch_bounds__(64 * kDecWaves) void kv8_decode_kernel(AttnArgs a) 
                 for (int u = 0; u < 2; ++u) {
                     u32x4 w;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t two = see[2 * u + i / 2] >> (16 * (i & 1));
-                        w[i] = (two & 1 ? 0x3F80u : 0u) | (two & 0x100u ? 0x3F800000u : 0u);
+                    for (int n = 0; n < 4; ++n) {
+                        const uint32_t two = see[2 * u + n / 2] >> (16 * (n & 1));
+                        w[n] = (two & 1 ? 0x3F80u : 0u) | (two & 0x100u ? 0x3F800000u : 0u);
                     }
                     seen[u] = __builtin_bit_cast(bf16x8, w);
                 }
@@ -228,29 +249,33 @@ __global__ __launch_bounds__(64 * kDecWaves) void kv8_decode_kernel(AttnArgs a) 
                 }
             const bf16x8 w0 = pack8(w, vscale), w1 = pack8(w + 8, vscale);
 #pragma unroll
-            for (int i = 0; i < DT; ++i)
+            for (int n = 0; n < DT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
-            if (!__any(nan != 0)) {
+                for (int e = 0; e < 4; ++e) o[n][e] *= alpha;
+            if (__any(nan != 0)) {  // NaN reaches the queries that see its token, and no other
 #pragma unroll
-                for (int i = 0; i < DT; ++i) {
-                    o[i] = mfma_bf16_16x16x32(fp8_widen8(vc[i][0], vc[i][1]), w0, o[i]);
-                    o[i] = mfma_bf16_16x16x32(fp8_widen8(vc[i][2], vc[i][3]), w1, o[i]);
-                }
-            } else {  // NaN reaches the queries that see its token, and no other
+                for (int n = 0; n < DT; ++n) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    u32x4 one;  // the code of 1 for each NaN, which becomes 0 itself
 #pragma unroll
-                for (int i = 0; i < DT; ++i) {
-                    bf16x8 v0 = fp8_widen8(vc[i][0], vc[i][1]), v1 = fp8_widen8(vc[i][2], vc[i][3]), n0, n1;
-                    split_nan(v0, n0);
-                    split_nan(v1, n1);
-                    f32x4 count = mfma_bf16_16x16x32(n0, seen[0], f32x4{0.f, 0.f, 0.f, 0.f});
-                    count = mfma_bf16_16x16x32(n1, seen[1], count);
-                    o[i] = mfma_bf16_16x16x32(v0, w0, o[i]);
-                    o[i] = mfma_bf16_16x16x32(v1, w1, o[i]);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t at = (nan_codes(v[n][j]) >> 7) * 0xFFu;
+                        one[j] = at & 0x38383838u;
+                        v[n][j] &= ~at;
+                    }
+                    f32x4 count = mfma_bf16_16x16x32(fp8_widen8(one[0], one[1]), seen[0], f32x4{0.f, 0.f, 0.f, 0.f});
+                    count = mfma_bf16_16x16x32(fp8_widen8(one[2], one[3]), seen[1], count);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[i][e] = count[e] > 0.0f ? NAN : o[i][e];
+                    for (int e = 0; e < 4; ++e) o[n][e] = count[e] > 0.0f ? NAN : o[n][e];
                 }
             }
+#pragma unroll
+            for (int n = 0; n < DT; ++n) {
+                if (n % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+                o[n] = mfma_bf16_16x16x32(fp8_widen8(v[n][0], v[n][1]), w0, o[n]);
+                o[n] = mfma_bf16_16x16x32(fp8_widen8(v[n][2], v[n][3]), w1, o[n]);
+            }
+            if (more) load_values(i + 1);
         }
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
@@ -294,60 +319,54 @@ __global__ __launch_bounds__(64 * kDecWaves) void kv8_decode_kernel(AttnArgs a) 
     }
 }
 
-// The splits' sums of one query joined, by the waves of a block each a part.
+// The splits' sums of one query joined, by the waves of a block each a part. What is
+// read does not depend on what is read before, so that one wait covers all.
 template <int D>
 __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
-    constexpr int E = D / 64;
-    __shared__ float o_s[4][D], f_s[SVDQ_KV8_MAX_SPLITS];
-    __shared__ float red[2][4];
+    constexpr int E = D / 64, kEach = SVDQ_KV8_MAX_SPLITS / 4;
+    __shared__ float o_s[4][D];
     const int64_t at = (int64_t)blockIdx.x * a.Hq + blockIdx.y;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int first = min(max(a.kv.starts[0], 0), a.kv.T);
-    if (row < first || row >= min(max(a.kv.starts[a.kv.B], first), a.kv.T)) return;
+    const float *src = a.part + at * a.splits * D + lane * E;
+    float x[kEach][E];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i][e] = 4 * i + wave < a.splits ? src[(int64_t)(4 * i + wave) * D + e] : 0.0f;
     const float *ml = a.part + (int64_t)a.kv.T * a.Hq * a.splits * D + at * a.splits * 2;
-    float top = -INFINITY;
-    for (int s = tid; s < a.splits; s += 256) top = fmaxf(top, ml[2 * s]);
+    const float m = lane < a.splits ? ml[2 * lane] : -INFINITY, l = lane < a.splits ? ml[2 * lane + 1] : 0.0f;
+    const int first = min(max(a.kv.starts[0], 0), a.kv.T);
+    const int last = min(max(a.kv.starts[a.kv.B], first), a.kv.T);
+    float top = m;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) red[0][wave] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    float sum = 0.0f;
-    for (int s = tid; s < a.splits; s += 256) {
-        const float l = ml[2 * s + 1];
-        const float f = top == -INFINITY ? 1.0f : exp2_of(ml[2 * s] - top);
-        f_s[s] = l == 0.0f ? 0.0f : f;
-        sum += l * f;
-    }
+    const float f = top == -INFINITY ? 1.0f : exp2_of(m - top);
+    const float weight = l == 0.0f ? 0.0f : f;  // a part of nothing
+    float sum = l * weight;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-    if (lane == 0) red[1][wave] = sum;
-    __syncthreads();
-    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    const float *src = a.part + at * a.splits * D + lane * E;
-#pragma unroll 8
-    for (int s = wave; s < a.splits; s += 4) {
-        const float f = f_s[s];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(f, src[(int64_t)s * D + e], acc[e]);
+    for (int i = 0; i < kEach; ++i) {
+        const float w = __shfl(weight, (4 * i + wave) & 63);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(w, x[i][e], acc[e]);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) o_s[wave][lane * E + e] = acc[e];
     __syncthreads();
-    if (tid < D / 2) {
-        float v[2];
-        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (row < first || row >= last || tid >= D / 2) return;
+    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+    float v[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int d = 2 * tid + e;
-            v[e] = ((o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d])) * f;
-        }
-        reinterpret_cast<uint32_t *>(a.O + at * D)[tid] = bf16x2_bits(v[0], v[1]);
-        if (a.lse && tid == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
+    for (int e = 0; e < 2; ++e) {
+        const int d = 2 * tid + e;
+        v[e] = ((o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d])) * r;
     }
+    reinterpret_cast<uint32_t *>(a.O + at * D)[tid] = bf16x2_bits(v[0], v[1]);
+    if (a.lse && tid == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
 // ---- many queries ----------------------------------------------------------

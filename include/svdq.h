@@ -118,7 +118,7 @@ typedef enum svdq_qformat {
 #define SVDQ_ROPE_MAX_AXES 4
 #define SVDQ_ROPE_MAX_PAIRS 256
 #define SVDQ_KV8_PAGE 64
-#define SVDQ_KV8_MAX_SPLITS 128
+#define SVDQ_KV8_MAX_SPLITS 64
 
 /* Text of a status code (static storage; never NULL). */
 const char *svdq_status_string(int status);
