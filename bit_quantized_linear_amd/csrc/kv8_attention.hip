@@ -319,20 +319,25 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
     }
 }
 
-// The splits' sums of one query joined, by the waves of a block each a part. What is
-// read does not depend on what is read before, so that one wait covers all.
-template <int D>
+// The parts' sums of a query joined: by a wave, where it has at most 8 parts, or by
+// the W waves of a block. What is read does not depend on what is read before, so
+// that one wait covers all.
+constexpr int kJoinAlone = 8;
+
+template <int D, int W>
 __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
-    constexpr int E = D / 64, kEach = SVDQ_KV8_MAX_SPLITS / 4;
-    __shared__ float o_s[4][D];
-    const int64_t at = (int64_t)blockIdx.x * a.Hq + blockIdx.y;
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int E = D / 64, kEach = W == 1 ? kJoinAlone : SVDQ_KV8_MAX_SPLITS / W;
+    __shared__ float o_s[W == 1 ? 1 : W][D];
+    const int lane = threadIdx.x & 63, wave = W == 1 ? 0 : threadIdx.x >> 6;
+    const int64_t at = W == 1 ? 4 * (int64_t)blockIdx.x + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+    if (at >= (int64_t)a.kv.T * a.Hq) return;
+    const int row = (int)(at / a.Hq);
     const float *src = a.part + at * a.splits * D + lane * E;
     float x[kEach][E];
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[i][e] = 4 * i + wave < a.splits ? src[(int64_t)(4 * i + wave) * D + e] : 0.0f;
+        for (int e = 0; e < E; ++e) x[i][e] = W * i + wave < a.splits ? src[(int64_t)(W * i + wave) * D + e] : 0.0f;
     const float *ml = a.part + (int64_t)a.kv.T * a.Hq * a.splits * D + at * a.splits * 2;
     const float m = lane < a.splits ? ml[2 * lane] : -INFINITY, l = lane < a.splits ? ml[2 * lane + 1] : 0.0f;
     const int first = min(max(a.kv.starts[0], 0), a.kv.T);
@@ -350,23 +355,30 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const float w = __shfl(weight, (4 * i + wave) & 63);
+        const float w = __shfl(weight, (W * i + wave) & 63);
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(w, x[i][e], acc[e]);
     }
+    if constexpr (W > 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) o_s[wave][lane * E + e] = acc[e];
-    __syncthreads();
-    if (row < first || row >= last || tid >= D / 2) return;
-    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-    float v[2];
+        for (int e = 0; e < E; ++e) o_s[wave][lane * E + e] = acc[e];
+        __syncthreads();
+        if (wave > 0) return;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int d = 2 * tid + e;
-        v[e] = ((o_s[0][d] + o_s[1][d]) + (o_s[2][d] + o_s[3][d])) * r;
+        for (int e = 0; e < E; ++e) {
+            acc[e] = o_s[0][lane * E + e];
+#pragma unroll
+            for (int w = 1; w < W; ++w) acc[e] += o_s[w][lane * E + e];
+        }
     }
-    reinterpret_cast<uint32_t *>(a.O + at * D)[tid] = bf16x2_bits(v[0], v[1]);
-    if (a.lse && tid == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
+    if (row < first || row >= last) return;
+    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *out = a.O + at * D + lane * E;
+    if constexpr (E == 2)
+        *reinterpret_cast<uint32_t *>(out) = bf16x2_bits(acc[0] * r, acc[1] * r);
+    else
+        *out = (uint16_t)bf16x2_bits(acc[0] * r, 0.0f);
+    if (a.lse && lane == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
 // ---- many queries ----------------------------------------------------------
@@ -751,7 +763,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
         load_info(s0, s1);
         meet();
         // Page p is in k_s[kc], v_s[vc], its factor is c and `plain` says what it is; page p + 1 is held
-        int kc = 0, vc = 0, vp = 2;
+        int kc = 0, vc = 0;
         const auto after = [&](int v) { return v == 2 ? 0 : v + 1; };
         const auto info_at = [&](int p) { return min(p, s1 - 1) - info0; };
         fetch(info_s[0]);
@@ -838,45 +850,77 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
     if (a.lse && h == 0) a.lse[at] = (base + log2f(l)) * kLn2;
 }
 
-// Few queries per sequence and key head on average: the kernel that splits pages.
-bool few_queries(int T, int B, int group) { return (int64_t)T * group <= (int64_t)kDecRows * B; }
+// Parts of a sequence's pages: as many as give each compute unit a block.
+constexpr int kCus = 256;
+constexpr int kAlonePages = 16, kDeepPages = 128;
+constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
 
-// Blocks that share a sequence's pages: as many as give the chip four blocks per
-// compute unit, a page for each wave at the least.
-int split_count(int B, int Hk, int max_pages) {
-    const int64_t want = (1024 + (int64_t)B * Hk - 1) / ((int64_t)B * Hk);
-    const int64_t most = (max_pages + kDecWaves - 1) / kDecWaves;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, SVDQ_KV8_MAX_SPLITS}));
+// How a call is cut: which kernel, its queries per block (`rows`), the blocks of a
+// head (`tiles`, prompts) and the parts of a sequence's pages.
+struct AttnPlan {
+    bool few;
+    int rows, tiles, splits;
+};
+
+AttnPlan attn_plan(int T, int B, int max_pages, int Hk, int group) {
+    AttnPlan p;
+    const int64_t queries = (int64_t)T * group;
+    p.few = queries <= (int64_t)kDecRows * B;
+    p.rows = p.few ? kDecRows : queries <= 128 * (int64_t)B ? 128 : 256;
+    p.tiles = p.few ? B : (int)((queries + (int64_t)(p.rows - 1) * B) / p.rows);
+    p.splits = 1;
+    const int fill = (int)std::min<int64_t>(SVDQ_KV8_MAX_SPLITS, kCus / ((int64_t)p.tiles * Hk));
+    if (p.few) {
+        if (max_pages > kAlonePages) {
+            const int deep = std::min((max_pages + kDeepPages - 1) / kDeepPages, SVDQ_KV8_MAX_SPLITS);
+            p.splits = std::max(1, std::min(std::max(fill, deep), (max_pages + kDecWaves - 1) / kDecWaves));
+        }
+    } else {
+        float best = kPageTime * max_pages;
+        for (int s = 2; s <= fill && s <= max_pages; ++s) {
+            const float time = kPageTime * ((max_pages + s - 1) / s) + kJoinTime + kPartTime * (float)queries * Hk * s;
+            if (time < best) {
+                best = time;
+                p.splits = s;
+            }
+        }
+    }
+    return p;
 }
 
 }  // namespace
 
 size_t kv8_attention_workspace(int T, int B, int max_pages, int Hq, int Hk, int D) {
-    if (T == 0 || B == 0 || !few_queries(T, B, Hq / Hk)) return 0;
-    const int splits = split_count(B, Hk, max_pages);
+    if (T == 0 || B == 0) return 0;
+    const int splits = attn_plan(T, B, max_pages, Hk, Hq / Hk).splits;
     return splits == 1 ? 0 : (size_t)T * Hq * splits * (D + 2) * sizeof(float);
 }
 
 hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_stride, const uint8_t *kc,
                                 const float *ks, const uint8_t *vc, const float *vs, int Hq, int Hk, int D, float scale,
                                 bool causal, int window, uint16_t *O, float *lse, void *workspace, hipStream_t stream) {
-    AttnArgs a{kv, Q,  q_stride, kc,  vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal, window,
-               O,  lse, static_cast<float *>(workspace), 1};
-    if (few_queries(kv.T, kv.B, a.group)) {
-        a.splits = split_count(kv.B, Hk, kv.max_pages);
+    const AttnPlan plan = attn_plan(kv.T, kv.B, kv.max_pages, Hk, Hq / Hk);
+    const AttnArgs a{kv, Q,  q_stride, kc,  vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal, window,
+                     O,  lse, static_cast<float *>(workspace), plan.splits};
+    if (plan.few)
         hipLaunchKernelGGL(D == 64 ? kv8_decode_kernel<64> : kv8_decode_kernel<128>,
-                           dim3((unsigned)a.splits, (unsigned)Hk, (unsigned)kv.B), dim3(64 * kDecWaves), 0, stream, a);
-        if (a.splits == 1) return hipGetLastError();
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(D == 64 ? kv8_join_kernel<64> : kv8_join_kernel<128>, dim3((unsigned)kv.T, (unsigned)Hq),
+                           dim3((unsigned)plan.splits, (unsigned)Hk, (unsigned)kv.B), dim3(64 * kDecWaves), 0, stream, a);
+    else if (plan.rows == 128)
+        hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 4> : kv8_prompt_kernel<128, 4>),
+                           dim3((unsigned)(plan.tiles * Hk), (unsigned)plan.splits), dim3(256), 0, stream, a, plan.tiles);
+    else
+        hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 8> : kv8_prompt_kernel<128, 8>),
+                           dim3((unsigned)(plan.tiles * Hk), (unsigned)plan.splits), dim3(512), 0, stream, a, plan.tiles);
+    if (plan.splits == 1) return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t queries = (int64_t)kv.T * Hq;
+    if (plan.splits <= kJoinAlone)
+        hipLaunchKernelGGL((D == 64 ? kv8_join_kernel<64, 1> : kv8_join_kernel<128, 1>), dim3((unsigned)((queries + 3) / 4)),
                            dim3(256), 0, stream, a);
-        return hipGetLastError();
-    }
-    const auto tiles = [&](int rows) { return (int)(((int64_t)kv.T * a.group + (int64_t)(rows - 1) * kv.B) / rows); };
-    const int n = tiles(256);
-    hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 8> : kv8_prompt_kernel<128, 8>), dim3((unsigned)(n * Hk)),
-                       dim3(512), 0, stream, a, n);
+    else
+        hipLaunchKernelGGL((D == 64 ? kv8_join_kernel<64, 4> : kv8_join_kernel<128, 4>), dim3((unsigned)queries), dim3(256),
+                           0, stream, a);
     return hipGetLastError();
 }
 
