@@ -645,6 +645,27 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
     _check("svdq_fp8_moe_layer", st)
 
 
+def _ptr(t, nbytes, name, dev, formats):
+    """As _dev_ptr, for the entry points with many tensors: one look at each of a
+    tensor's properties, and the reasons only where one is not as it must be."""
+    if t is None:
+        return None
+    if t.dtype in formats and t.get_device() == dev and t.is_contiguous() and t.nbytes >= nbytes:
+        return t.data_ptr()
+    return _dev_ptr(t, t.element_size(), nbytes, name, dev, formats)
+
+
+def _shaped_ptr(t, shape, name, dev, formats):
+    """The same for a tensor that has exactly the shape."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} is {list(t.shape)}, the call takes {list(shape)}")
+    if t.dtype in formats and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _dev_ptr(t, t.element_size(), 0, name, dev, formats)
+
+
 def svdq_fp8_norm_quantize(X, residual, weight, eps, total, Y, qx, sx, stream=None):
     """Root-mean-square norm of X [M, K] (+ residual), bf16, with weights [K]:
     total = the sum (bf16; may be residual or X itself), Y = the norm in bf16, qx
@@ -656,10 +677,9 @@ def svdq_fp8_norm_quantize(X, residual, weight, eps, total, Y, qx, sx, stream=No
     e4m3, bf16, f32, _ = _fp8_formats()
     n = M * K * 2
     st = lib().svdq_fp8_norm_quantize(
-        _dev_ptr(X, 2, n, "X", dev, bf16), _dev_ptr(residual, 2, n, "residual", dev, bf16),
-        _dev_ptr(weight, 2, K * 2, "weight", dev, bf16), eps, M, K, _dev_ptr(total, 2, n, "total", dev, bf16),
-        _dev_ptr(Y, 2, n, "Y", dev, bf16), _dev_ptr(qx, 1, M * K, "qx", dev, e4m3),
-        _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev, f32), _stream(stream))
+        _ptr(X, n, "X", dev, bf16), _ptr(residual, n, "residual", dev, bf16), _ptr(weight, K * 2, "weight", dev, bf16),
+        eps, M, K, _ptr(total, n, "total", dev, bf16), _ptr(Y, n, "Y", dev, bf16), _ptr(qx, M * K, "qx", dev, e4m3),
+        None if sx is None else _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev, f32), _stream(stream))
     _check("svdq_fp8_norm_quantize", st)
 
 
@@ -671,36 +691,18 @@ def _dev_heads(t, name, dev, bf16):
     if t.dtype not in bf16:
         raise TypeError(f"{name}: {t.dtype}, the call takes {', '.join(sorted(map(str, bf16)))}")
     index = t.get_device()
-    if index < 0:
-        raise TypeError(f"{name}: device entry points take GPU tensors")
     if index != dev:
+        if index < 0:
+            raise TypeError(f"{name}: device entry points take GPU tensors")
         raise TypeError(f"{name} is on cuda:{index}, the current device is cuda:{dev}")
-    T, H, D = t.shape
+    T, H, D = shape = t.shape
     row, head, one = t.stride()
-    if T <= 1 or H * D == 0:  # there is no next row
-        row = max(H * D, -(-H * D // 8) * 8)
-    if (D > 1 and one != 1) or (H > 1 and head != D) or row < H * D:
+    width = H * D
+    if T <= 1 or width == 0:  # there is no next row
+        row = -(-width // 8) * 8
+    if row < width or (one != 1 and D > 1) or (head != D and H > 1):
         raise TypeError(f"{name}: the heads of a token must be contiguous, and tokens apart")
-    return t.data_ptr(), row, T, H, D
-
-
-def svdq_rope(X, positions, freqs, sections, Y, interleaved=False, stream=None):
-    """Y = X [T, H, D] (bf16, rows may be parts of wider ones) turned by rotary
-    positions: positions [T, axes] int32, freqs [R / 2] fp64, sections: the pairs of
-    each axis, R / 2 in all. Y may be X."""
-    dev = _current_device()
-    _, bf16, _, i32 = _fp8_formats()
-    xp, xs, T, H, D = _dev_heads(X, "X", dev, bf16)
-    yp, ys, *shape = _dev_heads(Y, "Y", dev, bf16)
-    if shape != [T, H, D]:
-        raise ValueError(f"Y is {shape}, the call writes {[T, H, D]}")
-    axes = len(sections)
-    if positions is None or positions.dim() != 2 or tuple(positions.shape) != (T, axes):
-        raise ValueError(f"positions must be [{T}, {axes}]")
-    st = lib().svdq_rope(xp, xs, _dev_ptr(positions, 4, T * axes * 4, "positions", dev, i32),
-                         _dev_ptr(freqs, 8, 8 * sum(sections), "freqs", dev, _f64_format()), (_i * axes)(*sections),
-                         axes, 1 if interleaved else 0, T, H, D, yp, ys, _stream(stream))
-    _check("svdq_rope", st)
+    return t.data_ptr(), row, shape
 
 
 _f64_types = None
@@ -715,25 +717,40 @@ def _f64_format():
     return _f64_types
 
 
+def svdq_rope(X, positions, freqs, sections, Y, interleaved=False, stream=None):
+    """Y = X [T, H, D] (bf16, rows may be parts of wider ones) turned by rotary
+    positions: positions [T, axes] int32, freqs [R / 2] fp64, sections: the pairs of
+    each axis, R / 2 in all. Y may be X."""
+    dev = _current_device()
+    _, bf16, _, i32 = _fp8_formats()
+    xp, xs, shape = _dev_heads(X, "X", dev, bf16)
+    yp, ys, out = _dev_heads(Y, "Y", dev, bf16)
+    if out != shape:
+        raise ValueError(f"Y is {list(out)}, the call writes {list(shape)}")
+    T, H, D = shape
+    axes = len(sections)
+    if positions is None:
+        raise TypeError(f"positions must be a tensor [{T}, {axes}]")
+    st = lib().svdq_rope(xp, xs, _shaped_ptr(positions, (T, axes), "positions", dev, i32),
+                         _ptr(freqs, 8 * sum(sections), "freqs", dev, _f64_format()), (_i * axes)(*sections), axes,
+                         1 if interleaved else 0, T, H, D, yp, ys, _stream(stream))
+    _check("svdq_rope", st)
+
+
 def _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32):
     """Checked pointers of the 8-bit cache, and its number of pages."""
-    if kc is None or kc.dim() != 4 or vc is None or vc.dim() != 4 or ks is None or vs is None:
-        raise TypeError("kc and vc must be 4-D tensors, ks and vs the scales")
-    P = int(kc.shape[0])
-    if tuple(kc.shape[1:]) != (Hk, KV8_PAGE, D) or tuple(vc.shape) != (P, Hk, D, KV8_PAGE):
-        raise ValueError(f"kc {list(kc.shape)} and vc {list(vc.shape)} do not fit {Hk} heads of {D}: "
-                         f"[pages, {Hk}, {KV8_PAGE}, {D}] and [pages, {Hk}, {D}, {KV8_PAGE}]")
-    n = P * Hk * KV8_PAGE * D
-    return P, (_dev_ptr(kc, 1, n, "kc", dev, e4m3), _fp8_scales(ks, (P, Hk), "ks", dev, f32),
-               _dev_ptr(vc, 1, n, "vc", dev, e4m3), _fp8_scales(vs, (P, Hk), "vs", dev, f32))
+    if kc is None or vc is None or ks is None or vs is None or kc.dim() != 4:
+        raise TypeError("kc and vc must be 4-D tensors, ks and vs their scales")
+    P = kc.shape[0]
+    return P, (_shaped_ptr(kc, (P, Hk, KV8_PAGE, D), "kc", dev, e4m3), _shaped_ptr(ks, (P, Hk), "ks", dev, f32),
+               _shaped_ptr(vc, (P, Hk, D, KV8_PAGE), "vc", dev, e4m3), _shaped_ptr(vs, (P, Hk), "vs", dev, f32))
 
 
 def _kv8_batch(starts, lengths, table, dev, i32):
     """Checked pointers of a batch, its sequences and the table's width."""
     B, max_pages = _shape2(table, "table")
-    return B, max_pages, (_dev_ptr(starts, 4, 4 * (B + 1), "starts", dev, i32),
-                          _dev_ptr(lengths, 4, 4 * B, "lengths", dev, i32),
-                          _dev_ptr(table, 4, 4 * B * max_pages, "table", dev, i32))
+    return B, max_pages, (_ptr(starts, 4 * (B + 1), "starts", dev, i32), _ptr(lengths, 4 * B, "lengths", dev, i32),
+                          _ptr(table, 0, "table", dev, i32))
 
 
 def svdq_kv8_append(K, V, starts, lengths, table, kc, ks, vc, vs, stream=None):
@@ -743,10 +760,11 @@ def svdq_kv8_append(K, V, starts, lengths, table, kc, ks, vc, vs, stream=None):
     which rows are whose and where they go."""
     dev = _current_device()
     e4m3, bf16, f32, i32 = _fp8_formats()
-    kp, kst, T, Hk, D = _dev_heads(K, "K", dev, bf16)
-    vp, vst, *shape = _dev_heads(V, "V", dev, bf16)
-    if shape != [T, Hk, D]:
-        raise ValueError(f"V is {shape}, K {[T, Hk, D]}")
+    kp, kst, shape = _dev_heads(K, "K", dev, bf16)
+    vp, vst, other = _dev_heads(V, "V", dev, bf16)
+    if other != shape:
+        raise ValueError(f"V is {list(other)}, K {list(shape)}")
+    T, Hk, D = shape
     B, max_pages, batch = _kv8_batch(starts, lengths, table, dev, i32)
     P, cache = _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32)
     st = lib().svdq_kv8_append(kp, kst, vp, vst, *batch, T, B, max_pages, P, Hk, D, *cache, _stream(stream))
@@ -761,21 +779,19 @@ def svdq_kv8_attention(Q, kc, ks, vc, vs, starts, lengths, table, scale, O, lse=
                        causal=True, window=0, stream=None):
     """O [T, Hq, D] bf16 = attention of the newest tokens' queries Q [T, Hq, D] (bf16,
     rows may be parts of wider ones) over the 8-bit cache; lse [T, Hq] fp32 takes
-    the logarithms of the weights' sums. The rest as svdq_kv8_append."""
+    the logarithms of the weights' sums. The library refuses a workspace (any
+    contiguous GPU tensor) of too few bytes. The rest as svdq_kv8_append."""
     dev = _current_device()
     e4m3, bf16, f32, i32 = _fp8_formats()
-    qp, qst, T, Hq, D = _dev_heads(Q, "Q", dev, bf16)
-    Hk = int(kc.shape[1]) if kc is not None and kc.dim() == 4 else 0
+    qp, qst, shape = _dev_heads(Q, "Q", dev, bf16)
+    T, Hq, D = shape
+    Hk = kc.shape[1] if kc is not None and kc.dim() == 4 else 0
     P, cache = _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32)
     B, max_pages, batch = _kv8_batch(starts, lengths, table, dev, i32)
-    if lse is not None and tuple(lse.shape) != (T, Hq):
-        raise ValueError(f"lse is {list(lse.shape)}, the call writes {[T, Hq]}")
-    need = svdq_kv8_attention_workspace_bytes(T, B, max_pages, Hq, Hk, D)
-    st = lib().svdq_kv8_attention(qp, qst, *cache, *batch, T, B, max_pages, P, Hq, Hk, D, scale, 1 if causal else 0,
-                                  window, _dev_ptr(O, 2, T * Hq * D * 2, "O", dev, bf16),
-                                  _dev_ptr(lse, 4, T * Hq * 4, "lse", dev, f32),
-                                  _dev_ptr(workspace, None, need, "workspace", dev), 0 if workspace is None else need,
-                                  _stream(stream))
+    wp, wb = _ws(workspace, dev)
+    st = lib().svdq_kv8_attention(qp, qst, *cache, *batch, T, B, max_pages, P, Hq, Hk, D, scale, 1 if causal else 0, window,
+                                  _ptr(O, T * Hq * D * 2, "O", dev, bf16), _shaped_ptr(lse, (T, Hq), "lse", dev, f32), wp,
+                                  wb, _stream(stream))
     _check("svdq_kv8_attention", st)
 
 

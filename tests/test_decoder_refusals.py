@@ -64,8 +64,8 @@ def attention(Q=FAKE, qs=256, cache=(FAKE,) * 4, starts=FAKE, lengths=FAKE, tabl
     (attention, {"scale": NAN}, INVALID), (attention, {"scale": INF}, INVALID), (attention, {"scale": -1.0}, INVALID),
     (attention, {"window": -1}, INVALID), (attention, {"window": 4, "causal": 0}, INVALID),
     (attention, {"T": (1 << 24) - 1, "Hq": 65, "Hk": 65, "qs": 4160}, SHAPE), (attention, {"Q": None}, INVALID),
-    (attention, {"O": None}, INVALID), (attention, {"lengths": None}, INVALID), (attention, {"ws": None}, INVALID),
-    (attention, {"wb": 64}, INVALID), (attention, {"lse": MISALIGNED}, MIS), (attention, {"table": MISALIGNED}, MIS),
+    (attention, {"O": None}, INVALID), (attention, {"lengths": None}, INVALID), (attention, {"ws": None, "pages": 512}, INVALID),
+    (attention, {"wb": 64, "pages": 512}, INVALID), (attention, {"lse": MISALIGNED}, MIS), (attention, {"table": MISALIGNED}, MIS),
 ], ids=str)
 def test_refused_before_a_launch(call, args, status):
     assert call(**args) == status
@@ -123,6 +123,10 @@ class Dev:
 
     def element_size(self):
         return self.dtype.itemsize
+
+    @property
+    def nbytes(self):
+        return self.numel() * self.element_size()
 
     def is_contiguous(self):
         return self._plain
@@ -192,7 +196,7 @@ def test_well_formed_arguments_reach_the_library(call, guarded):
 def test_a_tensor_too_small_or_elsewhere_or_of_another_type_is_refused(call, name, guarded):
     shape, dtype = CALLS[call][1][name]
     other = {BF: torch.float16, F32: BF, F64: F32, I32: torch.int64, E4: torch.float8_e5m2, torch.uint8: None}[dtype]
-    if name not in ("X", "K", "Q", "table"):  # what gives the call its sizes
+    if name not in ("X", "K", "Q", "table", "workspace"):  # what gives the call its sizes
         with pytest.raises(ValueError):
             CALLS[call][0](tensors(call, **{name: Dev(shape[:-1] + (shape[-1] - 1,), dtype)}))
     with pytest.raises(TypeError):
