@@ -69,44 +69,58 @@ __device__ __forceinline__ uint32_t top_finite(u32x4 v) {
     return top;
 }
 
-// One page and head, keys or values (blockIdx.y % 2). A thread has 4 tokens x 8
-// features: for values their codes are 8 pieces of 4 tokens, as a page holds them.
+// One page and head, keys or values (blockIdx.y % 2). A thread has 8 features of 4
+// tokens. Of keys, neighbouring threads have neighbouring features, so that rows are
+// read and written whole; of values, neighbouring tokens, whose codes are 8 pieces
+// of 4 tokens as a page holds them. The tokens are under way while the page's
+// number, then its scale and the codes that share a piece with new ones are.
 __global__ __launch_bounds__(kAppThreads) void kv8_append_kernel(AppendArgs a) {
     __shared__ uint32_t tops[kAppThreads / 64];
     const int head = blockIdx.y >> 1;
     const bool values = blockIdx.y & 1;
     int b, nth;
-    if (!kv_find(a.kv, blockIdx.x, b, nth, [](const KvSeq &s) {
+    KvSeq seq;
+    if (!kv_find(a.kv, blockIdx.x, b, seq, nth, [](const KvSeq &s) {
             const int first = max(0, s.length - s.rows);
             return s.rows > 0 && s.length > 0 ? (s.length - 1) / kKvPage - first / kKvPage + 1 : 0;
         }))
         return;
-    const KvSeq seq = kv_seq(a.kv, b);
     const int first = max(0, seq.length - seq.rows);
     const int p = first / kKvPage + nth;
-    const int page = kv_page(a.kv, b, p);
-    if (page < 0) return;
     // new tokens low .. high - 1 of the page; token t is row row0 + t
     const int low = max(first - p * kKvPage, 0), high = min(seq.length - p * kKvPage, kKvPage);
     const int64_t row0 = seq.row0 + seq.rows - seq.length + (int64_t)p * kKvPage;
     const int64_t stride = values ? a.v_stride : a.k_stride;
     const uint16_t *x = (values ? a.V : a.K) + (int64_t)head * a.D;
+
+    const int per = a.D / 8;  // threads of a row of keys
+    const int token = values ? 4 * (threadIdx.x & 15) : threadIdx.x / per, step = values ? 1 : kAppThreads / per;
+    const int f = values ? (threadIdx.x >> 4) * 8 : threadIdx.x % per * 8;
+    const bool mine = f < a.D;
+    u32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = token + i * step;
+        v[i] = u32x4{0u, 0u, 0u, 0u};
+        if (mine && t >= low && t < high) v[i] = *reinterpret_cast<const u32x4 *>(x + (row0 + t) * stride + f);
+    }
+    const int page = kv_page(a.kv, b, p);
+    if (page < 0) return;
     const int64_t unit = (int64_t)page * a.Hk + head;
     uint8_t *codes = (values ? a.vc : a.kc) + unit * kKvPage * a.D;
     float *scale = (values ? a.vs : a.ks) + unit;
     const float old = *scale;
-
-    const int q = threadIdx.x & 15, f = (threadIdx.x >> 4) * 8;  // tokens 4 q .. 4 q + 3, features f .. f + 7
-    const bool mine = f < a.D;
-    u32x4 v[4];
+    // of values: bytes of the new tokens among the thread's 4, and the codes there if others share their pieces
+    uint32_t fresh = 0, was[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fresh |= token + i >= low && token + i < high ? 0xFFu << (8 * i) : 0u;
+    const bool shared = values && mine && fresh != 0u && fresh != 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        was[j] = shared ? *reinterpret_cast<const uint32_t *>(codes + (f + j) * kKvPage + token) : 0u;
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 4 * q + i;
-        v[i] = u32x4{0u, 0u, 0u, 0u};
-        if (mine && t >= low && t < high) v[i] = *reinterpret_cast<const u32x4 *>(x + (row0 + t) * stride + f);
-        top = max(top, top_finite(v[i]));
-    }
+    for (int i = 0; i < 4; ++i) top = max(top, top_finite(v[i]));
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
     if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
@@ -123,7 +137,7 @@ __global__ __launch_bounds__(kAppThreads) void kv8_append_kernel(AppendArgs a) {
     if (!values) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = 4 * q + i;
+            const int t = token + i * step;
             u32x2 *at = reinterpret_cast<u32x2 *>(codes + t * a.D + f);
             if (t >= low && t < high) {
                 u32x2 w;
@@ -141,25 +155,23 @@ __global__ __launch_bounds__(kAppThreads) void kv8_append_kernel(AppendArgs a) {
         }
         return;
     }
-    // bytes of the new and of the earlier ones among the 4 tokens
-    uint32_t fresh = 0, before = 0;
+    uint32_t before = 0;  // bytes of earlier tokens, to be rounded to a larger scale
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 4 * q + i;
-        if (t >= low && t < high) fresh |= 0xFFu << (8 * i);
-        if (shrink && t < low) before |= 0xFFu << (8 * i);
-    }
+    for (int i = 0; i < 4; ++i) before |= shrink && token + i < low ? 0xFFu << (8 * i) : 0u;
     if (!(fresh | before)) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        uint32_t *at = reinterpret_cast<uint32_t *>(codes + (f + j) * kKvPage + 4 * q);
+        uint32_t *at = reinterpret_cast<uint32_t *>(codes + (f + j) * kKvPage + token);
+        if (!fresh) {
+            *at = rescale4(*at, ratio);
+            continue;
+        }
         const int sh = 16 * (j & 1);
         uint32_t w = codes4(kv_value(v[0][j / 2] >> sh & 0xFFFFu) * r, kv_value(v[1][j / 2] >> sh & 0xFFFFu) * r,
                             kv_value(v[2][j / 2] >> sh & 0xFFFFu) * r, kv_value(v[3][j / 2] >> sh & 0xFFFFu) * r);
-        if (fresh != 0xFFFFFFFFu) {
-            const uint32_t was = *at;
-            w = (w & fresh) | (was & ~(fresh | before));
-            if (before) w |= rescale4(was, ratio) & before;
+        if (shared) {
+            w = (w & fresh) | (was[j] & ~(fresh | before));
+            if (before) w |= rescale4(was[j], ratio) & before;
         }
         *at = w;
     }

@@ -457,11 +457,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
         }
     }
     int b, tile;
-    if (!kv_find(a.kv, item, b, tile, [=](const KvSeq &s) { return (s.rows * group + kRows - 1) / kRows; })) return;
-    b = __builtin_amdgcn_readfirstlane(b);
-    const KvSeq seq = kv_seq(a.kv, b);
+    KvSeq seq;
+    if (!kv_find(a.kv, item, b, seq, tile, [=](const KvSeq &s) { return (s.rows * group + kRows - 1) / kRows; })) return;
     const int rows = seq.rows * group;
-    tile = (rows + kRows - 1) / kRows - 1 - __builtin_amdgcn_readfirstlane(tile);  // the longest first
+    tile = (rows + kRows - 1) / kRows - 1 - tile;  // the longest first
     const int r0 = tile * kRows, last = min(r0 + kRows, rows) - 1;
     const int row = min(r0 + 32 * wave + q32, last);
     int low, high, low0, high0, low1, high1;

@@ -35,13 +35,14 @@ __device__ __forceinline__ int kv_page(const KvBatch &kv, int b, int p) {
 }
 
 // Work item `item` of a batch whose sequence b has count(sequence) of them: the
-// sequence in b and the number within it, or false past the last. A wave looks
-// at 64 sequences at a time; every lane takes part and has the same answer.
+// sequence, in b and seq, and the number within it, or false past the last. A wave
+// looks at 64 sequences at a time; every lane takes part and has the same answer.
 template <class Count>
-__device__ __forceinline__ bool kv_find(const KvBatch &kv, int item, int &b, int &within, Count count) {
+__device__ __forceinline__ bool kv_find(const KvBatch &kv, int item, int &b, KvSeq &seq, int &within, Count count) {
     const int lane = threadIdx.x & 63;
     for (int b0 = 0; b0 < kv.B; b0 += 64) {
-        int n = b0 + lane < kv.B ? count(kv_seq(kv, b0 + lane)) : 0;
+        const KvSeq mine = kv_seq(kv, min(b0 + lane, kv.B - 1));
+        const int n = b0 + lane < kv.B ? count(mine) : 0;
         int upto = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -52,10 +53,13 @@ __device__ __forceinline__ bool kv_find(const KvBatch &kv, int item, int &b, int
         if (past) {
             const int at = __ffsll((unsigned long long)past) - 1;
             b = b0 + at;
-            within = item - __shfl(upto - n, at);
+            seq.row0 = __builtin_amdgcn_readlane(mine.row0, at);
+            seq.rows = __builtin_amdgcn_readlane(mine.rows, at);
+            seq.length = __builtin_amdgcn_readlane(mine.length, at);
+            within = item - __builtin_amdgcn_readlane(upto - n, at);
             return true;
         }
-        item -= __shfl(upto, 63);
+        item -= __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
