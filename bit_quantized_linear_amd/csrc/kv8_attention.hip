@@ -637,7 +637,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
     auto step = [&](auto kStage, int ki, int vi, int next, const float (&s)[16], float c, bf16x8 (&w)[2], int kn, int hn,
                     float (&sn)[16], float &top, int vp, int hp, const bf16x8 (&wp)[2], int ka,
                     int ha) __attribute__((always_inline)) {
-        float sum[2] = {0.0f, 0.0f}, most = -INFINITY;
+        float x[16], sum[2] = {0.0f, 0.0f}, most = -INFINITY;
         uint32_t packed[2][4];
         f32x16 acc;
         zero(acc);
@@ -646,12 +646,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
         for (int n = 0; n < kParts; ++n) {
             __builtin_amdgcn_sched_barrier(0);
             if (kStage && n == kParts - kAhead) meet();
-            const bf16x8 x = operand[n % kRing];
             const int v = n - KS;
             if (n < KS)
-                acc = mfma_bf16_32x32x16(x, q[n], acc);
+                acc = mfma_bf16_32x32x16(operand[n % kRing], q[n], acc);
             else
-                o[v % DT] = mfma_bf16_32x32x16(x, wp[v / DT], o[v % DT]);
+                o[v % DT] = mfma_bf16_32x32x16(operand[n % kRing], wp[v / DT], o[v % DT]);
             const int r = n + kAhead, rv = r - KS;
             operand[r % kRing] = r < KS       ? key(kn, hn, r)
                                  : r < kParts ? value(vp, hp, rv / DT, rv % DT)
@@ -662,16 +661,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
                 for (int i = n * 2 * PC / KS; i < (n + 1) * 2 * PC / KS; ++i) store_piece(i, ki, vi);
             }
             if (kStage && n == KS) fetch(info);
-            // this part's share of the 8 pairs of weights
+            // this part's share of the 16 weights
 #pragma unroll
-            for (int j = n * 8 / kParts; j < (n + 1) * 8 / kParts; ++j) {
-                const int e = 2 * j;
-                const float x0 = exp2_of(__builtin_fmaf(s[e], c, -base));
-                const float x1 = exp2_of(__builtin_fmaf(s[e + 1], c, -base));
-                sum[0] += x0;
-                sum[1] += x1;
-                packed[j / 4][j % 4] = bf16x2_bits(x0, x1);
-                asm volatile("" : "+v"(packed[j / 4][j % 4]), "+v"(sum[0]), "+v"(sum[1]));  // here, not later
+            for (int e = n * 16 / kParts; e < (n + 1) * 16 / kParts; ++e) {
+                x[e] = exp2_of(__builtin_fmaf(s[e], c, -base));
+                sum[e & 1] += x[e];
+                asm volatile("" : "+v"(x[e]), "+v"(sum[e & 1]));  // here, not later
+                if (e & 1) {
+                    packed[e / 8][e % 8 / 2] = bf16x2_bits(x[e - 1], x[e]);
+                    asm volatile("" : "+v"(packed[e / 8][e % 8 / 2]));
+                }
             }
             // and, from the second part behind the scores on, of the largest scores
             if (n > KS) {
@@ -698,49 +697,61 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
         uint32_t slow = 0;
 #pragma unroll
         for (int i = 0; i < NW; ++i) slow |= nan_s[vi][i];
-        for (int half = 0; c > 0.0f && half < 2; ++half) {
-            // the tokens that the lane's query sees, counted as its elements are: count of them, from `from` on
-            const int at = p * kKvPage + 32 * half + 8 * h, from = low - at;
-            const uint32_t count = (uint32_t)max(high - low, 0);
-            auto sees = [&](int e) { return (uint32_t)(16 * (e >> 3) + (e & 7) - from) < count; };
-            f32x16 s;
-            zero(s);
+        if (!(c > 0.0f)) return;
+        // the tokens that the lane's query sees, counted as its elements are: count of them, from `from` on
+        const int from = low - p * kKvPage - 8 * h;
+        const uint32_t count = (uint32_t)max(high - low, 0);
+        auto sees = [&](int half, int e) { return (uint32_t)(32 * half + 16 * (e >> 3) + (e & 7) - from) < count; };
+        f32x16 s[2];
+        zero(s[0]);
+        zero(s[1]);
 #pragma unroll
-            for (int i = 0; i < KS; ++i) s = mfma_bf16_32x32x16(key(ki, half, i), q[i], s);
+        for (int i = 0; i < KS; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
-            const float top = top_of(s) * c;
-            if (__any(top > base + kRise)) raise_to(top);
-            bf16x8 w[2];
+            for (int half = 0; half < 2; ++half) s[half] = mfma_bf16_32x32x16(key(ki, half, i), q[i], s[half]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[half][e] = sees(half, e) ? s[half][e] : -INFINITY;
+        const float top = fmaxf(top_of(s[0]), top_of(s[1])) * c;
+        if (__any(top > base + kRise)) raise_to(top);
+        bf16x8 w[2][2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[e] = exp2_of(__builtin_fmaf(s[8 * u + e], c, -base));
+                    x[e] = exp2_of(__builtin_fmaf(s[half][8 * u + e], c, -base));
                     l += x[e];
                 }
-                w[u] = pack8(x, 1.0f);
+                w[half][u] = pack8(x, 1.0f);
             }
-            if (!slow) {
+        if (!slow) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < DT; ++i) o[i] = mfma_bf16_32x32x16(value(vi, half, u, i), w[u], o[i]);
-                continue;
-            }
-            // NaN reaches the queries that see its token, and no other
+                    for (int i = 0; i < DT; ++i) o[i] = mfma_bf16_32x32x16(value(vi, half, u, i), w[half][u], o[i]);
+            return;
+        }
+        // NaN reaches the queries that see its token, and no other
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
             bf16x8 seen[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 u32x4 see;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    see[e] = (sees(8 * u + 2 * e) ? 0x3F80u : 0u) | (sees(8 * u + 2 * e + 1) ? 0x3F800000u : 0u);
+                    see[e] = (sees(half, 8 * u + 2 * e) ? 0x3F80u : 0u) | (sees(half, 8 * u + 2 * e + 1) ? 0x3F800000u : 0u);
                 seen[u] = __builtin_bit_cast(bf16x8, see);
             }
 #pragma unroll
             for (int i = 0; i < DT; ++i) {
+                __builtin_amdgcn_sched_barrier(0);  // one tile at a time: registers
                 f32x16 nans;
                 zero(nans);
 #pragma unroll
@@ -748,7 +759,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
                     bf16x8 v = value(vi, half, u, i), nan;
                     split_nan(v, nan);
                     nans = mfma_bf16_32x32x16(nan, seen[u], nans);
-                    o[i] = mfma_bf16_32x32x16(v, w[u], o[i]);
+                    o[i] = mfma_bf16_32x32x16(v, w[half][u], o[i]);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[i][e] = nans[e] > 0.0f ? NAN : o[i][e];
