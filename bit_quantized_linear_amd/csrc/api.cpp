@@ -121,9 +121,11 @@ svdq_status check_kv8_shape(int T, int B, int max_pages, int num_pages, int Hk, 
     return SVDQ_OK;
 }
 
-svdq_status check_kv8_queries(int T, int Hq, int Hk) {
+svdq_status check_kv8_queries(int T, int B, int Hq, int Hk) {
     if (Hq <= 0) return SVDQ_ERR_INVALID_ARGUMENT;
-    return Hq % Hk || Hq > 65535 || (int64_t)T * Hq >= 1 << 30 ? SVDQ_ERR_UNSUPPORTED_SHAPE : SVDQ_OK;
+    if (Hq % Hk || Hq > 65535 || (int64_t)T * Hq >= 1 << 30) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    // tiles of 256 queries, of 512 threads each, in one grid dimension
+    return (int64_t)T * Hq + 255LL * B * Hk >= 1LL << 31 ? SVDQ_ERR_UNSUPPORTED_SHAPE : SVDQ_OK;
 }
 
 // Rows of heads: a stride between tokens that holds a row and keeps 16-byte pieces aligned.
@@ -646,7 +648,7 @@ svdq_status svdq_kv8_append(const uint16_t *K, int64_t k_stride, const uint16_t 
 }
 
 size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, int Hk, int D) {
-    if (check_kv8_shape(T, B, max_pages, 1, Hk, D) != SVDQ_OK || check_kv8_queries(T, Hq, Hk) != SVDQ_OK) return 0;
+    if (check_kv8_shape(T, B, max_pages, 1, Hk, D) != SVDQ_OK || check_kv8_queries(T, B, Hq, Hk) != SVDQ_OK) return 0;
     return svdq::kv8_attention_workspace(T, B, max_pages, Hq, Hk, D);
 }
 
@@ -656,7 +658,7 @@ svdq_status svdq_kv8_attention(const uint16_t *Q, int64_t q_stride, const uint8_
                                float scale, int causal, int window, uint16_t *O, float *lse, void *workspace,
                                size_t workspace_bytes, void *stream) {
     svdq_status st = check_kv8_shape(T, B, max_pages, num_pages, Hk, D);
-    if (st == SVDQ_OK) st = check_kv8_queries(T, Hq, Hk);
+    if (st == SVDQ_OK) st = check_kv8_queries(T, B, Hq, Hk);
     if (st == SVDQ_OK) st = check_rows(q_stride, (int64_t)Hq * D);
     if (st != SVDQ_OK) return st;
     if (!(scale > 0.0f) || std::isinf(scale) || window < 0 || (window > 0 && !causal)) return SVDQ_ERR_INVALID_ARGUMENT;

@@ -34,6 +34,7 @@ namespace svdq {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLeastFactor = 0x1p-126f;  // of scores: a page's key scale may be 0, a hidden score -infinity
 
 struct AttnArgs {
     KvBatch kv;
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
             const int p = p0 + wave + kDecWaves * (from + lane);
             number = p < p1 ? kv_page(a.kv, b, p) : -1;
             const int64_t unit = (int64_t)max(number, 0) * a.Hk + head;
-            factor = a.ks[unit] * a.scale;
+            factor = fmaxf(a.ks[unit] * a.scale, kLeastFactor);
             vs = a.vs[unit];
         };
         u32x4 k[4][KC], v[DT];
@@ -505,7 +506,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
             if (page >= 0) {
                 const int64_t unit = (int64_t)page * a.Hk + head;
                 const float ks = a.ks[unit], vs = a.vs[unit];
-                x[1] = __float_as_uint(fmaxf(ks * a.scale, 1.17549435e-38f));
+                x[1] = __float_as_uint(fmaxf(ks * a.scale, kLeastFactor));
                 x[2] = __float_as_uint(vs);
                 x[3] = p >= f0 && p < f1 && power_of_two(vs);
             }
@@ -860,7 +861,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
     if (a.lse && h == 0) a.lse[at] = (base + log2f(l)) * kLn2;
 }
 
-// Parts of a sequence's pages: as many as give each compute unit a block.
+// Parts of a sequence's pages. Few queries: as many as give each compute unit a
+// block (8 heads, one token after 32759: 17.6 us in 32 parts, 20.6 in 16, 17.9 in 64;
+// 32 sequences of up to 8192, 8 heads: 70 in one, 71 in two, 69 in four), at least
+// one for each 128 pages while that makes no more than 16 blocks a unit (a long
+// sequence among short ones; 16384 tokens a part take about as long as the chip's
+// whole cache in decoding), and one up to 16 pages (500 tokens: 7.0 in one, 8.9 in
+// two; 1000: 9.5 and 8.8, but a launch less, 3.4 on the host).
+// Prompts: what takes least by the time of a page in a block, of the second launch
+// and of a query's part on its way through memory (64 tokens after 32000, 8 heads:
+// 58 us in 32 parts, 735 in one; 1000 tokens alone, 8 heads: 36 in one, 70 in two).
 constexpr int kCus = 256;
 constexpr int kAlonePages = 16, kDeepPages = 128;
 constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
@@ -882,8 +892,8 @@ AttnPlan attn_plan(int T, int B, int max_pages, int Hk, int group) {
     const int fill = (int)std::min<int64_t>(SVDQ_KV8_MAX_SPLITS, kCus / ((int64_t)p.tiles * Hk));
     if (p.few) {
         if (max_pages > kAlonePages) {
-            const int deep = std::min((max_pages + kDeepPages - 1) / kDeepPages, SVDQ_KV8_MAX_SPLITS);
-            p.splits = std::max(1, std::min(std::max(fill, deep), (max_pages + kDecWaves - 1) / kDecWaves));
+            const int deep = (int)std::min<int64_t>((max_pages + kDeepPages - 1) / kDeepPages, 16 * kCus / ((int64_t)B * Hk));
+            p.splits = std::min({std::max({fill, deep, 1}), (max_pages + kDecWaves - 1) / kDecWaves, SVDQ_KV8_MAX_SPLITS});
         }
     } else {
         float best = kPageTime * max_pages;
@@ -910,8 +920,9 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
                                 const float *ks, const uint8_t *vc, const float *vs, int Hq, int Hk, int D, float scale,
                                 bool causal, int window, uint16_t *O, float *lse, void *workspace, hipStream_t stream) {
     const AttnPlan plan = attn_plan(kv.T, kv.B, kv.max_pages, Hk, Hq / Hk);
-    const AttnArgs a{kv, Q,  q_stride, kc,  vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal, window,
-                     O,  lse, static_cast<float *>(workspace), plan.splits};
+    const AttnArgs a{kv, Q,  q_stride, kc,  vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal,
+                     std::min(window, 1 << 30),  // no position is further
+                                         O,  lse, static_cast<float *>(workspace), plan.splits};
     if (plan.few)
         hipLaunchKernelGGL(D == 64 ? kv8_decode_kernel<64> : kv8_decode_kernel<128>,
                            dim3((unsigned)plan.splits, (unsigned)Hk, (unsigned)kv.B), dim3(64 * kDecWaves), 0, stream, a);

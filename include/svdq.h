@@ -615,7 +615,9 @@ svdq_status svdq_rope(const uint16_t *X, int64_t x_stride, const int32_t *positi
 /* The 8-bit key and value cache. num_pages pages of SVDQ_KV8_PAGE = 64 tokens:
  *   kc [num_pages, Hk, 64, D] E4M3 bytes (keys), ks [num_pages, Hk] fp32,
  *   vc [num_pages, Hk, D, 64] E4M3 bytes (values, a feature's 64 tokens
- *   together), vs [num_pages, Hk] fp32; value = code * the page's scale.
+ *   together), vs [num_pages, Hk] fp32; value = code * the page's scale. Scales
+ *   are not negative; svdq_kv8_append writes powers of two, others (a cache filled
+ *   elsewhere) serve as well.
  * A batch of B sequences in a call:
  *   starts [B + 1] int32: rows starts[b] .. starts[b + 1] - 1 of the call's T
  *      rows are the newest tokens of sequence b, in order;
@@ -634,13 +636,13 @@ svdq_status svdq_rope(const uint16_t *X, int64_t x_stride, const int32_t *positi
  *   per page, head, and keys and values: A = max(max |x| over the new tokens,
  *   2^-100), need = the least power of two with A <= 448 need; s = need, or
  *   max(need, the page's scale) where the page holds earlier tokens of the
- *   sequence; code = E4M3(fp32(x / s)), and the earlier tokens' codes become
- *   E4M3(fp32(code * (old scale / s))), both round to nearest even.
+ *   sequence; code = E4M3(fp32(x * fp32(1 / s))), and the earlier tokens' codes
+ *   become E4M3(fp32(code * fp32(old scale / s))), both round to nearest even.
  * Values that are not finite become the NaN code and do not count for A. What a
  * page holds behind the sequence's last token is neither read nor written.
  * In:  K, V bf16, head h of row t at K + t k_stride + h D (strides in elements).
  * In/out: kc, ks, vc, vs. A page that a call writes belongs to one sequence of
- *      the batch (a page shared as a prefix is copied before it is written).
+ *      the batch, once (a page shared as a prefix is copied before it is written).
  * The same call again gives the same cache.
  * Shapes: T >= 0, B >= 0 (either 0 launches nothing), T < 2^24, B < 65536,
  *      D 64 or 128, 1 <= Hk <= 1024, strides % 8 == 0 and >= Hk D,
@@ -667,7 +669,8 @@ size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, i
  *   see have no part in its output, NaN or infinities in their place or not.
  * Head hq of a query uses the keys and values of head hq / (Hq / Hk).
  * Scores, weights' sums and outputs are fp32 sums of products of bf16 numbers
- * (the codes' values, exact; weights rounded to bf16); one rounding to bf16.
+ * (the codes' values, exact; weights rounded to bf16, and values times a scale
+ * that is no power of two); one rounding to bf16.
  * In:  Q bf16, head h of row t at Q + t q_stride + h D (stride in elements);
  *      scale finite and > 0.
  * Out: O [T, Hq, D] bf16; lse [T, Hq] fp32 or NULL: the natural logarithm of the
@@ -680,7 +683,7 @@ size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, i
  * sequence's pages between blocks; other batches share the queries only, so
  * decoded tokens are best kept in calls of their own.
  * Shapes: as svdq_kv8_append, with Hq % Hk == 0, T Hq < 2^30, Hq <= 65535,
- *      q_stride >= Hq D. Deterministic.
+ *      T Hq + 255 B Hk < 2^31, q_stride >= Hq D. Deterministic.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
  *      HIP. */
 svdq_status svdq_kv8_attention(const uint16_t *Q, int64_t q_stride, const uint8_t *kc, const float *ks,

@@ -63,6 +63,7 @@ def attention(Q=FAKE, qs=256, cache=(FAKE,) * 4, starts=FAKE, lengths=FAKE, tabl
     (attention, {"Hq": 0}, INVALID), (attention, {"qs": 248}, INVALID), (attention, {"scale": 0.0}, INVALID),
     (attention, {"scale": NAN}, INVALID), (attention, {"scale": INF}, INVALID), (attention, {"scale": -1.0}, INVALID),
     (attention, {"window": -1}, INVALID), (attention, {"window": 4, "causal": 0}, INVALID),
+    (attention, {"B": 65535, "Hq": 1024, "Hk": 1024, "qs": 1 << 20}, SHAPE),
     (attention, {"T": (1 << 24) - 1, "Hq": 65, "Hk": 65, "qs": 4160}, SHAPE), (attention, {"Q": None}, INVALID),
     (attention, {"O": None}, INVALID), (attention, {"lengths": None}, INVALID), (attention, {"ws": None, "pages": 512}, INVALID),
     (attention, {"wb": 64, "pages": 512}, INVALID), (attention, {"lse": MISALIGNED}, MIS), (attention, {"table": MISALIGNED}, MIS),

@@ -106,7 +106,7 @@ def check(got, ref, lengths, D, rows=None):
     empty = np.isneginf(r["lse"])
     assert np.array_equal(np.isneginf(lse), empty) and np.all(o[empty] == 0.0)
     fine = np.isfinite(r["lse"])
-    far = np.abs(lse - r["lse"])[fine]
+    far = np.abs(lse[fine] - r["lse"][fine])
     assert np.all(far <= (delta[..., 0] + (length + 64) * 2.0 ** -23 + 2.0 ** -22 * np.abs(r["lse"]))[fine])
     assert np.array_equal(np.isnan(lse), np.isnan(r["lse"]))
 

@@ -147,6 +147,23 @@ def test_masks_over_many_pages(lengths, new, Hq, Hk, kw):
         run(7 + D, lengths, new, Hq, Hk, D, **kw)
 
 
+@pytest.mark.parametrize("new", [5, 60])
+def test_a_window_past_everything(new):
+    """The widest window, and more new tokens than the sequence has."""
+    t = H.torch()
+    x = Batch(17, [40], [40], 2, 1, 64)
+    O, L = (t.zeros((new, 2, 64), dtype=t.bfloat16, device="cuda"), t.zeros((new, 2), device="cuda"))  # noqa: E741
+    args = (t.cat([x.q, x.q])[:new], x.kc, x.ks, x.vc, x.vs, t.tensor([0, new], dtype=t.int32, device="cuda"))
+    out = []
+    for window in (0, 2147483647):
+        for length in (40, 3):
+            b.svdq_kv8_attention(*args, t.tensor([length], dtype=t.int32, device="cuda"), x.table, 0.125, O, L, window=window)
+            out.append((O.clone(), L.clone()))
+    for a, c in zip(out[:2], out[2:]):
+        assert t.equal(a[0], c[0]) and t.equal(a[1], c[1])
+    assert (out[1][0][: new - 3] == 0).all() and t.isneginf(out[1][1][: new - 3]).all() and (out[1][0][-3:] != 0).any()
+
+
 @pytest.mark.parametrize("lengths,new", [([3000], [1]), ([3000], [300]), ([200], [150])])
 def test_scales_that_are_no_powers_of_two(lengths, new):
     for D in (64, 128):
@@ -154,11 +171,12 @@ def test_scales_that_are_no_powers_of_two(lengths, new):
 
 
 @pytest.mark.parametrize("new", [1, 300])
-def test_a_value_scale_of_0(new):
-    """Pages of zeros, as another program may write them, in the middle of the others."""
+@pytest.mark.parametrize("what", ["ks", "vs"])
+def test_scales_of_0(new, what):
+    """Pages of zeros, as another program may write them, the last among them."""
     x = Batch(11, [2000], [new], 2, 1, 64)
-    for i in (3, 4, 17, 30):
-        x.vs[x.pages[0][i]] = 0.0
+    for i in (3, 4, 17, 30, 31):
+        getattr(x, what)[x.pages[0][i]] = 0.0
     O, L, ws = x.buffers()  # noqa: E741
     x.call(O, L, ws)
     x.check(O, L)
