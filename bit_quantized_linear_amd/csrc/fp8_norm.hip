@@ -22,6 +22,8 @@ namespace svdq {
 
 namespace {
 
+constexpr int kCus = 256;  // compute units
+
 // The largest of 16 lanes' values (lanes 16 n .. 16 n + 15), in all of them.
 __device__ __forceinline__ uint32_t max_of_16(uint32_t v) {
     v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));   // lane ^ 1
@@ -94,20 +96,24 @@ __device__ __forceinline__ void norm_output(const NormArgs &a, int m, int k, flo
     if (k % kF8Block == 0) a.sx[(size_t)(k / kF8Block) * a.M + m] = A / kF8Max;
 }
 
-// A token per block of NT threads, C pieces of 8 features per thread in
-// registers; the rest of a longer row is read again for the second pass (each
-// thread reads what it has read before and writes there afterwards, so that the
-// sum may replace the residual).
-template <int NT, int C>
-__global__ __launch_bounds__(NT) void fp8_norm_kernel(NormArgs a) {
+// HBM-bound: 2 bytes in, 2 of the residual, 2 of the sum out and 1 of a code per
+// feature, each once; 32760 x 5120 takes 213 us, 5.5 TB/s (a large copy: 5.15), 8 x
+// 4096 3.0 us, of which an empty launch is 2 to 3.
+// TR threads a token, C pieces of 8 features per thread in registers; the rest of a
+// longer row is read again for the second pass (each thread reads what it has read
+// before and writes there afterwards, so that the sum may replace the residual).
+template <int TR, int C>
+__global__ __launch_bounds__(TR < 256 ? 256 : TR) void fp8_norm_kernel(NormArgs a) {
+    constexpr int NT = TR < 256 ? 256 : TR;
     __shared__ double part[NT / 64];
-    const int m = blockIdx.x;
+    const int m = blockIdx.x * (NT / TR) + threadIdx.x / TR, t = threadIdx.x % TR;
+    if (TR < 256 && m >= a.M) return;
     const size_t row = (size_t)m * a.K;
     float h[C][8];
     double ss = 0.0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int k = (c * NT + (int)threadIdx.x) * 8;
+        const int k = (c * TR + t) * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
         if (k < a.K) norm_input(a, row + k, h[c]);
@@ -116,28 +122,28 @@ __global__ __launch_bounds__(NT) void fp8_norm_kernel(NormArgs a) {
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)h[c][i], (double)h[c][i], ss);
-    for (int k = (C * NT + (int)threadIdx.x) * 8; k < a.K; k += NT * 8) {
+    for (int k = (C * TR + t) * 8; k < a.K; k += TR * 8) {
         float g[8];
         norm_input(a, row + k, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)g[i], (double)g[i], ss);
     }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) ss += __shfl_xor(ss, d);
-    if (NT > 64) {
+    for (int d = 1; d < 64 && d < TR; d <<= 1) ss += __shfl_xor(ss, d);
+    if constexpr (TR > 64) {
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
         __syncthreads();
         ss = 0.0;
 #pragma unroll
-        for (int w = 0; w < NT / 64; ++w) ss += part[w];
+        for (int w = 0; w < TR / 64; ++w) ss += part[w];
     }
     const float rs = (float)(1.0 / sqrt(ss / a.K + (double)a.eps));
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int k = (c * NT + (int)threadIdx.x) * 8;
-        if (k - (int)(threadIdx.x & 15) * 8 < a.K) norm_output(a, m, k, h[c], rs);
+        const int k = (c * TR + t) * 8;
+        if (k - (t & 15) * 8 < a.K) norm_output(a, m, k, h[c], rs);
     }
-    for (int k = (C * NT + (int)threadIdx.x) * 8; k - (int)(threadIdx.x & 15) * 8 < a.K; k += NT * 8) {
+    for (int k = (C * TR + t) * 8; k - (t & 15) * 8 < a.K; k += TR * 8) {
         float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (k < a.K) norm_input(a, row + k, g);
         norm_output(a, m, k, g, rs);
@@ -149,8 +155,24 @@ __global__ __launch_bounds__(NT) void fp8_norm_kernel(NormArgs a) {
 hipError_t launch_fp8_norm(const uint16_t *X, const uint16_t *residual, const uint16_t *w, float eps, int M, int K,
                            uint16_t *sum, uint16_t *Y, uint8_t *qx, float *sx, hipStream_t stream) {
     const NormArgs a{X, residual, w, eps, M, K, sum, Y, qx, sx};
-    hipLaunchKernelGGL((fp8_norm_kernel<256, 4>), dim3((unsigned)M), dim3(256), 0, stream, a);
-    return hipGetLastError();
+    const auto launch = [&](auto kernel, int per_token) {
+        const int threads = std::max(per_token, 256), tokens = threads / per_token;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((M + tokens - 1) / tokens)), dim3((unsigned)threads), 0, stream, a);
+        return hipGetLastError();
+    };
+    // Short rows: several tokens a block, so that its threads have work (32760 x 256: 12.6
+    // us against 49.7 with a block per token, x 1024: 47.9 against 66.5, x 2048: 95 and 85.5)
+    if (K <= 128) return launch(fp8_norm_kernel<16, 1>, 16);
+    if (K <= 256) return launch(fp8_norm_kernel<32, 1>, 32);
+    if (K <= 512) return launch(fp8_norm_kernel<64, 1>, 64);
+    const bool few = M <= kCus;
+    if (!few && K <= 1024) return launch(fp8_norm_kernel<64, 2>, 64);
+    if (K <= 2048) return launch(fp8_norm_kernel<256, 1>, 256);
+    // Long rows: 512 threads where a compute unit has one token (16 x 8192: 3.8 us against
+    // 5.1 with 256) or they spare registers (4096 x 8192: 49.6 against 55.1; 32760 x
+    // 5120: 231 against 213)
+    if (few || K > 6144) return launch(fp8_norm_kernel<512, 2>, 512);
+    return launch(fp8_norm_kernel<256, 3>, 256);
 }
 
 }  // namespace svdq

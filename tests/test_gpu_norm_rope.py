@@ -98,7 +98,8 @@ def norm_check(got, ref):
 
 
 @pytest.mark.parametrize("M,K", [(1, 16), (1, 128), (3, 144), (2, 1936), (5, 2048), (17, 5120), (333, 400), (2, 8192),
-                                 (3, 8208), (2, 20000), (1030, 1040), (4097, 96), (1, 65552)])
+                                 (3, 8208), (2, 20000), (1030, 1040), (4097, 96), (1, 65552),
+                                 (1001, 256), (257, 1024), (256, 1024), (300, 2064), (257, 6144), (300, 6160), (259, 512)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm(M, K, residual):
     xv, x = bf16(M + K, (M, K))
