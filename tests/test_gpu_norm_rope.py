@@ -189,7 +189,8 @@ def rope_check(y, x, pos, freqs, sections, interleaved):
 @pytest.mark.parametrize("T,H_,D,sections,far", [(1, 1, 16, (8,), 10), (3, 5, 64, (32,), 1 << 20), (7, 3, 128, (22, 21, 21), 50),
                                                  (2, 40, 128, (16, 24, 24), 1000), (5, 9, 80, (0, 7, 9), 100),
                                                  (33, 2, 96, (4, 8, 12, 16), 77), (2, 3, 512, (100, 156), 3000),
-                                                 (4, 80, 128, (64,), 2147483647), (300, 6, 64, (3, 0, 5), 40)])
+                                                 (4, 80, 128, (64,), 2147483647), (300, 6, 64, (3, 0, 5), 40), (4099, 2, 64, (10, 22), 90),
+                                                 (8191, 1, 80, (16,), 1000), (6146, 4, 128, (60, 4), 70)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rope(T, H_, D, sections, far, interleaved):
     t = H.torch()
