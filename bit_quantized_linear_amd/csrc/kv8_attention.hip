@@ -47,6 +47,7 @@ struct AttnArgs {
     int causal, window;
     uint16_t *O;
     float *lse;
+    bool sorted;  // prompts: tiles in the order of all sequences' pages
     float *part;  // splits' sums [T][Hq][splits][D], then maxima and sums of weights [T][Hq][splits][2]
     int splits;
 };
@@ -417,6 +418,56 @@ __device__ __forceinline__ float max_of_halves(float v) {
 
 constexpr float kRise = 6.0f;  // how far, in powers of two, a score may pass the base that weights are taken to
 
+// The sum of a wave's values: of 16 lanes each by rotations, of the four rows by hand.
+__device__ __forceinline__ int wave_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);   // lane ^ 2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);  // 7 - lane, of 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);  // 15 - lane, of 16
+    return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
+           __builtin_amdgcn_readlane(v, 48);
+}
+
+// kv_find for the tiles of up to 64 sequences in the order of the pages that they see
+// (windows apart), the longest first: the last blocks of a launch are then short
+// ones. Tile k of a sequence sees at least P pages from a k on that is easily worked
+// out; a search over P finds the item's.
+__device__ __forceinline__ bool find_longest(const AttnArgs &a, int item, int tile_rows, int &b, KvSeq &seq, int &tile) {
+    const int lane = threadIdx.x & 63;
+    const KvSeq mine = kv_seq(a.kv, min(lane, a.kv.B - 1));
+    const int rows = lane < a.kv.B ? mine.rows * a.group : 0, tiles = (rows + tile_rows - 1) / tile_rows;
+    // the first tile that sees at least `pages` pages
+    auto first_with = [&](int pages) {
+        if (!a.causal) return mine.length > (pages - 1) * kKvPage ? 0 : tiles;
+        const int token = max(0, (pages - 1) * kKvPage - (mine.length - mine.rows));  // the first that does
+        return token < mine.rows ? min(tiles, max(0, (a.group * token + tile_rows) / tile_rows - 1)) : tiles;
+    };
+    if (item >= wave_sum(tiles)) return false;
+    // low: at least item + 1 tiles see so many pages, high: they do not
+    int low = 0, high = a.kv.max_pages + 1;
+    while (high - low > 1) {
+        const int mid = low + (high - low) / 2;
+        if (wave_sum(tiles - first_with(mid)) > item)
+            low = mid;
+        else
+            high = mid;
+    }
+    const int from = low > 0 ? first_with(low) : 0, n = first_with(low + 1) - from;
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int other = __shfl_up(upto, d);
+        upto += lane >= d ? other : 0;
+    }
+    item -= wave_sum(tiles - first_with(low + 1));
+    b = __ffsll((unsigned long long)__ballot(item < upto)) - 1;
+    seq.row0 = __builtin_amdgcn_readlane(mine.row0, b);
+    seq.rows = __builtin_amdgcn_readlane(mine.rows, b);
+    seq.length = __builtin_amdgcn_readlane(mine.length, b);
+    tile = __builtin_amdgcn_readlane(from, b) + item - __builtin_amdgcn_readlane(upto - n, b);
+    return true;
+}
+
 constexpr int kPreInfo = 512;  // pages whose numbers and scales are in LDS at a time
 
 // A block takes 32 queries a wave and walks the pages that they see, or its part of
@@ -459,9 +510,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
     }
     int b, tile;
     KvSeq seq;
-    if (!kv_find(a.kv, item, b, seq, tile, [=](const KvSeq &s) { return (s.rows * group + kRows - 1) / kRows; })) return;
+    if (a.sorted) {
+        if (!find_longest(a, item, kRows, b, seq, tile)) return;
+    } else {
+        if (!kv_find(a.kv, item, b, seq, tile, [=](const KvSeq &s) { return (s.rows * group + kRows - 1) / kRows; })) return;
+        tile = (seq.rows * group + kRows - 1) / kRows - 1 - tile;  // a sequence's longest first
+    }
     const int rows = seq.rows * group;
-    tile = (rows + kRows - 1) / kRows - 1 - tile;  // the longest first
     const int r0 = tile * kRows, last = min(r0 + kRows, rows) - 1;
     const int row = min(r0 + 32 * wave + q32, last);
     int low, high, low0, high0, low1, high1;
@@ -878,7 +933,7 @@ constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
 // How a call is cut: which kernel, its queries per block (`rows`), the blocks of a
 // head (`tiles`, prompts) and the parts of a sequence's pages.
 struct AttnPlan {
-    bool few;
+    bool few, sorted;
     int rows, tiles, splits;
 };
 
@@ -888,6 +943,8 @@ AttnPlan attn_plan(int T, int B, int max_pages, int Hk, int group) {
     p.few = queries <= (int64_t)kDecRows * B;
     p.rows = p.few ? kDecRows : queries <= 128 * (int64_t)B ? 128 : 256;
     p.tiles = p.few ? B : (int)((queries + (int64_t)(p.rows - 1) * B) / p.rows);
+    // more blocks than units: in order, where the sequences fit a wave
+    p.sorted = !p.few && B > 1 && B <= 64 && (int64_t)p.tiles * Hk > kCus;
     p.splits = 1;
     const int fill = (int)std::min<int64_t>(SVDQ_KV8_MAX_SPLITS, kCus / ((int64_t)p.tiles * Hk));
     if (p.few) {
@@ -922,7 +979,7 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
     const AttnPlan plan = attn_plan(kv.T, kv.B, kv.max_pages, Hk, Hq / Hk);
     const AttnArgs a{kv, Q,  q_stride, kc,  vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal,
                      std::min(window, 1 << 30),  // no position is further
-                                         O,  lse, static_cast<float *>(workspace), plan.splits};
+                                         O,  lse, plan.sorted, static_cast<float *>(workspace), plan.splits};
     if (plan.few)
         hipLaunchKernelGGL(D == 64 ? kv8_decode_kernel<64> : kv8_decode_kernel<128>,
                            dim3((unsigned)plan.splits, (unsigned)Hk, (unsigned)kv.B), dim3(64 * kDecWaves), 0, stream, a);
