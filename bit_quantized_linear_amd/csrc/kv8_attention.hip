@@ -94,62 +94,71 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 // ---- few queries -----------------------------------------------------------
 
 constexpr int kDecWaves = 4;
-constexpr int kDecRows = 16;
+constexpr int kDecRows = 16;  // of a matrix-core tile
 
-// A block takes up to 16 queries at a time and a run of the sequence's pages, its
-// waves every fourth of them, straight into registers: the next page's keys as soon
-// as this one's scores are there, its values as soon as this one's are multiplied.
-// The numbers and scales of a wave's next 64 pages are in its lanes. The waves' sums
-// are joined in LDS and, where a sequence's pages are split over blocks, by a second
-// kernel.
-template <int D>
+// A block takes up to 16, 32 or 64 queries at a time and a run of the sequence's
+// pages, its waves every fourth of them (or every second, half of the queries each),
+// straight into registers: the next page's keys as soon as this one's scores are
+// there, its values as soon as this one's are multiplied. A wave takes QT tiles of 16
+// queries, one after the other up to their weights, then each value to all of them.
+// The numbers and scales of a wave's next 64 pages are in its lanes, the queries in
+// LDS. The waves' sums are joined in LDS and, where a sequence's pages are split over
+// blocks, by a second kernel.
+template <int D, int QT, int WR>
 __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs a) {
     constexpr int KC = D / 64;  // 64-byte pieces of a key
     constexpr int DT = D / 16;  // 16-row tiles of V^T
+    constexpr int kRows = kDecRows * QT * WR, kStride = kDecWaves / WR;
+    static_assert(QT <= kStride, "one wave for each tile of queries");
     __shared__ __align__(16) float o_s[kDecWaves][kDecRows][D + 4];
+    __shared__ u32x4 q_s[WR * QT][2 * KC][64];
     __shared__ float m_s[kDecWaves][kDecRows], l_s[kDecWaves][kDecRows];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q16 = lane & 15, g4 = lane >> 4;
     const int split = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
     const KvSeq seq = kv_seq(a.kv, b);
     const int rows = seq.rows * a.group;
-    for (int r0 = 0; r0 < rows; r0 += kDecRows) {
-        const int last = min(r0 + kDecRows, rows) - 1;
-        const int r = min(r0 + q16, last);
-        int low, high, low0, high0, low1, high1;
-        kv_seen(a, seq, r / a.group, low, high);
+    const int wp = wave / WR, wr = wave % WR * QT;  // which pages are the wave's, and the first of its tiles
+    for (int r0 = 0; r0 < rows; r0 += kRows) {
+        const int last = min(r0 + kRows, rows) - 1;
+        int low[QT], high[QT], low0, high0, low1, high1;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) kv_seen(a, seq, min(r0 + kDecRows * (wr + t) + q16, last) / a.group, low[t], high[t]);
         kv_seen(a, seq, r0 / a.group, low0, high0);
         kv_seen(a, seq, last / a.group, low1, high1);
-        // low0 <= low <= low1 and high0 <= high <= high1
+        // low0 <= low[t] <= low1 and high0 <= high[t] <= high1
         const int first_page = low0 / kKvPage, pages = max(0, (high1 + kKvPage - 1) / kKvPage - first_page);
         const int per = (pages + a.splits - 1) / a.splits;
         const int p0 = first_page + split * per, p1 = min(p0 + per, first_page + pages);
 
-        bf16x8 q[2 * KC];
-        {
+        if (wp < QT) {  // a tile's queries to LDS
+            const int r = min(r0 + kDecRows * (wr + wp) + q16, last);
             const uint16_t *src = a.Q + (int64_t)(seq.row0 + r / a.group) * a.q_stride +
                                   (int64_t)(head * a.group + r % a.group) * D + 16 * g4;
 #pragma unroll
-            for (int i = 0; i < KC; ++i) {
-                q[2 * i] = bitcast<bf16x8>(src + 64 * i);
-                q[2 * i + 1] = bitcast<bf16x8>(src + 64 * i + 8);
-            }
+            for (int i = 0; i < 2 * KC; ++i) q_s[wr + wp][i][lane] = bitcast<u32x4>(src + 64 * (i / 2) + 8 * (i & 1));
         }
-        float m = -INFINITY, l = 0.0f;
-        f32x4 o[DT];
+        __syncthreads();
+        float m[QT], l[QT];
+        f32x4 o[QT][DT];
 #pragma unroll
-        for (int i = 0; i < DT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < QT; ++t) {
+            m[t] = -INFINITY;
+            l[t] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
 
-        // lane i: page p0 + wave + 4 (first + i) of the sequence
+        // lane i: page p0 + wp + kStride (first + i) of the sequence
         int number = -1, first = 0;
         float factor = 0.0f, vs = 0.0f;
         auto look_up = [&](int from) __attribute__((always_inline)) {
             first = from;
-            const int p = p0 + wave + kDecWaves * (from + lane);
+            const int p = p0 + wp + kStride * (from + lane);
             number = p < p1 ? kv_page(a.kv, b, p) : -1;
             const int64_t unit = (int64_t)max(number, 0) * a.Hk + head;
             factor = fmaxf(a.ks[unit] * a.scale, kLeastFactor);
-            vs = a.vs[unit];
+            vs = number >= 0 ? a.vs[unit] : 0.0f;
         };
         u32x4 k[4][KC], v[DT];
         auto unit_of = [&](int i) {
@@ -169,95 +178,99 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
 #pragma unroll
             for (int n = 0; n < DT; ++n) v[n] = bitcast<u32x4>(vp + (16 * n + q16) * kKvPage + 16 * g4);
         };
-        const int count = p1 > p0 + wave ? (p1 - p0 - wave + kDecWaves - 1) / kDecWaves : 0;
+        const int count = p1 > p0 + wp ? (p1 - p0 - wp + kStride - 1) / kStride : 0;
         if (count > 0) {
             look_up(0);
             load_keys(0);
             load_values(0);
         }
         for (int i = 0; i < count; ++i) {
-            const int p = p0 + wave + kDecWaves * i;
+            const int p = p0 + wp + kStride * i;
             const bool there = __builtin_amdgcn_readlane(number, i - first) >= 0, more = i + 1 < count;
             const float c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(factor), i - first));
             const float vscale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), i - first));
-            f32x4 s[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                __builtin_amdgcn_sched_barrier(0);  // few converted operands at a time: registers
-                s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < KC; ++i) {
-                    s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][i][0], k[j][i][1]), q[2 * i], s[j]);
-                    s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][i][2], k[j][i][3]), q[2 * i + 1], s[j]);
-                }
-            }
             const int t0 = p * kKvPage;
-            if (more) {
-                if (i + 1 - first == 64) look_up(i + 1);
-                load_keys(i + 1);
-            }
-            if (!there) {
-                if (more) load_values(i + 1);
-                continue;
-            }
             // a page that some query does not see whole: hidden tokens' weights are
-            // 0, and their values are not multiplied, as they may be NaN
+            // 0, and their values are not multiplied, as they may be NaN. Of a page
+            // that is not there, all are hidden
+            const bool cut = !there || t0 < low1 || t0 + kKvPage > high0;
             uint32_t nan = 0;
-            bf16x8 seen[2];
-            if (t0 < low1 || t0 + kKvPage > high0) {
-                uint32_t see[4] = {0u, 0u, 0u, 0u};
+            bf16x8 w[QT][2];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                f32x4 s[4];
+                bf16x8 q[2 * KC];
+#pragma unroll
+                for (int n = 0; n < 2 * KC; ++n) q[n] = __builtin_bit_cast(bf16x8, q_s[wr + t][n][lane]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t mask = byte_mask(t0 + 16 * g4 + 4 * j, low0, high1);
+                    __builtin_amdgcn_sched_barrier(0);  // few converted operands at a time: registers
+                    s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int n = 0; n < DT; ++n) {
-                        v[n][j] &= mask;
-                        nan |= nan_codes(v[n][j]);
+                    for (int n = 0; n < KC; ++n) {
+                        s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][n][0], k[j][n][1]), q[2 * n], s[j]);
+                        s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][n][2], k[j][n][3]), q[2 * n + 1], s[j]);
                     }
-                    see[j] = byte_mask(t0 + 16 * g4 + 4 * j, low, high);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[j][e] = see[j] >> (8 * e) & 1 ? s[j][e] : -INFINITY;
                 }
+                if (QT > 1) __builtin_amdgcn_sched_barrier(0);
+                if (t < QT - 1) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    u32x4 w;
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const uint32_t two = see[2 * u + n / 2] >> (16 * (n & 1));
-                        w[n] = (two & 1 ? 0x3F80u : 0u) | (two & 0x100u ? 0x3F800000u : 0u);
+                        for (int n = 0; n < KC; ++n) asm volatile("" : "+v"(k[j][n]));  // widened again for each tile: registers
+                } else if (more) {
+                    if (i + 1 - first == 64) look_up(i + 1);
+                    load_keys(i + 1);
+                }
+                if (cut) {
+                    if (t == 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t mask = byte_mask(t0 + 16 * g4 + 4 * j, low0, there ? high1 : 0);
+#pragma unroll
+                            for (int n = 0; n < DT; ++n) {
+                                v[n][j] &= mask;
+                                nan |= nan_codes(v[n][j]);
+                            }
+                        }
                     }
-                    seen[u] = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t see = byte_mask(t0 + 16 * g4 + 4 * j, low[t], there ? high[t] : 0);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[j][e] = see >> (8 * e) & 1 ? s[j][e] : -INFINITY;
+                    }
                 }
+                float top = s[0][0];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[j][e]);
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float m_new = fmaxf(m[t], top * c);
+                const float base = m_new == -INFINITY ? 0.0f : m_new;
+                const float alpha = exp2_of(m[t] - base);
+                m[t] = m_new;
+                l[t] *= alpha;
+#pragma unroll
+                for (int n = 0; n < DT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][n][e] *= alpha;
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[4 * j + e] = exp2_of(__builtin_fmaf(s[j][e], c, -base));
+                        l[t] += x[4 * j + e];
+                    }
+                w[t][0] = pack8(x, vscale);
+                w[t][1] = pack8(x + 8, vscale);
             }
-            float top = s[0][0];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[j][e]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m_new = fmaxf(m, top * c);
-            const float base = m_new == -INFINITY ? 0.0f : m_new;
-            const float alpha = exp2_of(m - base);
-            m = m_new;
-            l *= alpha;
-            float w[16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[4 * j + e] = exp2_of(__builtin_fmaf(s[j][e], c, -base));
-                    l += w[4 * j + e];
-                }
-            const bf16x8 w0 = pack8(w, vscale), w1 = pack8(w + 8, vscale);
-#pragma unroll
-            for (int n = 0; n < DT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][e] *= alpha;
             if (__any(nan != 0)) {  // NaN reaches the queries that see its token, and no other
 #pragma unroll
                 for (int n = 0; n < DT; ++n) {
-                    __builtin_amdgcn_sched_barrier(0);
                     u32x4 one;  // the code of 1 for each NaN, which becomes 0 itself
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -265,59 +278,83 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
                         one[j] = at & 0x38383838u;
                         v[n][j] &= ~at;
                     }
-                    f32x4 count = mfma_bf16_16x16x32(fp8_widen8(one[0], one[1]), seen[0], f32x4{0.f, 0.f, 0.f, 0.f});
-                    count = mfma_bf16_16x16x32(fp8_widen8(one[2], one[3]), seen[1], count);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][e] = count[e] > 0.0f ? NAN : o[n][e];
+                    for (int t = 0; t < QT; ++t) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        f32x4 count = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            u32x4 seen;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t two = byte_mask(t0 + 16 * g4 + 8 * u + 2 * e, low[t], high[t]);
+                                seen[e] = (two & 1 ? 0x3F80u : 0u) | (two & 0x100u ? 0x3F800000u : 0u);
+                            }
+                            count = mfma_bf16_16x16x32(fp8_widen8(one[2 * u], one[2 * u + 1]),
+                                                       __builtin_bit_cast(bf16x8, seen), count);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[t][n][e] = count[e] > 0.0f ? NAN : o[t][n][e];
+                    }
                 }
             }
 #pragma unroll
             for (int n = 0; n < DT; ++n) {
-                if (n % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-                o[n] = mfma_bf16_16x16x32(fp8_widen8(v[n][0], v[n][1]), w0, o[n]);
-                o[n] = mfma_bf16_16x16x32(fp8_widen8(v[n][2], v[n][3]), w1, o[n]);
+                if (QT > 1 || n % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const bf16x8 value = fp8_widen8(v[n][2 * u], v[n][2 * u + 1]);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) o[t][n] = mfma_bf16_16x16x32(value, w[t][u], o[t][n]);
+                }
             }
             if (more) load_values(i + 1);
         }
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
-        if (g4 == 0) {
-            m_s[wave][q16] = m;
-            l_s[wave][q16] = l;
-        }
 #pragma unroll
-        for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4 *>(&o_s[wave][q16][16 * i + 4 * g4]) = o[i];
-        __syncthreads();
-        for (int i = tid; i < kDecRows * D / 4; i += 64 * kDecWaves) {
-            const int row = i / (D / 4), d = i % (D / 4) * 4;
-            if (r0 + row > last) continue;
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kDecWaves; ++w) top = fmaxf(top, m_s[w][row]);
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < kDecWaves; ++w) {
-                const float f = top == -INFINITY ? 1.0f : exp2_of(m_s[w][row] - top);
-                sum += l_s[w][row] * f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] += o_s[w][row][d + e] * f;
+        for (int t = 0; t < QT; ++t) {  // the waves' sums of a tile
+            const int first_row = r0 + kDecRows * t;
+            if (first_row > last) break;
+            l[t] += __shfl_xor(l[t], 16);
+            l[t] += __shfl_xor(l[t], 32);
+            if (g4 == 0) {
+                m_s[wave][q16] = m[t];
+                l_s[wave][q16] = l[t];
             }
-            const int64_t at = (int64_t)(seq.row0 + (r0 + row) / a.group) * a.Hq + head * a.group + (r0 + row) % a.group;
-            if (a.splits == 1) {
-                const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-                *reinterpret_cast<u32x2 *>(a.O + at * D + d) =
-                    u32x2{bf16x2_bits(acc[0] * f, acc[1] * f), bf16x2_bits(acc[2] * f, acc[3] * f)};
-                if (a.lse && d == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
-            } else {
-                *reinterpret_cast<f32x4 *>(a.part + (at * a.splits + split) * D + d) = acc;
-                if (d == 0) {
-                    float *ml = a.part + (int64_t)a.kv.T * a.Hq * a.splits * D + (at * a.splits + split) * 2;
-                    ml[0] = top;
-                    ml[1] = sum;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4 *>(&o_s[wave][q16][16 * i + 4 * g4]) = o[t][i];
+            __syncthreads();
+            for (int i = tid; i < WR * kDecRows * D / 4; i += 64 * kDecWaves) {
+                const int part = i / (kDecRows * D / 4), row = i / (D / 4) % kDecRows, d = i % (D / 4) * 4;
+                const int r = first_row + kDecRows * QT * part + row;
+                if (r > last) continue;
+                float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int w = part; w < kDecWaves; w += WR) top = fmaxf(top, m_s[w][row]);
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = part; w < kDecWaves; w += WR) {
+                    const float f = top == -INFINITY ? 1.0f : exp2_of(m_s[w][row] - top);
+                    sum += l_s[w][row] * f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] += o_s[w][row][d + e] * f;
+                }
+                const int64_t at = (int64_t)(seq.row0 + r / a.group) * a.Hq + head * a.group + r % a.group;
+                if (a.splits == 1) {
+                    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    *reinterpret_cast<u32x2 *>(a.O + at * D + d) =
+                        u32x2{bf16x2_bits(acc[0] * f, acc[1] * f), bf16x2_bits(acc[2] * f, acc[3] * f)};
+                    if (a.lse && d == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
+                } else {
+                    *reinterpret_cast<f32x4 *>(a.part + (at * a.splits + split) * D + d) = acc;
+                    if (d == 0) {
+                        float *ml = a.part + (int64_t)a.kv.T * a.Hq * a.splits * D + (at * a.splits + split) * 2;
+                        ml[0] = top;
+                        ml[1] = sum;
+                    }
                 }
             }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -932,6 +969,12 @@ constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
 
 // How a call is cut: which kernel, its queries per block (`rows`), the blocks of a
 // head (`tiles`, prompts) and the parts of a sequence's pages.
+// Queries per block: the least of 16, 32, 64, 128 and 256 that the average sequence
+// fits, up to 64 in the kernel for few (32 sequences of up to 8192, 8 heads: 32
+// queries 78 us, 64 queries 108, 164 both with 128 to a block; 128 queries 170 with
+// 128, 193 twice 64, 229 with 256; 100 queries after 8000 alone 22, 26 and 24; 64
+// sequences of 128 queries after 500 51, 47 and 59; of 256 queries 98 with 128, 72
+// with 256; 200 queries after 500 alone 17 and 20).
 struct AttnPlan {
     bool few, sorted;
     int rows, tiles, splits;
@@ -940,8 +983,9 @@ struct AttnPlan {
 AttnPlan attn_plan(int T, int B, int max_pages, int Hk, int group) {
     AttnPlan p;
     const int64_t queries = (int64_t)T * group;
-    p.few = queries <= (int64_t)kDecRows * B;
-    p.rows = p.few ? kDecRows : queries <= 128 * (int64_t)B ? 128 : 256;
+    p.rows = kDecRows;
+    while (p.rows < 256 && queries > (int64_t)p.rows * B) p.rows *= 2;
+    p.few = p.rows <= 64;
     p.tiles = p.few ? B : (int)((queries + (int64_t)(p.rows - 1) * B) / p.rows);
     // more blocks than units: in order, where the sequences fit a wave
     p.sorted = !p.few && B > 1 && B <= 64 && (int64_t)p.tiles * Hk > kCus;
@@ -965,6 +1009,11 @@ AttnPlan attn_plan(int T, int B, int max_pages, int Hk, int group) {
     return p;
 }
 
+template <int D>
+auto decode_kernel(int rows) {
+    return rows == 16 ? kv8_decode_kernel<D, 1, 1> : rows == 32 ? kv8_decode_kernel<D, 2, 1> : kv8_decode_kernel<D, 2, 2>;
+}
+
 }  // namespace
 
 size_t kv8_attention_workspace(int T, int B, int max_pages, int Hq, int Hk, int D) {
@@ -981,7 +1030,7 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
                      std::min(window, 1 << 30),  // no position is further
                                          O,  lse, plan.sorted, static_cast<float *>(workspace), plan.splits};
     if (plan.few)
-        hipLaunchKernelGGL(D == 64 ? kv8_decode_kernel<64> : kv8_decode_kernel<128>,
+        hipLaunchKernelGGL(D == 64 ? decode_kernel<64>(plan.rows) : decode_kernel<128>(plan.rows),
                            dim3((unsigned)plan.splits, (unsigned)Hk, (unsigned)kv.B), dim3(64 * kDecWaves), 0, stream, a);
     else if (plan.rows == 128)
         hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 4> : kv8_prompt_kernel<128, 4>),

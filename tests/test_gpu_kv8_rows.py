@@ -1,0 +1,93 @@
+"""The 8-bit cache's attention where a sequence has 17 to 64 queries of a key head: a
+few drafted tokens, or one of many heads (needs an MI355X).
+
+Tolerances as in tests/test_gpu_kv8.py and tests/test_gpu_kv8_paths.py.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import decoder as od
+from tests.test_gpu_kv8 import PAGE, attend, attention_case, bf16_values, check, plan, poison, random_cache
+from tests.test_gpu_kv8_paths import run
+from tests.test_gpu_norm_rope import _gpu  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lengths,new,Hq,Hk", [
+    ([17], [17], 1, 1), ([64], [4], 16, 2), ([65], [33], 1, 1), ([130], [64], 1, 1), ([300, 2, 66], [8, 2, 3], 16, 2),
+    ([333, 50, 700], [3, 20, 60], 2, 2), ([700, 64, 0, 5], [9, 1, 0, 5], 10, 2), ([200], [1], 40, 1), ([129, 400], [1, 1], 64, 1),
+    ([100, 100, 100], [90, 1, 1], 1, 1), ([100, 500], [90, 3], 1, 1)])
+def test_rows(lengths, new, Hq, Hk, D):
+    assert 16 * len(new) < sum(new) * (Hq // Hk) <= 64 * len(new)
+    attention_case(sum(lengths) + D, lengths, new, Hq, Hk, D)
+
+
+@pytest.mark.parametrize("lengths,new,Hq,Hk,causal,window", [
+    ([300, 70], [20, 9], 4, 2, False, 0), ([300, 70], [9, 10], 4, 2, True, 100), ([300], [12], 4, 2, True, 1),
+    ([300, 64], [16, 64], 1, 1, True, 64), ([400], [60], 1, 1, True, 5), ([500], [20], 2, 1, True, 129)])
+def test_masks(lengths, new, Hq, Hk, causal, window):
+    for D in (64, 128):
+        attention_case(window + D, lengths, new, Hq, Hk, D, causal, window)
+
+
+@pytest.mark.parametrize("new", [[12, 8, 9], [30, 3, 20]])
+@pytest.mark.parametrize("causal", [True, False])
+def test_queries_that_see_nothing(new, causal):
+    attention_case(31, [10, 0, 0], new, 4, 2, 64, causal=causal)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lengths,new,Hq,Hk,parts", [
+    ([20001], [5], 8, 2, (9, 64)), ([20001, 70], [32, 10], 4, 2, (9, 64)), ([3000] * 40, [2] * 40, 80, 8, (1, 1)),
+    ([18000] + [100] * 35, [8] * 36, 32, 8, (2, 8)), ([2000] * 3, [60] * 3, 1, 1, (2, 64))])
+def test_long_contexts(lengths, new, Hq, Hk, parts, D):
+    run(sum(lengths) + D, lengths, new, Hq, Hk, D, parts)
+
+
+@pytest.mark.parametrize("kw", [{"causal": False}, {"window": 1000}, {"window": 257}])
+def test_masks_over_many_pages(kw):
+    for new in (20, 60):
+        run(7 + new, [6000], [new], 1, 1, 128, **kw)
+
+
+def test_scales_that_are_no_powers_of_two():
+    for D in (64, 128):
+        run(9 + D, [3000, 100], [20, 50], 2, 2, D, scales="any")
+
+
+@pytest.mark.parametrize("new", [20, 50])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_reaches_the_queries_that_see_it(new, D):
+    rng = np.random.default_rng(14)
+    lengths, Hq, Hk = [200], 2, 2
+    starts, table, P = plan(rng, lengths, [new])
+    Q = bf16_values(rng, (new, Hq, D))
+    for what, token, window in (("v", 199 - new // 2, 0), ("k", 199 - new // 2, 0), ("v", 150, 60), ("k", 150, 60), ("v", 3, 0)):
+        cache = random_cache(rng, P, Hk, D)
+        poison(cache, lengths, table)
+        page, at = table[0, token // PAGE], token % PAGE
+        if what == "v":
+            cache.vc[page, 0, 5, at] = 0x7F
+        else:
+            cache.kc[page, 1, at, 9] = 0xFF
+        got = attend(Q, cache, starts, lengths, table, 0.125, window=window)
+        ref = od.attention(Q, cache, starts, lengths, table, 0.125, True, window)
+        assert np.isnan(ref["o"]).any()
+        check(got, ref, lengths, D)
+
+
+@pytest.mark.parametrize("new", [20, 50])
+def test_pages_that_are_not_there(new):
+    rng = np.random.default_rng(15)
+    for D in (64, 128):
+        lengths = [700, 90]
+        starts, table, P = plan(rng, lengths, [new, 3])
+        cache = random_cache(rng, P, 2, D)
+        table[0, 0], table[0, 5], table[0, 10], table[1, 0] = -1, P, -9, P + 4
+        poison(cache, lengths, table)
+        Q = bf16_values(rng, (new + 3, 2, D))
+        ref = od.attention(Q, cache, starts, lengths, table, 0.125)
+        check(attend(Q, cache, starts, lengths, table, 0.125), ref, lengths, D)
