@@ -943,13 +943,18 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
         return;
     }
     const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    // A lane has 4 of each 8 features and its half wave's other lane the rest: one takes
+    // the first 8, one the next (2048 queries of 32 heads over themselves: 73.5 us
+    // against 77.6 with 8-byte stores)
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<u32x2 *>(a.O + at * D + 32 * i + 8 * e + 4 * h) =
-                u32x2{bf16x2_bits(o[i][4 * e] * f, o[i][4 * e + 1] * f),
-                      bf16x2_bits(o[i][4 * e + 2] * f, o[i][4 * e + 3] * f)};
+        for (int e = 0; e < 16; e += 8) {
+            const auto two = [&](int j) { return bf16x2_bits(o[i][e + j] * f, o[i][e + j + 1] * f); };
+            const auto x = __builtin_amdgcn_permlane32_swap(two(0), two(4), false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(two(2), two(6), false, false);
+            *reinterpret_cast<u32x4 *>(a.O + at * D + 32 * i + 2 * e + 8 * h) = u32x4{x[0], y[0], x[1], y[1]};
+        }
     if (a.lse && h == 0) a.lse[at] = (base + log2f(l)) * kLn2;
 }
 
