@@ -91,3 +91,10 @@ def test_pages_that_are_not_there(new):
         Q = bf16_values(rng, (new + 3, 2, D))
         ref = od.attention(Q, cache, starts, lengths, table, 0.125)
         check(attend(Q, cache, starts, lengths, table, 0.125), ref, lengths, D)
+
+
+@pytest.mark.parametrize("new,window", [(1, 100), (1, 2000), (20, 64), (60, 700), (200, 300), (300, 64)])
+def test_windows_much_shorter_than_the_context(new, window):
+    """As many parts as the window's pages ask for, fewer than the workspace holds."""
+    for D in (64, 128):
+        run(new + D, [20000, 300], [new, 1], 4, 2, D, window=window)
