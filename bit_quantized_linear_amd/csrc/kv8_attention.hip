@@ -960,16 +960,19 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a,
 
 // Parts of a sequence's pages. Few queries: as many as give each compute unit a
 // block (8 heads, one token after 32759: 17.6 us in 32 parts, 20.6 in 16, 17.9 in 64;
-// 32 sequences of up to 8192, 8 heads: 70 in one, 71 in two, 69 in four), at least
-// one for each 128 pages while that makes no more than 16 blocks a unit (a long
-// sequence among short ones; 16384 tokens a part take about as long as the chip's
-// whole cache in decoding), and one up to 16 pages (500 tokens: 7.0 in one, 8.9 in
-// two; 1000: 9.5 and 8.8, but a launch less, 3.4 on the host).
+// 32 sequences of up to 8192, 8 heads: 67 in one, 69 in two, 68 in four); tables of
+// more than 128 pages in parts of 64 pages at the most, while that makes no more than
+// 16 blocks a unit, so that a long sequence among short ones is not one block's alone
+// (one of 18000 tokens, 35 of 100: 98 us in one part, 41 in 3, 29 in 5, 25 in 9; one of
+// 32000, 31 of 500: 168, 51 in 4, 31 in 8, 45 in 16; 40 of 16000: 277, 244 in two, 227
+// in four; 32 of 8000, where the second launch is not worth it: 93 and 98); and one
+// up to 16 pages (500 tokens: 7.0 in one, 8.9 in two; 1000: 9.5 and 8.8, but a launch
+// less, 3.4 on the host).
 // Prompts: what takes least by the time of a page in a block, of the second launch
 // and of a query's part on its way through memory (64 tokens after 32000, 8 heads:
 // 58 us in 32 parts, 735 in one; 1000 tokens alone, 8 heads: 36 in one, 70 in two).
 constexpr int kCus = 256;
-constexpr int kAlonePages = 16, kDeepPages = 128;
+constexpr int kAlonePages = 16, kDeepPages = 128, kDeepPart = 64;
 constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
 
 // How a call is cut: which kernel, its queries per block (`rows`), the blocks of a
@@ -998,7 +1001,8 @@ AttnPlan attn_plan(int T, int B, int pages, int Hk, int group) {
     const int fill = (int)std::min<int64_t>(SVDQ_KV8_MAX_SPLITS, kCus / ((int64_t)p.tiles * Hk));
     if (p.few) {
         if (pages > kAlonePages) {
-            const int deep = (int)std::min<int64_t>((pages + kDeepPages - 1) / kDeepPages, 16 * kCus / ((int64_t)B * Hk));
+            const int parts = pages > kDeepPages ? (pages + kDeepPart - 1) / kDeepPart : 1;
+            const int deep = (int)std::min<int64_t>(parts, 16 * kCus / ((int64_t)B * Hk));
             p.splits = std::min({std::max({fill, deep, 1}), (pages + kDecWaves - 1) / kDecWaves, SVDQ_KV8_MAX_SPLITS});
         }
     } else {
