@@ -98,7 +98,7 @@ __device__ __forceinline__ void norm_output(const NormArgs &a, int m, int k, flo
 
 // HBM-bound: 2 bytes in, 2 of the residual, 2 of the sum out and 1 of a code per
 // feature, each once; 32760 x 5120 takes 213 us, 5.5 TB/s (a large copy: 5.15), 8 x
-// 4096 3.0 us, of which an empty launch is 2 to 3.
+// 4096 3.7 us (3.0 in a graph), of which an empty launch is 2 to 3.
 // TR threads a token, C pieces of 8 features per thread in registers; the rest of a
 // longer row is read again for the second pass (each thread reads what it has read
 // before and writes there afterwards, so that the sum may replace the residual).

@@ -41,7 +41,7 @@ __device__ __forceinline__ void rope_turn(float c, float s, float &a, float &b) 
 // A block takes `tokens` tokens: their angles' sines and cosines to LDS, then the
 // heads in pieces of 8 features (two of them, R / 2 apart, where pairs are).
 // HBM-bound: 2 bytes in and 2 out per feature; 32760 tokens of 80 heads of 128 take
-// 245 us, 5.5 TB/s (a large copy: 5.15); 16 tokens of 40 heads 2.5 us, an empty launch.
+// 245 us, 5.5 TB/s (a large copy: 5.15); 16 tokens of 40 heads 3.3 us, an empty launch 2 to 3.
 template <bool kInterleaved>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     __shared__ __align__(16) float cs[kRopeAngles], sn[kRopeAngles];

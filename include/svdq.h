@@ -679,9 +679,11 @@ size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, i
  * Workspace: device memory of at least svdq_kv8_attention_workspace_bytes(T, B,
  *      max_pages, Hq, Hk, D) bytes (NULL if that is 0), owned by the caller, not
  *      read before it is written; calls that may overlap in time need one each.
- * A batch with few queries per sequence on average (T Hq / Hk <= 16 B) shares a
- * sequence's pages between blocks; other batches share the queries only, so
- * decoded tokens are best kept in calls of their own.
+ * A call is cut by its averages: up to 64 queries of a key head per sequence
+ * (T Hq / Hk <= 64 B) take a kernel made for few, more of them one made for many,
+ * so decoded tokens are best kept in calls of their own. max_pages, too, decides
+ * how a sequence's pages are shared between blocks; a table much wider than the
+ * lengths costs time, not results.
  * Shapes: as svdq_kv8_append, with Hq % Hk == 0, T Hq < 2^30, Hq <= 65535,
  *      T Hq + 255 B Hk < 2^31, q_stride >= Hq D. Deterministic.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
