@@ -528,8 +528,11 @@ constexpr int kPreInfo = 512;  // pages whose numbers and scales are in LDS at a
 // other's products: one wave of 64 a SIMD took 3.2 ms. Prompts of three sequences, up
 // to 2777 tokens after up to 1500: 240 us, 940 TFLOP/s; a block's start takes 6 to 7 us,
 // its outputs 2, and pages with masks are not pipelined.
+// Waves a SIMD: two, where D = 64 in two blocks if they have 4 waves (100 queries after 1000
+// of 16 sequences of 16 heads: 32.4 us, 36.5 with one); with D = 128 4 waves need the
+// registers of one (with two, spilled: 49 against 39 us), and two blocks' LDS is not there.
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, NW / 4) void kv8_prompt_kernel(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kernel(AttnArgs a, int tiles) {
     constexpr int KS = D / 16, DT = D / 32, KCH = D / 8;
     constexpr int PC = D / 8 / NW;  // pieces of 8 codes of a page's keys, and of its values, per thread
     constexpr int kRows = 32 * NW;
