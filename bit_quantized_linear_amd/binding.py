@@ -645,6 +645,29 @@ def svdq_fp8_moe_layer(X, wr, w13, s13, w2, s2, Y, idx, gate, workspace, top_k=N
     _check("svdq_fp8_moe_layer", st)
 
 
+_quick_calls = None
+_ANY_KIND = 2 ** 64 - 1
+
+
+def _quick():
+    """pointers and heads of `_tensors`, which look at all tensors of a call at once,
+    and its names for E4M3 codes, bf16, fp32, int32 and fp64 numbers; empty where it
+    was not built for this torch. What they refuse is looked at again below, for the
+    error that fits."""
+    global _quick_calls
+    if _quick_calls is None:
+        _quick_calls = ()
+        try:
+            import torch as t
+
+            from . import _tensors as m
+
+            _quick_calls = (m.pointers, m.heads, *(m.kind(*f) for f in (*_fp8_formats(), (t.float64,))))
+        except ImportError:
+            pass
+    return _quick_calls
+
+
 def _ptr(t, nbytes, name, dev, formats):
     """As _dev_ptr, for the entry points with many tensors: one look at each of a
     tensor's properties, and the reasons only where one is not as it must be."""
@@ -674,18 +697,30 @@ def svdq_fp8_norm_quantize(X, residual, weight, eps, total, Y, qx, sx, stream=No
     None, but not both Y and qx."""
     M, K = _shape2(X, "X")
     dev = _current_device()
-    e4m3, bf16, f32, _ = _fp8_formats()
     n = M * K * 2
-    st = lib().svdq_fp8_norm_quantize(
-        _ptr(X, n, "X", dev, bf16), _ptr(residual, n, "residual", dev, bf16), _ptr(weight, K * 2, "weight", dev, bf16),
-        eps, M, K, _ptr(total, n, "total", dev, bf16), _ptr(Y, n, "Y", dev, bf16), _ptr(qx, M * K, "qx", dev, e4m3),
-        None if sx is None else _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev, f32), _stream(stream))
+    p, quick = None, _quick()
+    if quick:
+        pointers, _, e4m3, bf16, f32, _, _ = quick
+        p = pointers(dev, X, bf16, n, residual, bf16, n, weight, bf16, K * 2, total, bf16, n, Y, bf16, n, qx, e4m3, M * K,
+                     sx, f32, (fp8_blocks(K), M))
+    if p is None:
+        e4m3, bf16, f32, _ = _fp8_formats()
+        p = (_ptr(X, n, "X", dev, bf16), _ptr(residual, n, "residual", dev, bf16), _ptr(weight, K * 2, "weight", dev, bf16),
+             _ptr(total, n, "total", dev, bf16), _ptr(Y, n, "Y", dev, bf16), _ptr(qx, M * K, "qx", dev, e4m3),
+             None if sx is None else _fp8_scales(sx, (fp8_blocks(K), M), "sx", dev, f32))
+    st = lib().svdq_fp8_norm_quantize(p[0], p[1], p[2], eps, M, K, p[3], p[4], p[5], p[6], _stream(stream))
     _check("svdq_fp8_norm_quantize", st)
 
 
-def _dev_heads(t, name, dev, bf16):
-    """Pointer, stride between tokens and shape of heads [T, H, D] in bf16, whose
+def _dev_heads(t, name, dev):
+    """Pointer, stride between tokens and T, H, D of heads [T, H, D] in bf16, whose
     rows may be parts of wider ones (a projection's output)."""
+    quick = _quick()
+    if quick:
+        seen = quick[1](dev, quick[3], t)
+        if seen is not None:
+            return seen
+    bf16 = _fp8_formats()[1]
     if t is None or t.dim() != 3:
         raise TypeError(f"{name} must be a 3-D tensor")
     if t.dtype not in bf16:
@@ -695,14 +730,14 @@ def _dev_heads(t, name, dev, bf16):
         if index < 0:
             raise TypeError(f"{name}: device entry points take GPU tensors")
         raise TypeError(f"{name} is on cuda:{index}, the current device is cuda:{dev}")
-    T, H, D = shape = t.shape
+    T, H, D = t.shape
     row, head, one = t.stride()
     width = H * D
     if T <= 1 or width == 0:  # there is no next row
         row = -(-width // 8) * 8
     if row < width or (one != 1 and D > 1) or (head != D and H > 1):
         raise TypeError(f"{name}: the heads of a token must be contiguous, and tokens apart")
-    return t.data_ptr(), row, shape
+    return t.data_ptr(), row, T, H, D
 
 
 _f64_types = None
@@ -722,35 +757,47 @@ def svdq_rope(X, positions, freqs, sections, Y, interleaved=False, stream=None):
     positions: positions [T, axes] int32, freqs [R / 2] fp64, sections: the pairs of
     each axis, R / 2 in all. Y may be X."""
     dev = _current_device()
-    _, bf16, _, i32 = _fp8_formats()
-    xp, xs, shape = _dev_heads(X, "X", dev, bf16)
-    yp, ys, out = _dev_heads(Y, "Y", dev, bf16)
+    xp, xs, *shape = x = _dev_heads(X, "X", dev)
+    yp, ys, *out = x if Y is X else _dev_heads(Y, "Y", dev)
     if out != shape:
-        raise ValueError(f"Y is {list(out)}, the call writes {list(shape)}")
+        raise ValueError(f"Y is {out}, the call writes {shape}")
     T, H, D = shape
     axes = len(sections)
     if positions is None:
         raise TypeError(f"positions must be a tensor [{T}, {axes}]")
-    st = lib().svdq_rope(xp, xs, _shaped_ptr(positions, (T, axes), "positions", dev, i32),
-                         _ptr(freqs, 8 * sum(sections), "freqs", dev, _f64_format()), (_i * axes)(*sections), axes,
-                         1 if interleaved else 0, T, H, D, yp, ys, _stream(stream))
+    p, quick = None, _quick()
+    if quick:
+        pointers, _, _, _, _, i32, f64 = quick
+        p = pointers(dev, positions, i32, (T, axes), freqs, f64, 8 * sum(sections))
+    if p is None:
+        p = (_shaped_ptr(positions, (T, axes), "positions", dev, _fp8_formats()[3]),
+             _ptr(freqs, 8 * sum(sections), "freqs", dev, _f64_format()))
+    st = lib().svdq_rope(xp, xs, p[0], p[1], (_i * axes)(*sections), axes, 1 if interleaved else 0, T, H, D, yp, ys,
+                         _stream(stream))
     _check("svdq_rope", st)
 
 
-def _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32):
-    """Checked pointers of the 8-bit cache, and its number of pages."""
+def _kv8_tensors(kc, ks, vc, vs, starts, lengths, table, Hk, D, dev):
+    """Checked pointers of the 8-bit cache and of a batch, as the library takes them:
+    kc, ks, vc, vs, starts, lengths, table; and the batch's sequences, the table's
+    width and the cache's pages."""
     if kc is None or vc is None or ks is None or vs is None or kc.dim() != 4:
         raise TypeError("kc and vc must be 4-D tensors, ks and vs their scales")
     P = kc.shape[0]
-    return P, (_shaped_ptr(kc, (P, Hk, KV8_PAGE, D), "kc", dev, e4m3), _shaped_ptr(ks, (P, Hk), "ks", dev, f32),
-               _shaped_ptr(vc, (P, Hk, D, KV8_PAGE), "vc", dev, e4m3), _shaped_ptr(vs, (P, Hk), "vs", dev, f32))
-
-
-def _kv8_batch(starts, lengths, table, dev, i32):
-    """Checked pointers of a batch, its sequences and the table's width."""
     B, max_pages = _shape2(table, "table")
-    return B, max_pages, (_ptr(starts, 4 * (B + 1), "starts", dev, i32), _ptr(lengths, 4 * B, "lengths", dev, i32),
-                          _ptr(table, 0, "table", dev, i32))
+    keys, values, scales = (P, Hk, KV8_PAGE, D), (P, Hk, D, KV8_PAGE), (P, Hk)
+    p, quick = None, _quick()
+    if quick:
+        pointers, _, e4m3, _, f32, i32, _ = quick
+        p = pointers(dev, kc, e4m3, keys, ks, f32, scales, vc, e4m3, values, vs, f32, scales, starts, i32, 4 * (B + 1),
+                     lengths, i32, 4 * B, table, i32, 0)
+    if p is None:
+        e4m3, _, f32, i32 = _fp8_formats()
+        p = (_shaped_ptr(kc, keys, "kc", dev, e4m3), _shaped_ptr(ks, scales, "ks", dev, f32),
+             _shaped_ptr(vc, values, "vc", dev, e4m3), _shaped_ptr(vs, scales, "vs", dev, f32),
+             _ptr(starts, 4 * (B + 1), "starts", dev, i32), _ptr(lengths, 4 * B, "lengths", dev, i32),
+             _ptr(table, 0, "table", dev, i32))
+    return p, B, max_pages, P
 
 
 def svdq_kv8_append(K, V, starts, lengths, table, kc, ks, vc, vs, stream=None):
@@ -759,15 +806,14 @@ def svdq_kv8_append(K, V, starts, lengths, table, kc, ks, vc, vs, stream=None):
     vs [pages, Hk]; starts [B + 1], lengths [B] and table [B, max_pages] int32 say
     which rows are whose and where they go."""
     dev = _current_device()
-    e4m3, bf16, f32, i32 = _fp8_formats()
-    kp, kst, shape = _dev_heads(K, "K", dev, bf16)
-    vp, vst, other = _dev_heads(V, "V", dev, bf16)
+    kp, kst, *shape = _dev_heads(K, "K", dev)
+    vp, vst, *other = _dev_heads(V, "V", dev)
     if other != shape:
-        raise ValueError(f"V is {list(other)}, K {list(shape)}")
+        raise ValueError(f"V is {other}, K {shape}")
     T, Hk, D = shape
-    B, max_pages, batch = _kv8_batch(starts, lengths, table, dev, i32)
-    P, cache = _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32)
-    st = lib().svdq_kv8_append(kp, kst, vp, vst, *batch, T, B, max_pages, P, Hk, D, *cache, _stream(stream))
+    p, B, max_pages, P = _kv8_tensors(kc, ks, vc, vs, starts, lengths, table, Hk, D, dev)
+    st = lib().svdq_kv8_append(kp, kst, vp, vst, p[4], p[5], p[6], T, B, max_pages, P, Hk, D, p[0], p[1], p[2], p[3],
+                               _stream(stream))
     _check("svdq_kv8_append", st)
 
 
@@ -782,16 +828,18 @@ def svdq_kv8_attention(Q, kc, ks, vc, vs, starts, lengths, table, scale, O, lse=
     the logarithms of the weights' sums. The library refuses a workspace (any
     contiguous GPU tensor) of too few bytes. The rest as svdq_kv8_append."""
     dev = _current_device()
-    e4m3, bf16, f32, i32 = _fp8_formats()
-    qp, qst, shape = _dev_heads(Q, "Q", dev, bf16)
-    T, Hq, D = shape
+    qp, qst, T, Hq, D = _dev_heads(Q, "Q", dev)
     Hk = kc.shape[1] if kc is not None and kc.dim() == 4 else 0
-    P, cache = _kv8_cache(kc, ks, vc, vs, Hk, D, dev, e4m3, f32)
-    B, max_pages, batch = _kv8_batch(starts, lengths, table, dev, i32)
-    wp, wb = _ws(workspace, dev)
-    st = lib().svdq_kv8_attention(qp, qst, *cache, *batch, T, B, max_pages, P, Hq, Hk, D, scale, 1 if causal else 0, window,
-                                  _ptr(O, T * Hq * D * 2, "O", dev, bf16), _shaped_ptr(lse, (T, Hq), "lse", dev, f32), wp,
-                                  wb, _stream(stream))
+    p, B, max_pages, P = _kv8_tensors(kc, ks, vc, vs, starts, lengths, table, Hk, D, dev)
+    out, quick = None, _quick()
+    if quick:
+        pointers, _, _, bf16, f32, _, _ = quick
+        out = pointers(dev, O, bf16, T * Hq * D * 2, lse, f32, (T, Hq), workspace, _ANY_KIND, 0)
+    if out is None:
+        _, bf16, f32, _ = _fp8_formats()
+        out = (_ptr(O, T * Hq * D * 2, "O", dev, bf16), _shaped_ptr(lse, (T, Hq), "lse", dev, f32), _ws(workspace, dev)[0])
+    st = lib().svdq_kv8_attention(qp, qst, *p, T, B, max_pages, P, Hq, Hk, D, scale, 1 if causal else 0, window, out[0],
+                                  out[1], out[2], 0 if workspace is None else workspace.nbytes, _stream(stream))
     _check("svdq_kv8_attention", st)
 
 

@@ -6,7 +6,8 @@ HIP sources are compiled by hipcc for gfx950 only; host C++ sources by the
 ROCm clang++. Objects go to ``_build/`` beside this file and the shared
 library to ``libsvdq.so`` in this package directory. The GELU table of the
 fused MLP epilogue is generated first (``gelu_table.py`` ->
-``_build/gelu_table.h``).
+``_build/gelu_table.h``). Beside the library, ``_tensors.so``: a small module
+for this Python and torch, which the binding does without where it is missing.
 """
 
 from __future__ import annotations
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 if __package__:
     from . import gelu_table
@@ -29,6 +31,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsvdq.so")
+TENSORS = os.path.join(PKG, "_tensors.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
@@ -54,6 +57,20 @@ def _run(cmd):
     return p.stdout
 
 
+def _tensors_job():
+    """How _tensors.so is built, or None without torch."""
+    try:
+        import torch
+        from torch.utils.cpp_extension import include_paths
+    except ImportError:
+        return None
+    include = [x for path in [*include_paths(), sysconfig.get_paths()["include"]] for x in ("-isystem", path)]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [CLANGXX, "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden", "-Wall", *include,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "python", "tensors.cpp"),
+            "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", TENSORS + ".tmp"]
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     gelu_table.write(os.path.join(BUILD, "gelu_table.h"))
@@ -67,7 +84,17 @@ def build(verbose: bool = False) -> str:
         jobs.append([CLANGXX] + CXX_FLAGS + ["-c", src, "-o", obj])
     workers = max(1, min(len(jobs), int(os.environ.get("MAX_JOBS", "8"))))
     with cf.ThreadPoolExecutor(workers) as ex:
+        tensors = _tensors_job()
+        module = tensors and ex.submit(_run, tensors)
         outs = list(ex.map(_run, jobs))
+        if module:
+            try:
+                outs.append(module.result())
+                shutil.move(tensors[-1], TENSORS)
+            except RuntimeError as e:
+                if os.path.exists(TENSORS):
+                    os.remove(TENSORS)
+                print(f"{TENSORS} is left out: {e}", file=sys.stderr)
     if verbose:
         for o in outs:
             if o.strip():
