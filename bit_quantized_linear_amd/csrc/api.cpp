@@ -661,7 +661,8 @@ svdq_status svdq_kv8_attention(const uint16_t *Q, int64_t q_stride, const uint8_
     if (st == SVDQ_OK) st = check_kv8_queries(T, B, Hq, Hk);
     if (st == SVDQ_OK) st = check_rows(q_stride, (int64_t)Hq * D);
     if (st != SVDQ_OK) return st;
-    if (!(scale > 0.0f) || std::isinf(scale) || window < 0 || (window > 0 && !causal)) return SVDQ_ERR_INVALID_ARGUMENT;
+    // the kernels multiply scale by log2 e
+    if (!(scale > 0.0f) || scale > 0x1p126f || window < 0 || (window > 0 && !causal)) return SVDQ_ERR_INVALID_ARGUMENT;
     if (!kc || !ks || !vc || !vs || (T > 0 && (!Q || !O)) || !starts || (B > 0 && (!lengths || !table)))
         return SVDQ_ERR_INVALID_ARGUMENT;
     const size_t need = svdq::kv8_attention_workspace(T, B, max_pages, Hq, Hk, D);

@@ -664,7 +664,7 @@ size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, i
  *   with causal != 0 token i of n new ones is at position p = lengths[b] - n + i
  *   and sees the tokens up to p, with window > 0 only the last `window` of them
  *   (itself among them); with causal == 0 (text or frames that a diffusion model
- *   looks at) every token of its sequence.
+ *   looks at) every token of its sequence, and window must be 0.
  *   A query that sees nothing has 0 for its output. Tokens that a query does not
  *   see have no part in its output, NaN or infinities in their place or not.
  * Head hq of a query uses the keys and values of head hq / (Hq / Hk).
@@ -672,7 +672,7 @@ size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, i
  * (the codes' values, exact; weights rounded to bf16, and values times a scale
  * that is no power of two); one rounding to bf16.
  * In:  Q bf16, head h of row t at Q + t q_stride + h D (stride in elements);
- *      scale finite and > 0.
+ *      0 < scale <= 2^126.
  * Out: O [T, Hq, D] bf16; lse [T, Hq] fp32 or NULL: the natural logarithm of the
  *      sum of exp(scale q . k_t) over what is seen (-infinity for nothing), with
  *      which outputs over parts of a context can be joined.

@@ -231,3 +231,13 @@ def test_other_tensors_are_contiguous(call, name, guarded):
 def test_a_missing_workspace_reaches_the_library_which_refuses_it(guarded):
     with pytest.raises(Reached):
         CALLS["attention"][0](tensors("attention", workspace=None))
+
+
+def test_scales_that_overflow():
+    """Scores are base-2 logarithms: the scale times log2 e has to be a number."""
+    assert attention(scale=2.0 ** 126.5) == INVALID and attention(scale=3.4e38) == INVALID
+    b.svdq_debug_set_arch_override("gfx950")
+    try:
+        assert attention(T=0, Q=None, ws=None, scale=2.0 ** 126) == b.SVDQ_OK
+    finally:
+        b.svdq_debug_set_arch_override(None)
