@@ -987,6 +987,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
 // 58 us in 32 parts, 735 in one; 1000 tokens alone, 8 heads: 36 in one, 70 in two).
 constexpr int kCus = 256;
 constexpr int kAlonePages = 16, kDeepPages = 128, kDeepPart = 64;
+constexpr int kIdle = kCus * 3 / 4;
 constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
 
 // How a call is cut: which kernel, its queries per block (`rows`), the blocks of a
@@ -996,19 +997,21 @@ constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
 // queries 78 us, 64 queries 108, 164 both with 128 to a block; 128 queries 170 with
 // 128, 193 twice 64, 229 with 256; 100 queries after 8000 alone 22, 26 and 24; 64
 // sequences of 128 queries after 500 51, 47 and 59; of 256 queries 98 with 128, 72
-// with 256; 200 queries after 500 alone 17 and 20).
+// with 256). But 128, not 256, where blocks of 256 would leave a quarter of the compute
+// units idle (32 / 8 heads: 256 tokens alone 17 us against 20, 1000 30.6 and 33.7,
+// 1400, 176 blocks of 256, 38 and 43, 2000, 256 blocks, 62 and 59; 64 after 8000 29 and
+// 33, after 32000, in 32 parts, 62 and 56).
 struct AttnPlan {
     bool few, sorted;
     int rows, tiles, splits;
 };
 
-AttnPlan attn_plan(int T, int B, int pages, int Hk, int group) {
+// A plan with blocks of `rows` queries.
+AttnPlan attn_plan_of(int rows, int64_t queries, int B, int pages, int Hk) {
     AttnPlan p;
-    const int64_t queries = (int64_t)T * group;
-    p.rows = kDecRows;
-    while (p.rows < 256 && queries > (int64_t)p.rows * B) p.rows *= 2;
-    p.few = p.rows <= 64;
-    p.tiles = p.few ? B : (int)((queries + (int64_t)(p.rows - 1) * B) / p.rows);
+    p.rows = rows;
+    p.few = rows <= 64;
+    p.tiles = p.few ? B : (int)((queries + (int64_t)(rows - 1) * B) / rows);
     // more blocks than units: in order, where the sequences fit a wave
     p.sorted = !p.few && B > 1 && B <= 64 && (int64_t)p.tiles * Hk > kCus;
     p.splits = 1;
@@ -1030,6 +1033,14 @@ AttnPlan attn_plan(int T, int B, int pages, int Hk, int group) {
         }
     }
     return p;
+}
+
+AttnPlan attn_plan(int T, int B, int pages, int Hk, int group) {
+    const int64_t queries = (int64_t)T * group;
+    int rows = kDecRows;
+    while (rows < 256 && queries > (int64_t)rows * B) rows *= 2;
+    const AttnPlan p = attn_plan_of(rows, queries, B, pages, Hk);
+    return rows == 256 && (int64_t)p.tiles * Hk * p.splits <= kIdle ? attn_plan_of(128, queries, B, pages, Hk) : p;
 }
 
 template <int D>
@@ -1054,7 +1065,9 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
     // of 128: 5.2 us, in parts of the context 8.1; 64 tokens after 8000, 512: 16.6, 19.7)
     if (window > 0) {
         const int64_t pages = ((int64_t)window + kv.T + kKvPage - 3) / kKvPage + 1;
-        if (pages < kv.max_pages) plan.splits = std::min(plan.splits, attn_plan(kv.T, kv.B, (int)pages, Hk, Hq / Hk).splits);
+        const int most = plan.splits;
+        if (pages < kv.max_pages) plan = attn_plan(kv.T, kv.B, (int)pages, Hk, Hq / Hk);
+        plan.splits = std::min(plan.splits, most);
     }
     const AttnArgs a{kv, Q,  q_stride, kc,  vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal,
                      std::min(window, 1 << 30),  // no position is further

@@ -98,3 +98,12 @@ def test_windows_much_shorter_than_the_context(new, window):
     """As many parts as the window's pages ask for, fewer than the workspace holds."""
     for D in (64, 128):
         run(new + D, [20000, 300], [new, 1], 4, 2, D, window=window)
+
+
+@pytest.mark.parametrize("lengths,new,Hq,Hk,kw", [
+    ([300], [300], 8, 2, {}), ([700, 40], [600, 40], 8, 8, {}), ([5000], [300], 16, 2, {}), ([5000], [300], 16, 2, {"window": 700}),
+    ([3000, 200], [1000, 200], 4, 1, {"causal": False}), ([1400], [1400], 32, 8, {}), ([4000], [1100], 8, 8, {"window": 100})])
+def test_prompts_that_leave_units_idle(lengths, new, Hq, Hk, kw):
+    """More than 128 queries of a key head, in blocks of 128."""
+    for D in (64, 128):
+        run(sum(lengths) + D, lengths, new, Hq, Hk, D, **kw)
