@@ -983,8 +983,10 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
 // up to 16 pages (500 tokens: 7.0 in one, 8.9 in two; 1000: 9.5 and 8.8, but a launch
 // less, 3.4 on the host).
 // Prompts: what takes least by the time of a page in a block, of the second launch
-// and of a query's part on its way through memory (64 tokens after 32000, 8 heads:
-// 58 us in 32 parts, 735 in one; 1000 tokens alone, 8 heads: 36 in one, 70 in two).
+// and of a query's part on its way through memory (32 / 8 heads: 64 tokens after 32000
+// 57 us in 32 parts, 583 in one; after 8000 30, in all parts that there is room for 33,
+// in one 156; 1000 tokens alone 30 in one, 38 in two; 16 / 2 heads: 300 tokens after
+// 3000 29, 48 in all, 71 in one).
 constexpr int kCus = 256;
 constexpr int kAlonePages = 16, kDeepPages = 128, kDeepPart = 64;
 constexpr int kIdle = kCus * 3 / 4;
