@@ -7,8 +7,8 @@
 //   m' = max(m, max s_t),  p_t = 2^(s_t - m'),  l' = l 2^(m - m') + sum p_t,
 //   O' = O 2^(m - m') + sum (p_t vs) v_t
 // with vs the page's value scale. Products run on the bf16 matrix core: E4M3
-// codes are exact in bf16, p vs is rounded to bf16 (2^-9 of each weight; vs is a
-// power of two), sums and statistics are fp32.
+// codes are exact in bf16, p vs is rounded to bf16 (2^-8 of each weight at most; vs
+// is a power of two), sums and statistics are fp32.
 //
 // Both kernels compute S^T = K Q^T and O^T = V^T P^T, so that a lane holds one
 // query: its statistics need no broadcast, and the weights of S^T are the next
@@ -1071,9 +1071,9 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
         if (pages < kv.max_pages) plan = attn_plan(kv.T, kv.B, (int)pages, Hk, Hq / Hk);
         plan.splits = std::min(plan.splits, most);
     }
-    const AttnArgs a{kv, Q,  q_stride, kc,  vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal,
-                     std::min(window, 1 << 30),  // no position is further
-                                         O,  lse, plan.sorted, static_cast<float *>(workspace), plan.splits};
+    window = std::min(window, 1 << 30);  // no position is further
+    const AttnArgs a{kv, Q, q_stride, kc, vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal, window,
+                     O, lse, plan.sorted, static_cast<float *>(workspace), plan.splits};
     if (plan.few)
         hipLaunchKernelGGL(D == 64 ? decode_kernel<64>(plan.rows) : decode_kernel<128>(plan.rows),
                            dim3((unsigned)plan.splits, (unsigned)Hk, (unsigned)kv.B), dim3(64 * kDecWaves), 0, stream, a);
@@ -1083,9 +1083,8 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
     else
         hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 8> : kv8_prompt_kernel<128, 8>),
                            dim3((unsigned)(plan.tiles * Hk), (unsigned)plan.splits), dim3(512), 0, stream, a, plan.tiles);
-    if (plan.splits == 1) return hipGetLastError();
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || plan.splits == 1) return e;
     const int64_t queries = (int64_t)kv.T * Hq;
     if (plan.splits <= kJoinAlone)
         hipLaunchKernelGGL((D == 64 ? kv8_join_kernel<64, 1> : kv8_join_kernel<128, 1>), dim3((unsigned)((queries + 3) / 4)),
