@@ -95,8 +95,9 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 
 constexpr int kDecWaves = 4;
 constexpr int kDecRows = 16;  // of a matrix-core tile
+constexpr int kMostSequences = 65535;  // of a call, and of a grid's last dimension
 
-// A block takes up to 16, 32 or 64 queries at a time and a run of the sequence's
+// A block takes up to 16, 32 or 64 queries of a sequence and a run of its
 // pages, its waves every fourth of them (or every second, half of the queries each),
 // straight into registers: the next page's keys as soon as this one's scores are
 // there, its values as soon as this one's are multiplied. A wave takes QT tiles of 16
@@ -120,246 +121,262 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
     __shared__ float m_s[kDecWaves][kDecRows], l_s[kDecWaves][kDecRows];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q16 = lane & 15, g4 = lane >> 4;
-    const int split = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
-    const KvSeq seq = kv_seq(a.kv, b);
-    const int rows = seq.rows * a.group;
+    const int split = blockIdx.x;
     const int wp = wave / WR, wr = wave % WR * QT;  // which pages are the wave's, and the first of its tiles
-    for (int r0 = 0; r0 < rows; r0 += kRows) {
-        const int last = min(r0 + kRows, rows) - 1;
-        int low[QT], high[QT], low0, high0, low1, high1;
+    // The first queries of each sequence, then the others of those that have more (256
+    // tokens among 31 of one each, after 4000, 32 / 8 heads: 111 us, 946 where a
+    // sequence's queries are one block's)
+    int head = blockIdx.y, b = blockIdx.z, r0 = 0;
+    if (head >= a.Hk) {
+        head -= a.Hk;
+        b += kMostSequences;
+    }
+    KvSeq seq;
+    if (b < a.kv.B) {
+        seq = kv_seq(a.kv, b);
+    } else {
+        int nth;
+        if (!kv_find(a.kv, b - a.kv.B, b, seq, nth, [&](const KvSeq &s) { return max(s.rows * a.group - 1, 0) / kRows; })) return;
+        r0 = (nth + 1) * kRows;
+    }
+    const int rows = seq.rows * a.group;
+    if (r0 >= rows) return;
+    const int last = min(r0 + kRows, rows) - 1;
+    int low[QT], high[QT], low0, high0, low1, high1;
 #pragma unroll
-        for (int t = 0; t < QT; ++t) kv_seen(a, seq, min(r0 + kDecRows * (wr + t) + q16, last) / a.group, low[t], high[t]);
-        kv_seen(a, seq, r0 / a.group, low0, high0);
-        kv_seen(a, seq, last / a.group, low1, high1);
-        // low0 <= low[t] <= low1 and high0 <= high[t] <= high1
-        const int first_page = low0 / kKvPage, pages = max(0, (high1 + kKvPage - 1) / kKvPage - first_page);
-        const int per = (pages + a.splits - 1) / a.splits;
-        const int p0 = first_page + split * per, p1 = min(p0 + per, first_page + pages);
+    for (int t = 0; t < QT; ++t) kv_seen(a, seq, min(r0 + kDecRows * (wr + t) + q16, last) / a.group, low[t], high[t]);
+    kv_seen(a, seq, r0 / a.group, low0, high0);
+    kv_seen(a, seq, last / a.group, low1, high1);
+    // low0 <= low[t] <= low1 and high0 <= high[t] <= high1
+    const int first_page = low0 / kKvPage, pages = max(0, (high1 + kKvPage - 1) / kKvPage - first_page);
+    const int per = (pages + a.splits - 1) / a.splits;
+    const int p0 = first_page + split * per, p1 = min(p0 + per, first_page + pages);
 
-        if (wp < QT) {  // a tile's queries to LDS
-            const int r = min(r0 + kDecRows * (wr + wp) + q16, last);
-            const uint16_t *src = a.Q + (int64_t)(seq.row0 + r / a.group) * a.q_stride +
-                                  (int64_t)(head * a.group + r % a.group) * D + 16 * g4;
+    if (wp < QT) {  // a tile's queries to LDS
+        const int r = min(r0 + kDecRows * (wr + wp) + q16, last);
+        const uint16_t *src = a.Q + (int64_t)(seq.row0 + r / a.group) * a.q_stride +
+                              (int64_t)(head * a.group + r % a.group) * D + 16 * g4;
 #pragma unroll
-            for (int i = 0; i < 2 * KC; ++i) q_s[wr + wp][i][lane] = bitcast<u32x4>(src + 64 * (i / 2) + 8 * (i & 1));
-        }
-        __syncthreads();
-        float m[QT], l[QT];
-        f32x4 o[QT][DT];
+        for (int i = 0; i < 2 * KC; ++i) q_s[wr + wp][i][lane] = bitcast<u32x4>(src + 64 * (i / 2) + 8 * (i & 1));
+    }
+    __syncthreads();
+    float m[QT], l[QT];
+    f32x4 o[QT][DT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        m[t] = -INFINITY;
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // lane i: page p0 + wp + kStride (first + i) of the sequence
+    int number = -1, first = 0;
+    float factor = 0.0f, vs = 0.0f;
+    auto look_up = [&](int from) __attribute__((always_inline)) {
+        first = from;
+        const int p = p0 + wp + kStride * (from + lane);
+        number = p < p1 ? kv_page(a.kv, b, p) : -1;
+        const int64_t unit = (int64_t)max(number, 0) * a.Hk + head;
+        factor = fmaxf(a.ks[unit] * a.scale, kLeastFactor);
+        vs = number >= 0 ? a.vs[unit] : 0.0f;
+    };
+    u32x4 k[4][KC], v[DT];
+    auto unit_of = [&](int i) {
+        return (int64_t)max(__builtin_amdgcn_readlane(number, i - first), 0) * a.Hk + head;
+    };
+    auto load_keys = [&](int i) __attribute__((always_inline)) {
+        const uint8_t *kp = a.kc + unit_of(i) * kKvPage * D;
+        // tile j's row i is token 16 (i / 4) + 4 j + i % 4
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int n = 0; n < KC; ++n)
+                k[j][n] = bitcast<u32x4>(kp + (16 * (q16 >> 2) + 4 * j + (q16 & 3)) * D + 64 * n + 16 * g4);
+    };
+    auto load_values = [&](int i) __attribute__((always_inline)) {
+        const uint8_t *vp = a.vc + unit_of(i) * kKvPage * D;
+#pragma unroll
+        for (int n = 0; n < DT; ++n) v[n] = bitcast<u32x4>(vp + (16 * n + q16) * kKvPage + 16 * g4);
+    };
+    const int count = p1 > p0 + wp ? (p1 - p0 - wp + kStride - 1) / kStride : 0;
+    if (count > 0) {
+        look_up(0);
+        load_keys(0);
+        // the loop's order: its waits for keys then leave values under way (67 us against 72, 32 sequences)
+        __builtin_amdgcn_sched_barrier(0);
+        load_values(0);
+    }
+    for (int i = 0; i < count; ++i) {
+        const int p = p0 + wp + kStride * i;
+        const bool there = __builtin_amdgcn_readlane(number, i - first) >= 0, more = i + 1 < count;
+        const float c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(factor), i - first));
+        const float vscale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), i - first));
+        const int t0 = p * kKvPage;
+        // a page that some query does not see whole: hidden tokens' weights are
+        // 0, and their values are not multiplied, as they may be NaN. Of a page
+        // that is not there, all are hidden
+        const bool cut = !there || t0 < low1 || t0 + kKvPage > high0;
+        uint32_t nan = 0;
+        bf16x8 w[QT][2];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            m[t] = -INFINITY;
-            l[t] = 0.0f;
+            f32x4 s[4];
+            bf16x8 q[2 * KC];
 #pragma unroll
-            for (int i = 0; i < DT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-
-        // lane i: page p0 + wp + kStride (first + i) of the sequence
-        int number = -1, first = 0;
-        float factor = 0.0f, vs = 0.0f;
-        auto look_up = [&](int from) __attribute__((always_inline)) {
-            first = from;
-            const int p = p0 + wp + kStride * (from + lane);
-            number = p < p1 ? kv_page(a.kv, b, p) : -1;
-            const int64_t unit = (int64_t)max(number, 0) * a.Hk + head;
-            factor = fmaxf(a.ks[unit] * a.scale, kLeastFactor);
-            vs = number >= 0 ? a.vs[unit] : 0.0f;
-        };
-        u32x4 k[4][KC], v[DT];
-        auto unit_of = [&](int i) {
-            return (int64_t)max(__builtin_amdgcn_readlane(number, i - first), 0) * a.Hk + head;
-        };
-        auto load_keys = [&](int i) __attribute__((always_inline)) {
-            const uint8_t *kp = a.kc + unit_of(i) * kKvPage * D;
-            // tile j's row i is token 16 (i / 4) + 4 j + i % 4
+            for (int n = 0; n < 2 * KC; ++n) q[n] = __builtin_bit_cast(bf16x8, q_s[wr + t][n][lane]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                __builtin_amdgcn_sched_barrier(0);  // few converted operands at a time: registers
+                s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int n = 0; n < KC; ++n) {
+                    s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][n][0], k[j][n][1]), q[2 * n], s[j]);
+                    s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][n][2], k[j][n][3]), q[2 * n + 1], s[j]);
+                }
+            }
+            if (QT > 1) __builtin_amdgcn_sched_barrier(0);
+            if (t < QT - 1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int n = 0; n < KC; ++n) asm volatile("" : "+v"(k[j][n]));  // widened again for each tile: registers
+            } else if (more) {
+                if (i + 1 - first == 64) look_up(i + 1);
+                load_keys(i + 1);
+            }
+            if (cut) {
+                if (t == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t mask = byte_mask(t0 + 16 * g4 + 4 * j, low0, there ? high1 : 0);
+#pragma unroll
+                        for (int n = 0; n < DT; ++n) {
+                            v[n][j] &= mask;
+                            nan |= nan_codes(v[n][j]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t see = byte_mask(t0 + 16 * g4 + 4 * j, low[t], there ? high[t] : 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[j][e] = see >> (8 * e) & 1 ? s[j][e] : -INFINITY;
+                }
+            }
+            float top = s[0][0];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int n = 0; n < KC; ++n)
-                    k[j][n] = bitcast<u32x4>(kp + (16 * (q16 >> 2) + 4 * j + (q16 & 3)) * D + 64 * n + 16 * g4);
-        };
-        auto load_values = [&](int i) __attribute__((always_inline)) {
-            const uint8_t *vp = a.vc + unit_of(i) * kKvPage * D;
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[j][e]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m_new = fmaxf(m[t], top * c);
+            const float base = m_new == -INFINITY ? 0.0f : m_new;
+            const float alpha = exp2_of(m[t] - base);
+            m[t] = m_new;
+            l[t] *= alpha;
 #pragma unroll
-            for (int n = 0; n < DT; ++n) v[n] = bitcast<u32x4>(vp + (16 * n + q16) * kKvPage + 16 * g4);
-        };
-        const int count = p1 > p0 + wp ? (p1 - p0 - wp + kStride - 1) / kStride : 0;
-        if (count > 0) {
-            look_up(0);
-            load_keys(0);
-            load_values(0);
+            for (int n = 0; n < DT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][n][e] *= alpha;
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[4 * j + e] = exp2_of(__builtin_fmaf(s[j][e], c, -base));
+                    l[t] += x[4 * j + e];
+                }
+            w[t][0] = pack8(x, vscale);
+            w[t][1] = pack8(x + 8, vscale);
         }
-        for (int i = 0; i < count; ++i) {
-            const int p = p0 + wp + kStride * i;
-            const bool there = __builtin_amdgcn_readlane(number, i - first) >= 0, more = i + 1 < count;
-            const float c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(factor), i - first));
-            const float vscale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), i - first));
-            const int t0 = p * kKvPage;
-            // a page that some query does not see whole: hidden tokens' weights are
-            // 0, and their values are not multiplied, as they may be NaN. Of a page
-            // that is not there, all are hidden
-            const bool cut = !there || t0 < low1 || t0 + kKvPage > high0;
-            uint32_t nan = 0;
-            bf16x8 w[QT][2];
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                f32x4 s[4];
-                bf16x8 q[2 * KC];
-#pragma unroll
-                for (int n = 0; n < 2 * KC; ++n) q[n] = __builtin_bit_cast(bf16x8, q_s[wr + t][n][lane]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    __builtin_amdgcn_sched_barrier(0);  // few converted operands at a time: registers
-                    s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int n = 0; n < KC; ++n) {
-                        s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][n][0], k[j][n][1]), q[2 * n], s[j]);
-                        s[j] = mfma_bf16_16x16x32(fp8_widen8(k[j][n][2], k[j][n][3]), q[2 * n + 1], s[j]);
-                    }
-                }
-                if (QT > 1) __builtin_amdgcn_sched_barrier(0);
-                if (t < QT - 1) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int n = 0; n < KC; ++n) asm volatile("" : "+v"(k[j][n]));  // widened again for each tile: registers
-                } else if (more) {
-                    if (i + 1 - first == 64) look_up(i + 1);
-                    load_keys(i + 1);
-                }
-                if (cut) {
-                    if (t == 0) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t mask = byte_mask(t0 + 16 * g4 + 4 * j, low0, there ? high1 : 0);
-#pragma unroll
-                            for (int n = 0; n < DT; ++n) {
-                                v[n][j] &= mask;
-                                nan |= nan_codes(v[n][j]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t see = byte_mask(t0 + 16 * g4 + 4 * j, low[t], there ? high[t] : 0);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[j][e] = see >> (8 * e) & 1 ? s[j][e] : -INFINITY;
-                    }
-                }
-                float top = s[0][0];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[j][e]);
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float m_new = fmaxf(m[t], top * c);
-                const float base = m_new == -INFINITY ? 0.0f : m_new;
-                const float alpha = exp2_of(m[t] - base);
-                m[t] = m_new;
-                l[t] *= alpha;
-#pragma unroll
-                for (int n = 0; n < DT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[t][n][e] *= alpha;
-                float x[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[4 * j + e] = exp2_of(__builtin_fmaf(s[j][e], c, -base));
-                        l[t] += x[4 * j + e];
-                    }
-                w[t][0] = pack8(x, vscale);
-                w[t][1] = pack8(x + 8, vscale);
-            }
-            if (__any(nan != 0)) {  // NaN reaches the queries that see its token, and no other
-#pragma unroll
-                for (int n = 0; n < DT; ++n) {
-                    u32x4 one;  // the code of 1 for each NaN, which becomes 0 itself
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t at = (nan_codes(v[n][j]) >> 7) * 0xFFu;
-                        one[j] = at & 0x38383838u;
-                        v[n][j] &= ~at;
-                    }
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        f32x4 count = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            u32x4 seen;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t two = byte_mask(t0 + 16 * g4 + 8 * u + 2 * e, low[t], high[t]);
-                                seen[e] = (two & 1 ? 0x3F80u : 0u) | (two & 0x100u ? 0x3F800000u : 0u);
-                            }
-                            count = mfma_bf16_16x16x32(fp8_widen8(one[2 * u], one[2 * u + 1]),
-                                                       __builtin_bit_cast(bf16x8, seen), count);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[t][n][e] = count[e] > 0.0f ? NAN : o[t][n][e];
-                    }
-                }
-            }
+        if (__any(nan != 0)) {  // NaN reaches the queries that see its token, and no other
 #pragma unroll
             for (int n = 0; n < DT; ++n) {
-                if (QT > 1 || n % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+                u32x4 one;  // the code of 1 for each NaN, which becomes 0 itself
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const bf16x8 value = fp8_widen8(v[n][2 * u], v[n][2 * u + 1]);
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) o[t][n] = mfma_bf16_16x16x32(value, w[t][u], o[t][n]);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t at = (nan_codes(v[n][j]) >> 7) * 0xFFu;
+                    one[j] = at & 0x38383838u;
+                    v[n][j] &= ~at;
                 }
-            }
-            if (more) load_values(i + 1);
-        }
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {  // the waves' sums of a tile
-            const int first_row = r0 + kDecRows * t;
-            if (first_row > last) break;
-            l[t] += __shfl_xor(l[t], 16);
-            l[t] += __shfl_xor(l[t], 32);
-            if (g4 == 0) {
-                m_s[wave][q16] = m[t];
-                l_s[wave][q16] = l[t];
-            }
+                for (int t = 0; t < QT; ++t) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    f32x4 count = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4 *>(&o_s[wave][q16][16 * i + 4 * g4]) = o[t][i];
-            __syncthreads();
-            for (int i = tid; i < WR * kDecRows * D / 4; i += 64 * kDecWaves) {
-                const int part = i / (kDecRows * D / 4), row = i / (D / 4) % kDecRows, d = i % (D / 4) * 4;
-                const int r = first_row + kDecRows * QT * part + row;
-                if (r > last) continue;
-                float top = -INFINITY, sum = 0.0f;
+                    for (int u = 0; u < 2; ++u) {
+                        u32x4 seen;
 #pragma unroll
-                for (int w = part; w < kDecWaves; w += WR) top = fmaxf(top, m_s[w][row]);
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = part; w < kDecWaves; w += WR) {
-                    const float f = top == -INFINITY ? 1.0f : exp2_of(m_s[w][row] - top);
-                    sum += l_s[w][row] * f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] += o_s[w][row][d + e] * f;
-                }
-                const int64_t at = (int64_t)(seq.row0 + r / a.group) * a.Hq + head * a.group + r % a.group;
-                if (a.splits == 1) {
-                    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    *reinterpret_cast<u32x2 *>(a.O + at * D + d) =
-                        u32x2{bf16x2_bits(acc[0] * f, acc[1] * f), bf16x2_bits(acc[2] * f, acc[3] * f)};
-                    if (a.lse && d == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
-                } else {
-                    *reinterpret_cast<f32x4 *>(a.part + (at * a.splits + split) * D + d) = acc;
-                    if (d == 0) {
-                        float *ml = a.part + (int64_t)a.kv.T * a.Hq * a.splits * D + (at * a.splits + split) * 2;
-                        ml[0] = top;
-                        ml[1] = sum;
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t two = byte_mask(t0 + 16 * g4 + 8 * u + 2 * e, low[t], high[t]);
+                            seen[e] = (two & 1 ? 0x3F80u : 0u) | (two & 0x100u ? 0x3F800000u : 0u);
+                        }
+                        count = mfma_bf16_16x16x32(fp8_widen8(one[2 * u], one[2 * u + 1]),
+                                                   __builtin_bit_cast(bf16x8, seen), count);
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][n][e] = count[e] > 0.0f ? NAN : o[t][n][e];
                 }
             }
-            __syncthreads();
         }
+#pragma unroll
+        for (int n = 0; n < DT; ++n) {
+            if (QT > 1 || n % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 value = fp8_widen8(v[n][2 * u], v[n][2 * u + 1]);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) o[t][n] = mfma_bf16_16x16x32(value, w[t][u], o[t][n]);
+            }
+        }
+        if (more) load_values(i + 1);
+    }
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {  // the waves' sums of a tile
+        const int first_row = r0 + kDecRows * t;
+        if (first_row > last) break;
+        l[t] += __shfl_xor(l[t], 16);
+        l[t] += __shfl_xor(l[t], 32);
+        if (g4 == 0) {
+            m_s[wave][q16] = m[t];
+            l_s[wave][q16] = l[t];
+        }
+#pragma unroll
+        for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4 *>(&o_s[wave][q16][16 * i + 4 * g4]) = o[t][i];
+        __syncthreads();
+        for (int i = tid; i < WR * kDecRows * D / 4; i += 64 * kDecWaves) {
+            const int part = i / (kDecRows * D / 4), row = i / (D / 4) % kDecRows, d = i % (D / 4) * 4;
+            const int r = first_row + kDecRows * QT * part + row;
+            if (r > last) continue;
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = part; w < kDecWaves; w += WR) top = fmaxf(top, m_s[w][row]);
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = part; w < kDecWaves; w += WR) {
+                const float f = top == -INFINITY ? 1.0f : exp2_of(m_s[w][row] - top);
+                sum += l_s[w][row] * f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] += o_s[w][row][d + e] * f;
+            }
+            const int64_t at = (int64_t)(seq.row0 + r / a.group) * a.Hq + head * a.group + r % a.group;
+            if (a.splits == 1) {
+                const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+                *reinterpret_cast<u32x2 *>(a.O + at * D + d) =
+                    u32x2{bf16x2_bits(acc[0] * f, acc[1] * f), bf16x2_bits(acc[2] * f, acc[3] * f)};
+                if (a.lse && d == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
+            } else {
+                *reinterpret_cast<f32x4 *>(a.part + (at * a.splits + split) * D + d) = acc;
+                if (d == 0) {
+                    float *ml = a.part + (int64_t)a.kv.T * a.Hq * a.splits * D + (at * a.splits + split) * 2;
+                    ml[0] = top;
+                    ml[1] = sum;
+                }
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -1074,10 +1091,13 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
     window = std::min(window, 1 << 30);  // no position is further
     const AttnArgs a{kv, Q, q_stride, kc, vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal, window,
                      O, lse, plan.sorted, static_cast<float *>(workspace), plan.splits};
-    if (plan.few)
+    if (plan.few) {
+        const int blocks = kv.B + (int)((int64_t)kv.T * (Hq / Hk) / plan.rows);  // of a head and part: at most 2 B
+        const bool more = blocks > kMostSequences;
         hipLaunchKernelGGL(D == 64 ? decode_kernel<64>(plan.rows) : decode_kernel<128>(plan.rows),
-                           dim3((unsigned)plan.splits, (unsigned)Hk, (unsigned)kv.B), dim3(64 * kDecWaves), 0, stream, a);
-    else if (plan.rows == 128)
+                           dim3((unsigned)plan.splits, (unsigned)(more ? 2 * Hk : Hk), (unsigned)(more ? kMostSequences : blocks)),
+                           dim3(64 * kDecWaves), 0, stream, a);
+    } else if (plan.rows == 128)
         hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 4> : kv8_prompt_kernel<128, 4>),
                            dim3((unsigned)(plan.tiles * Hk), (unsigned)plan.splits), dim3(256), 0, stream, a, plan.tiles);
     else

@@ -7,7 +7,9 @@ Tolerances as in tests/test_gpu_kv8.py and tests/test_gpu_kv8_paths.py.
 import numpy as np
 import pytest
 
+from bit_quantized_linear_amd import binding as b
 from oracle import decoder as od
+from tests import gpu_harness as H
 from tests.test_gpu_kv8 import PAGE, attend, attention_case, bf16_values, check, plan, poison, random_cache
 from tests.test_gpu_kv8_paths import run
 from tests.test_gpu_norm_rope import _gpu  # noqa: F401
@@ -107,3 +109,42 @@ def test_prompts_that_leave_units_idle(lengths, new, Hq, Hk, kw):
     """More than 128 queries of a key head, in blocks of 128."""
     for D in (64, 128):
         run(sum(lengths) + D, lengths, new, Hq, Hk, D, **kw)
+
+
+@pytest.mark.parametrize("lengths,new,Hq,Hk,kw", [
+    ([700] + [300] * 15, [200] + [1] * 15, 4, 1, {}), ([300] * 7 + [500], [1] * 7 + [100], 8, 2, {}),
+    ([200, 1, 900, 64, 65], [1, 0, 90, 2, 33], 4, 2, {}), ([3000] * 70, [1] * 40 + [33] + [2] * 29, 16, 2, {}),
+    ([4000, 100, 100, 100], [150, 1, 1, 1], 1, 1, {"window": 300}), ([4000, 100, 100, 100], [150, 1, 1, 1], 1, 1, {"causal": False})])
+def test_a_prompt_among_decoded_tokens(lengths, new, Hq, Hk, kw):
+    """Sequences with more queries than a block of the kernel for few takes."""
+    assert max(new) * (Hq // Hk) > 64 and sum(new) * (Hq // Hk) <= 64 * len(new)
+    for D in (64, 128):
+        run(sum(lengths) + D, lengths, new, Hq, Hk, D, **kw)
+
+
+def test_more_blocks_than_a_grid_dimension_has():
+    """50000 sequences of two pages' halves: every other one has two new tokens of 16
+    heads, two blocks, and the others have none."""
+    t, B, D, heads = H.torch(), 50000, 64, 16
+    gen = t.Generator(device="cuda").manual_seed(3)
+    codes = lambda *s: t.randn(s, generator=gen, device="cuda").mul_(64).to(t.float8_e4m3fn)  # noqa: E731
+    kc, vc = t.full((B, 1, 64, D), 0x7F, dtype=t.uint8, device="cuda"), t.full((B, 1, D, 64), 0xFF, dtype=t.uint8, device="cuda")
+    k, v = codes(B, 2, D), codes(B, 2, D)
+    kc[:, 0, :2], vc[:, 0, :, :2] = k.view(t.uint8), v.view(t.uint8).transpose(1, 2)
+    scale = t.full((B, 1), 2.0 ** -6, device="cuda")
+    new = t.tensor([2, 0], device="cuda").repeat(B // 2)
+    starts = t.cat([t.zeros(1, dtype=t.long, device="cuda"), new.cumsum(0)]).int()
+    q = t.randn((B, heads, D), generator=gen, device="cuda").bfloat16()
+    O = t.zeros((B, heads, D), dtype=t.bfloat16, device="cuda")  # noqa: E741
+    table = t.arange(B, dtype=t.int32, device="cuda")[:, None].contiguous()
+    assert b.svdq_kv8_attention_workspace_bytes(B, B, 1, heads, 1, D) == 0
+    b.svdq_kv8_attention(q, kc, scale, vc, scale, starts, new.int(), table, 0.125, O)
+    k, v = (x.float()[::2].double() / 64 for x in (k, v))
+    s = 0.125 * t.einsum("bthd,bud->bthu", q.double().view(B // 2, 2, heads, D), k)
+    s[:, 0, :, 1] = -float("inf")
+    p = t.softmax(s, -1)
+    want = (p[..., None] * v[:, None, None]).sum(-2).reshape(B, heads, D)
+    mag = (p[..., None] * v[:, None, None].abs()).sum(-2).reshape(B, heads, D)
+    off = (O.double() - want).abs()
+    # half steps of bf16 of the output and of each weight; scores of up to 128 terms, fp32
+    assert (off <= 2.0 ** -8 * want.abs() + mag * (2.0 ** -8 * (1 + 2.0 ** -7) + 2.0 ** -12)).all()
