@@ -157,8 +157,7 @@ hipError_t launch_fp8_norm(const uint16_t *X, const uint16_t *residual, const ui
     const NormArgs a{X, residual, w, eps, M, K, sum, Y, qx, sx};
     const auto launch = [&](auto kernel, int per_token) {
         const int threads = std::max(per_token, 256), tokens = threads / per_token;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)((M + tokens - 1) / tokens)), dim3((unsigned)threads), 0, stream, a);
-        return hipGetLastError();
+        return launch_kernel(kernel, dim3((unsigned)((M + tokens - 1) / tokens)), (unsigned)threads, stream, a);
     };
     // Short rows: several tokens a block, so that its threads have work (32760 x 256: 12.6
     // us against 49.7 with a block per token, x 1024: 47.9 against 66.5, x 2048: 95 and 85.5)

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "svdq.h"
 
@@ -114,6 +115,15 @@ size_t fp8_moe_workspace_size(int T, int I, int E, int top_k);
 hipError_t launch_fp8_moe(const uint16_t *X, const uint16_t *wr, const uint8_t *w13, const float *s13,
                           const uint8_t *w2, const float *s2, int T, int H, int I, int E, int top_k, bool renorm,
                           int32_t *idx, float *gate, void *workspace, uint16_t *Y, hipStream_t stream);
+
+// A launch without the detour through a pushed configuration that <<<>>> takes (0.2 us
+// of 2.3 on the host).
+template <class... P, class... A>
+hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, unsigned threads, hipStream_t stream, const A &...args) {
+    static_assert((std::is_same_v<P, A> && ...), "the kernel's own types");
+    void *p[] = {const_cast<void *>(static_cast<const void *>(&args))...};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), grid, dim3(threads), p, 0, stream);
+}
 
 // norm, rotary positions, 8-bit key and value cache (fp8_norm.hip, rope.hip, kv8_append.hip, kv8_attention.hip)
 hipError_t launch_fp8_norm(const uint16_t *X, const uint16_t *residual, const uint16_t *w, float eps, int M, int K,

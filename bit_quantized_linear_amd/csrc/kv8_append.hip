@@ -189,9 +189,7 @@ static int64_t append_pages(int T, int B) { return ((int64_t)T + 62LL * B) / kKv
 hipError_t launch_kv8_append(const KvBatch &kv, const uint16_t *K, int64_t k_stride, const uint16_t *V, int64_t v_stride,
                              int Hk, int D, uint8_t *kc, float *ks, uint8_t *vc, float *vs, hipStream_t stream) {
     const AppendArgs a{kv, K, V, k_stride, v_stride, Hk, D, kc, vc, ks, vs};
-    hipLaunchKernelGGL(kv8_append_kernel, dim3((unsigned)append_pages(kv.T, kv.B), 2u * (unsigned)Hk),
-                       dim3(kAppThreads), 0, stream, a);
-    return hipGetLastError();
+    return launch_kernel(kv8_append_kernel, dim3((unsigned)append_pages(kv.T, kv.B), 2u * (unsigned)Hk), kAppThreads, stream, a);
 }
 
 }  // namespace svdq

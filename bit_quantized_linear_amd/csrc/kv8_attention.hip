@@ -1091,28 +1091,25 @@ hipError_t launch_kv8_attention(const KvBatch &kv, const uint16_t *Q, int64_t q_
     window = std::min(window, 1 << 30);  // no position is further
     const AttnArgs a{kv, Q, q_stride, kc, vc, ks, vs, Hq, Hk, Hq / Hk, scale * 1.44269504088896340736f, causal, window,
                      O, lse, plan.sorted, static_cast<float *>(workspace), plan.splits};
+    hipError_t e;
     if (plan.few) {
         const int blocks = kv.B + (int)((int64_t)kv.T * (Hq / Hk) / plan.rows);  // of a head and part: at most 2 B
         const bool more = blocks > kMostSequences;
-        hipLaunchKernelGGL(D == 64 ? decode_kernel<64>(plan.rows) : decode_kernel<128>(plan.rows),
-                           dim3((unsigned)plan.splits, (unsigned)(more ? 2 * Hk : Hk), (unsigned)(more ? kMostSequences : blocks)),
-                           dim3(64 * kDecWaves), 0, stream, a);
-    } else if (plan.rows == 128)
-        hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 4> : kv8_prompt_kernel<128, 4>),
-                           dim3((unsigned)(plan.tiles * Hk), (unsigned)plan.splits), dim3(256), 0, stream, a, plan.tiles);
-    else
-        hipLaunchKernelGGL((D == 64 ? kv8_prompt_kernel<64, 8> : kv8_prompt_kernel<128, 8>),
-                           dim3((unsigned)(plan.tiles * Hk), (unsigned)plan.splits), dim3(512), 0, stream, a, plan.tiles);
-    const hipError_t e = hipGetLastError();
+        e = launch_kernel(D == 64 ? decode_kernel<64>(plan.rows) : decode_kernel<128>(plan.rows),
+                          dim3((unsigned)plan.splits, (unsigned)(more ? 2 * Hk : Hk), (unsigned)(more ? kMostSequences : blocks)),
+                          64 * kDecWaves, stream, a);
+    } else {
+        const dim3 grid((unsigned)(plan.tiles * Hk), (unsigned)plan.splits);
+        e = plan.rows == 128
+                ? launch_kernel(D == 64 ? kv8_prompt_kernel<64, 4> : kv8_prompt_kernel<128, 4>, grid, 256, stream, a, plan.tiles)
+                : launch_kernel(D == 64 ? kv8_prompt_kernel<64, 8> : kv8_prompt_kernel<128, 8>, grid, 512, stream, a, plan.tiles);
+    }
     if (e != hipSuccess || plan.splits == 1) return e;
     const int64_t queries = (int64_t)kv.T * Hq;
     if (plan.splits <= kJoinAlone)
-        hipLaunchKernelGGL((D == 64 ? kv8_join_kernel<64, 1> : kv8_join_kernel<128, 1>), dim3((unsigned)((queries + 3) / 4)),
-                           dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL((D == 64 ? kv8_join_kernel<64, 4> : kv8_join_kernel<128, 4>), dim3((unsigned)queries), dim3(256),
-                           0, stream, a);
-    return hipGetLastError();
+        return launch_kernel(D == 64 ? kv8_join_kernel<64, 1> : kv8_join_kernel<128, 1>, dim3((unsigned)((queries + 3) / 4)), 256,
+                             stream, a);
+    return launch_kernel(D == 64 ? kv8_join_kernel<64, 4> : kv8_join_kernel<128, 4>, dim3((unsigned)queries), 256, stream, a);
 }
 
 }  // namespace svdq

@@ -110,9 +110,8 @@ hipError_t launch_rope(const uint16_t *X, int64_t x_stride, const int32_t *posit
     a.R = 2 * pairs;
     const int pieces = H * (a.R / (interleaved ? 8 : 16) + (D - a.R) / 8);
     a.tokens = std::max(1, std::min({kRopePieces / pieces, kRopeAngles / pairs, T / kRopeBlocks}));
-    hipLaunchKernelGGL(interleaved ? rope_kernel<true> : rope_kernel<false>, dim3((unsigned)((T + a.tokens - 1) / a.tokens)),
-                       dim3(kRopeThreads), 0, stream, a);
-    return hipGetLastError();
+    return launch_kernel(interleaved ? rope_kernel<true> : rope_kernel<false>, dim3((unsigned)((T + a.tokens - 1) / a.tokens)),
+                         kRopeThreads, stream, a);
 }
 
 }  // namespace svdq
