@@ -65,10 +65,11 @@ svdq_status current_device_ok() {
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
+// The status of a launch. An error that it left with the runtime is taken from there:
+// the next to ask would have it for its own.
 svdq_status launched(hipError_t e) {
-    if (e != hipSuccess) return SVDQ_ERR_HIP;
-    e = hipGetLastError();
-    return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+    const hipError_t left = hipGetLastError();
+    return e == hipSuccess && left == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
 }
 
 // Buffer loads address each operand with 32-bit offsets.
