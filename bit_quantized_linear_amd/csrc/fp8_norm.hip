@@ -65,9 +65,24 @@ __device__ __forceinline__ void norm_input(const NormArgs &a, size_t at, float (
     }
 }
 
+// What a token's h is multiplied with, 1 / sqrt(mean + eps), as the product of a power
+// of two and an ordinary number: for tokens near the smallest or the largest bf16
+// numbers (2^-133, subnormal; 2^128) it is itself past the largest fp32 number, or
+// subnormal with fewer bits. h times the first factor is exact, as far as the norm shows
+// it: it is 1 for all other tokens.
+struct NormFactor {
+    float power, rest;
+};
+
+__device__ __forceinline__ NormFactor norm_factor(double mean, float eps) {
+    const double r = 1.0 / sqrt(mean + (double)eps);
+    const float power = r > 0x1p100 ? 0x1p64f : r < 0x1p-100 ? 0x1p-64f : 1.0f;
+    return {power, (float)(r / (double)power)};
+}
+
 // Outputs of 8 features of token m from feature k on; the 16 lanes of a group of
 // 128 features call it together, h is 0 past K.
-__device__ __forceinline__ void norm_output(const NormArgs &a, int m, int k, float (&h)[8], float rs) {
+__device__ __forceinline__ void norm_output(const NormArgs &a, int m, int k, float (&h)[8], NormFactor f) {
     const size_t at = (size_t)m * a.K + k;
     const bool in = k < a.K;
     if (in && a.sum) *reinterpret_cast<u32x4 *>(a.sum + at) = narrow8(h);
@@ -76,7 +91,7 @@ __device__ __forceinline__ void norm_output(const NormArgs &a, int m, int k, flo
         float w[8];
         widen8(*reinterpret_cast<const u32x4 *>(a.w + k), w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = h[i] * rs * w[i];
+        for (int i = 0; i < 8; ++i) y[i] = h[i] * f.power * f.rest * w[i];
         if (a.Y) *reinterpret_cast<u32x4 *>(a.Y + at) = narrow8(y);
     }
     if (!a.qx) return;
@@ -137,16 +152,16 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void fp8_norm_kernel(NormArgs 
 #pragma unroll
         for (int w = 0; w < TR / 64; ++w) ss += part[w];
     }
-    const float rs = (float)(1.0 / sqrt(ss / a.K + (double)a.eps));
+    const NormFactor f = norm_factor(ss / a.K, a.eps);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int k = (c * TR + t) * 8;
-        if (k - (t & 15) * 8 < a.K) norm_output(a, m, k, h[c], rs);
+        if (k - (t & 15) * 8 < a.K) norm_output(a, m, k, h[c], f);
     }
     for (int k = (C * TR + t) * 8; k - (t & 15) * 8 < a.K; k += TR * 8) {
         float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (k < a.K) norm_input(a, row + k, g);
-        norm_output(a, m, k, g, rs);
+        norm_output(a, m, k, g, f);
     }
 }
 

@@ -578,7 +578,7 @@ svdq_status svdq_fp8_moe_layer(const uint16_t *X, const uint16_t *wr, const uint
  *   qx = E4M3(fp32(y * fp32(448 / A))), round to nearest even.
  *   The squares are summed in fp64; y goes to the codes without a rounding to
  *   bf16. A token with a value that is not finite has NaN or 0 for its outputs'
- *   values, other tokens are not affected.
+ *   values, as has one of zeros where eps is 0; other tokens are not affected.
  * In:  X [M, K] bf16; residual [M, K] bf16 or NULL; w [K] bf16; eps >= 0.
  * Out: sum [M, K] bf16: h rounded once, the next residual (NULL if not wanted;
  *      may be residual or X itself); Y [M, K] bf16: y rounded once, for layers
