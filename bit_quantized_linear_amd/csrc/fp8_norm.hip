@@ -76,8 +76,11 @@ struct NormFactor {
 
 __device__ __forceinline__ NormFactor norm_factor(double mean, float eps) {
     const double r = 1.0 / sqrt(mean + (double)eps);
-    const float power = r > 0x1p100 ? 0x1p64f : r < 0x1p-100 ? 0x1p-64f : 1.0f;
-    return {power, (float)(r / (double)power)};
+    if (__builtin_expect(r > 0x1p100 || r < 0x1p-100, 0)) {
+        const float power = r > 1.0 ? 0x1p64f : 0x1p-64f;
+        return {power, (float)(r * (r > 1.0 ? 0x1p-64 : 0x1p64))};
+    }
+    return {1.0f, (float)r};
 }
 
 // Outputs of 8 features of token m from feature k on; the 16 lanes of a group of
