@@ -432,7 +432,16 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
             for (int w = 1; w < W; ++w) acc[e] += o_s[w][lane * E + e];
         }
     }
-    if (row < first || row >= last) return;
+    // A row from the first start up to the last one is some sequence's. Others mostly are
+    // none's; but starts may fall, behind the last sequence for instance, and then all say
+    if (row < first || row >= last) {
+        bool found = false;
+        for (int b = lane; b < a.kv.B; b += 64) {
+            const KvSeq s = kv_seq(a.kv, b);
+            found |= row >= s.row0 && row < s.row0 + s.rows;
+        }
+        if (!__any(found)) return;
+    }
     const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t *out = a.O + at * D + lane * E;
     if constexpr (E == 2)

@@ -620,7 +620,8 @@ svdq_status svdq_rope(const uint16_t *X, int64_t x_stride, const int32_t *positi
  *   elsewhere) serve as well.
  * A batch of B sequences in a call:
  *   starts [B + 1] int32: rows starts[b] .. starts[b + 1] - 1 of the call's T
- *      rows are the newest tokens of sequence b, in order;
+ *      rows are the newest tokens of sequence b, in order (none where
+ *      starts[b + 1] is not above starts[b]; no row is two sequences');
  *   lengths [B] int32: tokens of sequence b, the new ones among them;
  *   table [B, max_pages] int32: token t of sequence b is token t % 64 of page
  *      table[b, t / 64].
