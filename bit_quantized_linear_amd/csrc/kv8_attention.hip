@@ -36,6 +36,14 @@ namespace {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLeastFactor = 0x1p-126f;  // of scores: a page's key scale may be 0, a hidden score -infinity
 
+// The factor of a page's scores, or -1 where its key scale is no number (or the product
+// overflows): the scores of its tokens are NaN then, for those who see them, and 1 serves.
+// NaN as a factor would reach the others through the scores that a mask has made -infinity.
+__device__ __forceinline__ float score_factor(float ks, float scale) {
+    const float f = ks * scale;
+    return f < INFINITY ? fmaxf(f, kLeastFactor) : -1.0f;
+}
+
 struct AttnArgs {
     KvBatch kv;
     const uint16_t *Q;
@@ -178,7 +186,7 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
         const int p = p0 + wp + kStride * (from + lane);
         number = p < p1 ? kv_page(a.kv, b, p) : -1;
         const int64_t unit = (int64_t)max(number, 0) * a.Hk + head;
-        factor = fmaxf(a.ks[unit] * a.scale, kLeastFactor);
+        factor = score_factor(a.ks[unit], a.scale);
         vs = number >= 0 ? a.vs[unit] : 0.0f;
     };
     u32x4 k[4][KC], v[DT];
@@ -210,13 +218,15 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
     for (int i = 0; i < count; ++i) {
         const int p = p0 + wp + kStride * i;
         const bool there = __builtin_amdgcn_readlane(number, i - first) >= 0, more = i + 1 < count;
-        const float c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(factor), i - first));
+        const int c_bits = __builtin_amdgcn_readlane(__float_as_int(factor), i - first);
+        const bool lost = c_bits < 0;
+        const float c = __int_as_float(c_bits & 0x7FFFFFFF);
         const float vscale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), i - first));
         const int t0 = p * kKvPage;
         // a page that some query does not see whole: hidden tokens' weights are
         // 0, and their values are not multiplied, as they may be NaN. Of a page
-        // that is not there, all are hidden
-        const bool cut = !there || t0 < low1 || t0 + kKvPage > high0;
+        // that is not there, all are hidden. Scores that are NaN take this path as well
+        const bool cut = !there || lost || t0 < low1 || t0 + kKvPage > high0;
         uint32_t nan = 0;
         bf16x8 w[QT][2];
 #pragma unroll
@@ -261,7 +271,7 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t see = byte_mask(t0 + 16 * g4 + 4 * j, low[t], there ? high[t] : 0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[j][e] = see >> (8 * e) & 1 ? s[j][e] : -INFINITY;
+                    for (int e = 0; e < 4; ++e) s[j][e] = see >> (8 * e) & 1 ? (lost ? NAN : s[j][e]) : -INFINITY;
                 }
             }
             float top = s[0][0];
@@ -536,6 +546,7 @@ __device__ __forceinline__ bool find_longest(const AttnArgs &a, int item, int ti
     return true;
 }
 
+constexpr uint32_t kNanCodes = 0x7F7F7F7Fu;
 constexpr int kPreInfo = 512;  // pages whose numbers and scales are in LDS at a time
 
 // A block takes 32 queries a wave and walks the pages that they see, or its part of
@@ -626,9 +637,9 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
     for (int i = 0; i < DT; ++i) zero(o[i]);
 
     // ---- pages to LDS ----
-    // info_s: page number (-1: not there), the factor of its scores, its value scale,
-    // and whether it is plain: there, seen whole by every query, its value scale a
-    // power of two. Plain pages are what the pipelined steps take
+    // info_s: page number (-1: not there), the factor of its scores (-1: they are NaN), its
+    // value scale, and whether it is plain: there, seen whole by every query, its scores
+    // numbers, its value scale a power of two. Plain pages are what the pipelined steps take
     int info0 = 0;  // the page of info_s[0]
     auto load_info = [&](int from, int to) __attribute__((always_inline)) {
         info0 = from;
@@ -638,9 +649,10 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
             if (page >= 0) {
                 const int64_t unit = (int64_t)page * a.Hk + head;
                 const float ks = a.ks[unit], vs = a.vs[unit];
-                x[1] = __float_as_uint(fmaxf(ks * a.scale, kLeastFactor));
+                const float factor = score_factor(ks, a.scale);
+                x[1] = __float_as_uint(factor);
                 x[2] = __float_as_uint(vs);
-                x[3] = p >= f0 && p < f1 && power_of_two(vs);
+                x[3] = p >= f0 && p < f1 && factor > 0.0f && power_of_two(vs);
             }
             info_s[i] = x;
         }
@@ -667,6 +679,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
             }
         }
     };
+    auto held_factor = [&]() __attribute__((always_inline)) { return fabsf(__uint_as_float(held[1])); };
     auto held_plain = [&]() __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane((int)held[3]) != 0; };
     // matrix-core row i of a tile of 32 keys is token 16 (i / 16) + 8 (i / 4 % 2) + 4 (i / 8 % 2) + i % 4, so that
     // element e of a lane's scores is token 16 (e / 8) + 8 h + e % 8: keys lie in LDS in that order
@@ -682,6 +695,10 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
         if (!there) {
 #pragma unroll
             for (int i = 0; i < PC; ++i) kr[i] = vr[i] = u32x2{0u, 0u};
+        }
+        if ((int)held[1] < 0) {
+#pragma unroll
+            for (int i = 0; i < PC; ++i) kr[i] = u32x2{kNanCodes, kNanCodes};
         }
         if (p < f0 || p >= f1) {
             uint32_t nan = 0;
@@ -910,7 +927,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
         const auto after = [&](int v) { return v == 2 ? 0 : v + 1; };
         const auto info_at = [&](int p) { return min(p, s1 - 1) - info0; };
         fetch(info_s[0]);
-        float c = __uint_as_float(held[1]);
+        float c = held_factor();
         bool plain = held_plain();
         store(s0, kc, vc);
         fetch(info_s[info_at(s0 + 1)]);
@@ -932,7 +949,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
                 for (int i = 0; i < kAhead; ++i) operand[i] = key(kc, 1, i);
                 int vw = vc;  // the values of w1 (at first zeros: any page that all see)
                 do {
-                    const float cn = __uint_as_float(held[1]);
+                    const float cn = held_factor();
                     const int vn = after(vc);
                     raise(top0 * c, w1);
                     step(std::true_type(), kc ^ 1, vn, info_at(p + 2), t0, c, w0, kc, 1, t1, top1, vw, 1, w1, kc ^ 1, 0);
@@ -949,7 +966,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
 #pragma unroll
                     for (int i = 0; i < DT; ++i) o[i] = mfma_bf16_32x32x16(value(vw, 1, u, i), w1[u], o[i]);
             }
-            const float cn = __uint_as_float(held[1]);
+            const float cn = held_factor();
             const int vn = after(vc);
             plain = held_plain();
             if (p + 1 < s1) {
