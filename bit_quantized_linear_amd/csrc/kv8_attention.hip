@@ -36,6 +36,9 @@ namespace {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLeastFactor = 0x1p-126f;  // of scores: a page's key scale may be 0, a hidden score -infinity
 
+constexpr uint32_t kNanCodes = 0x7F7F7F7Fu;  // those of a page whose scale is no number
+constexpr int kInfinityBits = 0x7F800000;    // all set in infinities and NaN
+
 // The factor of a page's scores, or -1 where its key scale is no number (or the product
 // overflows): the scores of its tokens are NaN then, for those who see them, and 1 serves.
 // NaN as a factor would reach the others through the scores that a mask has made -infinity.
@@ -221,12 +224,14 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
         const int c_bits = __builtin_amdgcn_readlane(__float_as_int(factor), i - first);
         const bool lost = c_bits < 0;
         const float c = __int_as_float(c_bits & 0x7FFFFFFF);
-        const float vscale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), i - first));
+        const int v_bits = __builtin_amdgcn_readlane(__float_as_int(vs), i - first);
+        const bool lost_values = (v_bits & kInfinityBits) == kInfinityBits;
+        const float vscale = lost_values ? 1.0f : __int_as_float(v_bits);
         const int t0 = p * kKvPage;
         // a page that some query does not see whole: hidden tokens' weights are
         // 0, and their values are not multiplied, as they may be NaN. Of a page
-        // that is not there, all are hidden. Scores that are NaN take this path as well
-        const bool cut = !there || lost || t0 < low1 || t0 + kKvPage > high0;
+        // that is not there, all are hidden. Scores or values that are NaN take this path as well
+        const bool cut = !there || lost || lost_values || t0 < low1 || t0 + kKvPage > high0;
         uint32_t nan = 0;
         bf16x8 w[QT][2];
 #pragma unroll
@@ -262,6 +267,7 @@ __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs 
                         const uint32_t mask = byte_mask(t0 + 16 * g4 + 4 * j, low0, there ? high1 : 0);
 #pragma unroll
                         for (int n = 0; n < DT; ++n) {
+                            if (lost_values) v[n][j] = kNanCodes;
                             v[n][j] &= mask;
                             nan |= nan_codes(v[n][j]);
                         }
@@ -546,7 +552,6 @@ __device__ __forceinline__ bool find_longest(const AttnArgs &a, int item, int ti
     return true;
 }
 
-constexpr uint32_t kNanCodes = 0x7F7F7F7Fu;
 constexpr int kPreInfo = 512;  // pages whose numbers and scales are in LDS at a time
 
 // A block takes 32 queries a wave and walks the pages that they see, or its part of
@@ -691,7 +696,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
     // one of the others is NaN
     auto store = [&](int p, int ki, int vi) __attribute__((always_inline)) {
         const bool there = (int)held[0] >= 0;
-        const float vs = __uint_as_float(held[2]);
+        float vs = __uint_as_float(held[2]);
         if (!there) {
 #pragma unroll
             for (int i = 0; i < PC; ++i) kr[i] = vr[i] = u32x2{0u, 0u};
@@ -699,6 +704,11 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
         if ((int)held[1] < 0) {
 #pragma unroll
             for (int i = 0; i < PC; ++i) kr[i] = u32x2{kNanCodes, kNanCodes};
+        }
+        if (!(fabsf(vs) < INFINITY)) {  // codes, as a mask clears those
+            vs = 1.0f;
+#pragma unroll
+            for (int i = 0; i < PC; ++i) vr[i] = u32x2{kNanCodes, kNanCodes};
         }
         if (p < f0 || p >= f1) {
             uint32_t nan = 0;

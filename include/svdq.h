@@ -617,7 +617,7 @@ svdq_status svdq_rope(const uint16_t *X, int64_t x_stride, const int32_t *positi
  *   vc [num_pages, Hk, D, 64] E4M3 bytes (values, a feature's 64 tokens
  *   together), vs [num_pages, Hk] fp32; value = code * the page's scale. Scales
  *   are not negative; svdq_kv8_append writes powers of two, others (a cache filled
- *   elsewhere) serve as well. A page's key scale that is not finite stands for NaN.
+ *   elsewhere) serve as well. A scale that is not finite stands for NaN.
  * A batch of B sequences in a call:
  *   starts [B + 1] int32: rows starts[b] .. starts[b + 1] - 1 of the call's T
  *      rows are the newest tokens of sequence b, in order (none where

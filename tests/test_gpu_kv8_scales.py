@@ -2,7 +2,8 @@
 (needs an MI355X).
 
 A page whose key scale is not finite has NaN for its scores: the queries that see one of
-its tokens have NaN for output and logarithm. Queries that see none of its tokens, and
+its tokens have NaN for output and logarithm. One whose value scale is not finite has NaN
+for its values: NaN outputs, the same logarithms. Queries that see none of its tokens, and
 other heads, are not touched. Tolerances as in tests/test_gpu_kv8.py.
 """
 
@@ -13,7 +14,7 @@ from tests.test_gpu_norm_rope import _gpu  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
-SPOILED = ["ks"]
+SPOILED = ["ks", "vs"]
 
 
 def spoil(x, what, value, page, head=0):
@@ -62,3 +63,11 @@ def test_a_scale_that_is_not_finite_and_seen_by_all(case, what):
     group = x.Hq // x.Hk
     assert O[: x.new[0], group: 2 * group].isnan().all() and not O[x.new[0]:].isnan().any()
     x.check(O, L, causal=False)
+
+
+@pytest.mark.parametrize("case", KERNELS, ids=kernel_id)
+def test_a_scale_of_no_power_of_two_beside_one_that_is_not_finite(case):
+    x = batch(5, case, 128, scales="any")
+    spoil(x, "vs", NAN, len(x.pages[0]) - 1)
+    O, L = x.attend()
+    x.check(O, L, values_rounded=case[0] > 64)
