@@ -34,7 +34,9 @@ namespace svdq {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kLeastFactor = 0x1p-126f;  // of scores: a page's key scale may be 0, a hidden score -infinity
+// Of scores: a page's key scale may be 0, a hidden score -infinity. The least number there
+// is: large queries and a small scale have factors below the smallest normal one
+constexpr float kLeastFactor = 0x1p-149f;
 
 constexpr uint32_t kNanCodes = 0x7F7F7F7Fu;  // those of a page whose scale is no number
 constexpr int kInfinityBits = 0x7F800000;    // all set in infinities and NaN

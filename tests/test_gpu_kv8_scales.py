@@ -1,5 +1,5 @@
-"""Page scales of the 8-bit cache that are not finite, in every kernel of the attention
-(needs an MI355X).
+"""Page scales of the 8-bit cache that are not finite, and factors of scores (scale times
+a page's key scale) far below 1, in every kernel of the attention (needs an MI355X).
 
 A page whose key scale is not finite has NaN for its scores: the queries that see one of
 its tokens have NaN for output and logarithm. One whose value scale is not finite has NaN
@@ -71,3 +71,18 @@ def test_a_scale_of_no_power_of_two_beside_one_that_is_not_finite(case):
     spoil(x, "vs", NAN, len(x.pages[0]) - 1)
     O, L = x.attend()
     x.check(O, L, values_rounded=case[0] > 64)
+
+
+@pytest.mark.parametrize("case", KERNELS, ids=kernel_id)
+def test_factors_below_the_smallest_normal_number(case):
+    """Queries near 2^112, scale 2^-112, key scales of 2^-20 to 2^-14: scores are ordinary,
+    their factors lie on both sides of 2^-126."""
+    x = batch(6, case, 64, spread=2.0 ** 112)
+    x.scale = 2.0 ** -112
+    x.ks.copy_(x.t.exp2(x.t.randint(-20, -13, x.ks.shape, generator=x.gen, device="cuda").float()))
+    assert x.t.isfinite(x.q).all()
+    O, L = x.attend()
+    x.check(O, L)
+    x.ks.mul_(2.0 ** -10)  # no score matters any more: the values' mean
+    O, L = x.attend()
+    x.check(O, L)
