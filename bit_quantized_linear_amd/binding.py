@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+import sys
 
 import numpy as np
 
@@ -649,11 +650,16 @@ _quick_calls = None
 _ANY_KIND = 2 ** 64 - 1
 
 
+def built_for(torch):
+    """The Python and torch whose structures `_tensors` reads."""
+    return f"{sys.implementation.cache_tag}, torch {torch.__version__} {torch.version.git_version}"
+
+
 def _quick():
     """pointers and heads of `_tensors`, which look at all tensors of a call at once,
     and its names for E4M3 codes, bf16, fp32, int32 and fp64 numbers; empty where it
-    was not built for this torch. What they refuse is looked at again below, for the
-    error that fits."""
+    was not built, or not for this Python and torch. What they refuse is looked at
+    again below, for the error that fits."""
     global _quick_calls
     if _quick_calls is None:
         _quick_calls = ()
@@ -662,7 +668,8 @@ def _quick():
 
             from . import _tensors as m
 
-            _quick_calls = (m.pointers, m.heads, *(m.kind(*f) for f in (*_fp8_formats(), (t.float64,))))
+            if getattr(m, "built_for", None) == built_for(t):
+                _quick_calls = (m.pointers, m.heads, *(m.kind(*f) for f in (*_fp8_formats(), (t.float64,))))
         except ImportError:
             pass
     return _quick_calls

@@ -6,14 +6,16 @@ HIP sources are compiled by hipcc for gfx950 only; host C++ sources by the
 ROCm clang++. Objects go to ``_build/`` beside this file and the shared
 library to ``libsvdq.so`` in this package directory. The GELU table of the
 fused MLP epilogue is generated first (``gelu_table.py`` ->
-``_build/gelu_table.h``). Beside the library, ``_tensors.so``: a small module
-for this Python and torch, which the binding does without where it is missing.
+``_build/gelu_table.h``). Beside the library, ``_tensors.<Python's tag>.so``: a
+small module for this Python and torch, which the binding does without where it
+is missing or was built for others.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -31,7 +33,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsvdq.so")
-TENSORS = os.path.join(PKG, "_tensors.so")
+TENSORS = os.path.join(PKG, "_tensors" + importlib.machinery.EXTENSION_SUFFIXES[0])
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
@@ -57,22 +59,30 @@ def _run(cmd):
     return p.stdout
 
 
+def _remove_tensors():
+    """An earlier build's module may be another Python's or torch's."""
+    for path in glob.glob(os.path.join(glob.escape(PKG), "_tensors*.so")):
+        os.remove(path)
+
+
 def _tensors_job():
-    """How _tensors.so is built, or None without torch."""
+    """How the module for tensors is built, or None without torch."""
     try:
         import torch
+        from bit_quantized_linear_amd.binding import built_for
         from torch.utils.cpp_extension import include_paths
     except ImportError:
         return None
     include = [x for path in [*include_paths(), sysconfig.get_paths()["include"]] for x in ("-isystem", path)]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     return [CLANGXX, "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden", "-Wall", *include,
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "python", "tensors.cpp"),
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{built_for(torch)}"', os.path.join(CSRC, "python", "tensors.cpp"),
             "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", TENSORS + ".tmp"]
 
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    _remove_tensors()
     gelu_table.write(os.path.join(BUILD, "gelu_table.h"))
     jobs = []
     for src in sorted(glob.glob(os.path.join(CSRC, "*.hip"))):
@@ -92,8 +102,6 @@ def build(verbose: bool = False) -> str:
                 outs.append(module.result())
                 shutil.move(tensors[-1], TENSORS)
             except RuntimeError as e:
-                if os.path.exists(TENSORS):
-                    os.remove(TENSORS)
                 print(f"{TENSORS} is left out: {e}", file=sys.stderr)
     if verbose:
         for o in outs:
