@@ -27,3 +27,16 @@ def test_the_batches_reach_the_kernels_that_they_name():
     for rows, parts, *sizes in KERNELS:
         plan = d.of(*sizes)
         assert plan.rows == rows and (plan.splits > 1) == parts, (sizes, plan)
+
+
+def test_the_cases_of_long_prompts_reach_blocks_of_256():
+    pytest.importorskip("torch")
+    from tests import test_gpu_kv8_blocks as blocks
+
+    plans = [d.of(*case) for case in blocks.EVERY]
+    assert all(p.rows == 256 for p in plans)
+    assert {(p.splits > 1, p.sorted) for p in plans} == {(False, True), (False, False), (True, False)}
+    assert len(blocks.MANY[0]) > 64 and max(blocks.LONG[0]) > 512 * 64
+    cuts = [d.attention(T, 2, width, Hq, Hk) for T, Hq, Hk, width in blocks.NONSENSE]
+    assert [(p.rows, p.splits > 1) for p in cuts] == [(256, False), (128, True), (128, True), (128, False), (16, True), (64, True)]
+    assert cuts[0].sorted
