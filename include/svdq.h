@@ -640,7 +640,7 @@ svdq_status svdq_rope(const uint16_t *X, int64_t x_stride, const int32_t *positi
  *   sequence; code = E4M3(fp32(x * fp32(1 / s))), and the earlier tokens' codes
  *   become E4M3(fp32(code * fp32(old scale / s))), both round to nearest even.
  * Values that are not finite become the NaN code and do not count for A. What a
- * page holds behind the sequence's last token is neither read nor written.
+ * page holds behind the sequence's last token stays as it is and counts for nothing.
  * In:  K, V bf16, head h of row t at K + t k_stride + h D (strides in elements).
  * In/out: kc, ks, vc, vs. A page that a call writes belongs to one sequence of
  *      the batch, once (a page shared as a prefix is copied before it is written).
@@ -672,6 +672,8 @@ size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, i
  * Scores, weights' sums and outputs are fp32 sums of products of bf16 numbers
  * (the codes' values, exact; weights rounded to bf16, and values times a scale
  * that is no power of two); one rounding to bf16.
+ * The outputs' sums are numbers while 64 times the tokens that a query sees times
+ * their largest value is below 2^128.
  * In:  Q bf16, head h of row t at Q + t q_stride + h D (stride in elements);
  *      0 < scale <= 2^126.
  * Out: O [T, Hq, D] bf16; lse [T, Hq] fp32 or NULL: the natural logarithm of the

@@ -7,9 +7,15 @@ for its values: NaN outputs, the same logarithms. Queries that see none of its t
 other heads, are not touched. Tolerances as in tests/test_gpu_kv8.py.
 """
 
+import numpy as np
 import pytest
 
+from bit_quantized_linear_amd import binding as b
+from oracle import decoder as od
+from oracle.fp8 import e4m3_decode
+from tests import gpu_harness as H
 from tests.kv8_batch import KERNELS, PAGE, batch, kernel_id
+from tests.test_gpu_kv8 import bf16_dev, bf16_values, random_cache, upload
 from tests.test_gpu_norm_rope import _gpu  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +92,51 @@ def test_factors_below_the_smallest_normal_number(case):
     x.ks.mul_(2.0 ** -10)  # no score matters any more: the values' mean
     O, L = x.attend()
     x.check(O, L)
+
+
+@pytest.mark.parametrize("power", [-110, 90])
+@pytest.mark.parametrize("case", KERNELS, ids=kernel_id)
+def test_values_near_the_ends_of_the_range(case, power):
+    """Values near 2^-108 (weights times their scale are subnormal) and near 2^92, whose
+    sums are numbers: 64 times 6018 tokens leave 2^18."""
+    for spread in (0.2, 3.0):
+        x = batch(7, case, 64, spread=spread)
+        x.vs.mul_(2.0 ** power)
+        O, L = x.attend()
+        assert x.t.isfinite(O).all() and (O != 0).any()
+        x.check(O, L)
+
+
+@pytest.mark.parametrize("old", [0.0, 0.0131, 2.0 ** -20, 2.0 ** 20, INF, NAN])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_behind_tokens_of_another_programs_scale(old, D):
+    """s = max(need, old), codes E4M3(fp32(x fp32(1 / s))), earlier ones E4M3(fp32(code
+    fp32(old / s))), byte for byte; where the scale is no number, the earlier tokens are
+    NaN, by their codes or by the scale that stays."""
+    t = H.torch()
+    rng = np.random.default_rng(D)
+    Hk, length, new, low = 2, 45, 7, 38
+    cache = random_cache(rng, 3, Hk, D)
+    cache.ks[1], cache.vs[1] = old, old
+    rows = bf16_values(rng, (new, 2 * Hk, D), 3.0)
+    dev, tensors = bf16_dev(rows), upload(cache)
+    whole = lambda v: t.tensor(v, dtype=t.int32, device="cuda")  # noqa: E731
+    b.svdq_kv8_append(dev[:, :Hk], dev[:, Hk:], whole([0, new]), whole([length]), whole([[1]]), *tensors)
+    kc, ks, vc, vs = (H.host(x) for x in tensors)
+    f32 = np.float32
+    for codes, scales, was, x in ((kc, ks, cache.kc, rows[:, :Hk]), (vc.transpose(0, 1, 3, 2), vs, cache.vc.transpose(0, 1, 3, 2),
+                                                                  rows[:, Hk:])):
+        assert np.array_equal(codes[[0, 2]], was[[0, 2]]) and np.array_equal(codes[1, :, length:], was[1, :, length:])
+        for h in range(Hk):
+            need = od.page_scale(np.abs(x[:, h].astype(np.float64)).max())
+            s = f32(need if np.isnan(old) else max(need, old))
+            assert scales[1, h] == s
+            with np.errstate(invalid="ignore"):
+                fresh, ratio = od.encode(x[:, h].astype(f32) * (f32(1) / s)), f32(old) / s
+                kept = was[1, h, :low] if s == f32(old) else od.encode(e4m3_decode(was[1, h, :low]).astype(f32) * ratio)
+            for got, want in ((codes[1, h, low:length], fresh), (codes[1, h, :low], kept)):
+                got, want = (np.where((c & 0x7F) == 0, 0, np.where((c & 0x7F) == 0x7F, 0x7F, c)) for c in (got, want))
+                assert np.array_equal(got, want)  # the signs of 0 and NaN are open
+    if not np.isfinite(old):
+        earlier = e4m3_decode(kc[1, :, :low]) * ks[1][:, None, None]
+        assert not np.isfinite(ks[1]).all() or np.isnan(earlier).all()

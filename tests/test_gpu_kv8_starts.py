@@ -4,6 +4,7 @@ above its own has no new tokens, and the others keep theirs, however a call is c
 
 import pytest
 
+from bit_quantized_linear_amd import binding as b
 from tests import gpu_harness as H
 from tests.kv8_batch import Batch64
 from tests.test_gpu_norm_rope import _gpu  # noqa: F401
@@ -59,3 +60,19 @@ def test_rows_of_no_sequence_between_starts_that_fall(parts):
     y.call(O, L, ws)
     assert (O[2:5] == 7.0).all() and (L[2:5] == 7.0).all()
     x.check(t.cat([O[5:7], O[0:2]]), t.cat([L[5:7], L[0:2]]))
+
+
+@pytest.mark.parametrize("fill", [0, -1, 1])
+def test_append_of_a_batch_whose_last_starts_fall(fill):
+    t = H.torch()
+    for D in (64, 128):
+        x = Batch64(D, [130, 200], [70, 3], 2, 2, D)
+        k, v = (t.randn((x.T, 2, D), generator=x.gen, device="cuda").bfloat16() for _ in range(2))
+        whole = lambda v: t.tensor(v, dtype=t.int32, device="cuda")  # noqa: E731
+        caches = [[c.clone() for c in (x.kc, x.ks, x.vc, x.vs)] for _ in range(2)]
+        b.svdq_kv8_append(k, v, x.starts, x.dev_lengths, x.table, *caches[0])
+        b.svdq_kv8_append(k, v, t.cat([x.starts, whole([fill] * 3)]), t.cat([x.dev_lengths, whole([0, 70, 64])]),
+                          t.cat([x.table, x.table.new_full((3, x.table.shape[1]), 1)]), *caches[1])
+        for a, c in zip(*caches):
+            assert t.equal(a.view(t.uint8), c.view(t.uint8))
+        assert not t.equal(caches[0][0], x.kc)
