@@ -7,8 +7,8 @@
 //   sx[g, m] = fp32(A / 448),  qx = E4M3(fp32(y fp32(448 / A)))
 //
 // y is not rounded to bf16 on its way to the codes. The sum of squares is kept in
-// fp64: it neither overflows nor underflows for any bf16 input, and its order
-// does not show in the result.
+// fp64: it neither overflows nor underflows for any bf16 input, and what its order
+// changes is far below fp32's rounding.
 
 #include <hip/hip_runtime.h>
 
@@ -115,8 +115,8 @@ __device__ __forceinline__ void norm_output(const NormArgs &a, int m, int k, flo
 }
 
 // HBM-bound: 2 bytes in, 2 of the residual, 2 of the sum out and 1 of a code per
-// feature, each once; 32760 x 5120 takes 213 us, 5.5 TB/s (a large copy: 5.15), 8 x
-// 4096 3.7 us (3.0 in a graph), of which an empty launch is 2 to 3.
+// feature, each once; 32760 x 5120 takes 214 us, 5.5 TB/s (a large copy: 5.15), 8 x
+// 4096 3.6 us (3.4 among others in a graph), of which an empty launch is 2 to 3.
 // TR threads a token, C pieces of 8 features per thread in registers; the rest of a
 // longer row is read again for the second pass (each thread reads what it has read
 // before and writes there afterwards, so that the sum may replace the residual).

@@ -75,8 +75,10 @@ __device__ __forceinline__ uint32_t top_finite(u32x4 v) {
 // of 4 tokens as a page holds them. The tokens are under way while the page's
 // number, then its scale and the codes that share a piece with new ones are.
 // HBM-bound: 4 bytes in and 2 out per token, head and feature. 4680 tokens of 40 heads of
-// 128: 28.4 us, 5.1 TB/s (a large copy: 5.15); one token each of 16 sequences 6.4 us,
-// four memory latencies in turn (sequence, page, scale and shared codes, codes).
+// 128: 35 us, 4.1 TB/s from memory (a large copy: 5.15; 27 to 30 us where the 96 MB of keys
+// and values are in the last-level cache), as a block is three memory latencies in turn;
+// one token each of 16 sequences 6.4 us, four of them (sequence, page, scale and shared
+// codes, codes).
 __global__ __launch_bounds__(kAppThreads) void kv8_append_kernel(AppendArgs a) {
     __shared__ uint32_t tops[kAppThreads / 64];
     const int head = blockIdx.y >> 1;

@@ -119,10 +119,10 @@ constexpr int kMostSequences = 65535;  // of a call, and of a grid's last dimens
 // LDS. The waves' sums are joined in LDS and, where a sequence's pages are split over
 // blocks, by a second kernel.
 // HBM-bound: 2 D bytes a token and key head, read once. 32 sequences of up to 8191
-// tokens, 8 heads of 128: 60.6 us, 5.2 TB/s (a large copy: 5.15); one token after
-// 32759 in 32 parts: 14.6 us, 4.6 TB/s, of which a block's start (its sequence, page
+// tokens, 8 heads of 128: 61 us, 5.2 TB/s (a large copy: 5.15); one token after
+// 32759 in 32 parts: 14.7 us, 4.6 TB/s, of which a block's start (its sequence, page
 // numbers, first keys, each waiting for the last) is 3 to 4. With 64 queries a head
-// 108 us: 2 waves a SIMD work out weights as long as they wait for keys.
+// 130 us: 2 waves a SIMD work out weights as long as they wait for keys.
 template <int D, int QT, int WR>
 __global__ __launch_bounds__(64 * kDecWaves, 2) void kv8_decode_kernel(AttnArgs a) {
     constexpr int KC = D / 64;  // 64-byte pieces of a key
@@ -570,8 +570,10 @@ constexpr int kPreInfo = 512;  // pages whose numbers and scales are in LDS at a
 // 40 heads of 128: 2.74 ms, 1145 TFLOP/s (the library's bf16 product of 8192^3: 1210
 // to 1230). 8 waves of 32 queries, two a SIMD, as one wave's weights then overlap the
 // other's products: one wave of 64 a SIMD took 3.2 ms. Prompts of three sequences, up
-// to 2777 tokens after up to 1500: 240 us, 940 TFLOP/s; a block's start takes 6 to 7 us,
-// its outputs 2, and pages with masks are not pipelined.
+// to 2777 tokens after up to 1500: 236 to 240 us, 940 TFLOP/s; a block's start takes 6 to
+// 7 us, its outputs 2, and pages with masks are not pipelined. 8192 tokens over themselves,
+// 32 / 8 heads: 507 us, 1084 TFLOP/s, with a window of 1024 171 us, 753; heads of 64, whose
+// products have half the work for the same weights: 341 us, 807 TFLOP/s.
 // Waves a SIMD: two, where D = 64 in two blocks if they have 4 waves (100 queries after 1000
 // of 16 sequences of 16 heads: 32.4 us, 36.5 with one); with D = 128 4 waves need the
 // registers of one (with two, spilled: 49 against 39 us), and two blocks' LDS is not there.
@@ -1037,6 +1039,8 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 2 : NW / 4) void kv8_prompt_kern
 // in four; 32 of 8000, where the second launch is not worth it: 93 and 98); and one
 // up to 16 pages (500 tokens: 7.0 in one, 8.9 in two; 1000: 9.5 and 8.8, but a launch
 // less, 3.4 on the host).
+// Pages are the table's width, which the host knows, not the lengths, which it does not:
+// 32 sequences of 1000 tokens 15.4 us up to 128 pages wide, 39.7 with 1024, in 16 parts.
 // Prompts: what takes least by the time of a page in a block, of the second launch
 // and of a query's part on its way through memory (32 / 8 heads: 64 tokens after 32000
 // 57 us in 32 parts, 583 in one; after 8000 30, in all parts that there is room for 33,
@@ -1051,13 +1055,15 @@ constexpr float kPageTime = 1.3f, kJoinTime = 6.0f, kPartTime = 0.00026f;
 // head (`tiles`, prompts) and the parts of a sequence's pages.
 // Queries per block: the least of 16, 32, 64, 128 and 256 that the average sequence
 // fits, up to 64 in the kernel for few (32 sequences of up to 8192, 8 heads: 32
-// queries 78 us, 64 queries 108, 164 both with 128 to a block; 128 queries 170 with
+// queries 76 us, 64 queries 130, 164 both with 128 to a block; 128 queries 170 with
 // 128, 193 twice 64, 229 with 256; 100 queries after 8000 alone 22, 26 and 24; 64
 // sequences of 128 queries after 500 51, 47 and 59; of 256 queries 98 with 128, 72
 // with 256). But 128, not 256, where blocks of 256 would leave a quarter of the compute
 // units idle (32 / 8 heads: 256 tokens alone 17 us against 20, 1000 30.6 and 33.7,
 // 1400, 176 blocks of 256, 38 and 43, 2000, 256 blocks, 62 and 59; 64 after 8000 29 and
-// 33, after 32000, in 32 parts, 62 and 56).
+// 33, after 32000, in 32 parts, 62 and 56). Sequences far from the average pay for it: 31
+// decoded tokens after 4000 and a prompt of 2048 290 us, 218 in two calls, of 256 105 and
+// 83, of 64 59 and 69.
 struct AttnPlan {
     bool few, sorted;
     int rows, tiles, splits;

@@ -684,9 +684,10 @@ size_t svdq_kv8_attention_workspace_bytes(int T, int B, int max_pages, int Hq, i
  *      read before it is written; calls that may overlap in time need one each.
  * A call is cut by its averages: up to 64 queries of a key head per sequence
  * (T Hq / Hk <= 64 B) take a kernel made for few, more of them one made for many,
- * so long prompts and decoded tokens are best kept in calls of their own.
- * max_pages, too, decides how a sequence's pages are shared between blocks; a
- * table much wider than the lengths costs time, not results.
+ * so long prompts and decoded tokens are best kept in calls of their own (one call
+ * takes up to 1.5 times as long). max_pages, too, decides how a sequence's pages are
+ * shared between blocks; a table much wider than the lengths costs time (up to 2.6
+ * times, 1000 tokens in a table for 65000), not results.
  * Shapes: as svdq_kv8_append, with Hq % Hk == 0, T Hq < 2^30, Hq <= 65535,
  *      T Hq + 255 B Hk < 2^31, q_stride >= Hq D. Deterministic.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, MISALIGNED, UNSUPPORTED_DEVICE,
