@@ -76,8 +76,8 @@ def _tensors_job():
     include = [x for path in [*include_paths(), sysconfig.get_paths()["include"]] for x in ("-isystem", path)]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     return [CLANGXX, "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden", "-Wall", *include,
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{built_for(torch)}"', os.path.join(CSRC, "python", "tensors.cpp"),
-            "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", TENSORS + ".tmp"]
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{built_for(torch)}"',
+            os.path.join(CSRC, "python", "tensors.cpp"), "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", TENSORS + ".tmp"]
 
 
 def build(verbose: bool = False) -> str:

@@ -46,7 +46,7 @@ constexpr int kInfinityBits = 0x7F800000;    // all set in infinities and NaN
 // NaN as a factor would reach the others through the scores that a mask has made -infinity.
 __device__ __forceinline__ float score_factor(float ks, float scale) {
     const float f = ks * scale;
-    return f < INFINITY ? fmaxf(f, kLeastFactor) : -1.0f;
+    return fabsf(f) < INFINITY ? fmaxf(f, kLeastFactor) : -1.0f;
 }
 
 struct AttnArgs {

@@ -27,7 +27,7 @@ def spoil(x, what, value, page, head=0):
     getattr(x, what)[x.pages[0][page], head] = value
 
 
-@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
 @pytest.mark.parametrize("what", SPOILED)
 @pytest.mark.parametrize("case", KERNELS, ids=kernel_id)
 def test_a_scale_that_is_not_finite(case, what, value):
